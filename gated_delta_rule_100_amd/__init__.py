@@ -30,12 +30,19 @@ __all__ = [
     "gdr_state_fixup",
     "gdr_chunk_layout",
     "gdr_max_chunks",
+    "gdr_linear_decode",
+    "gdr_linear_prefill",
+    "gdr_linear_prefill_workspace_bytes",
+    "gdr_linear_backward",
+    "gdr_linear_backward_workspace_bytes",
     "gdr_status_string",
     "gdr_last_error",
 ]
 
 GDR_BF16 = 0
 GDR_FP32 = 1
+GDR_DECAY_TOKEN = 0
+GDR_DECAY_HEAD = 1
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libgdr.so")
@@ -77,6 +84,19 @@ def _load():
     lib.gdr_chunk_prefill_noalloc.restype = I
     lib.gdr_state_fixup.argtypes = [P, P, P, P, I, P, I, I, I, I, P]
     lib.gdr_state_fixup.restype = I
+    L, F = ctypes.c_int64, ctypes.c_float
+    lib.gdr_linear_decode.argtypes = [P, P, P, P, P, P, I, I, I, I, I, L, L, L, F, I, I, I, P]
+    lib.gdr_linear_decode.restype = I
+    lib.gdr_linear_prefill.argtypes = [P, P, P, P, P, I, P, P, P, I, I, I, I, I, L, L, L, F, I, I,
+                                       I, P, S, P]
+    lib.gdr_linear_prefill.restype = I
+    lib.gdr_linear_prefill_workspace_bytes.argtypes = [I, I, I, I, I, I]
+    lib.gdr_linear_prefill_workspace_bytes.restype = S
+    lib.gdr_linear_backward.argtypes = [P, P, P, P, P, I, P, P, P, P, P, P, P, P, I, I, I, I, I,
+                                        L, L, L, F, I, I, I, P, S, P]
+    lib.gdr_linear_backward.restype = I
+    lib.gdr_linear_backward_workspace_bytes.argtypes = [I, I, I, I, I, I, I]
+    lib.gdr_linear_backward_workspace_bytes.restype = S
     lib.gdr_status_string.argtypes = [I]
     lib.gdr_status_string.restype = ctypes.c_char_p
     lib.gdr_last_error.argtypes = []
@@ -292,3 +312,159 @@ def gdr_state_fixup(L, M, state_in, chunk_offsets, fixed, stream=None) -> None:
         _dev_ptr(chunk_offsets, "chunk_offsets", _I32), N, _dev_ptr(fixed, "fixed", _F32),
         n_chunks, H, dk, dv, _stream(stream))
     _check(st, "gdr_state_fixup")
+
+
+def _rows_ptr(t, name, dtypes):
+    """Pointer and token stride of a [tokens, heads, d] tensor whose tokens may
+    be rows of a wider tensor (stride 0: dense)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise GdrError(f"{name} must be a torch tensor on the GPU")
+    if t.dtype not in dtypes:
+        raise GdrError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if t.is_contiguous():
+        return t.data_ptr(), 0
+    n, h, d = t.shape
+    st, sh, sd = t.stride()
+    if sd != 1 or (h > 1 and sh != d) or (n > 1 and st < h * d):
+        raise GdrError(f"{name}: the heads of a token must be contiguous and tokens must not overlap")
+    return t.data_ptr(), st if n > 1 else 0
+
+
+def _gates(g, tokens, H, who):
+    """Pointer and decay code of g, [tokens, H] or [H]."""
+    if g.shape == (tokens, H):
+        return _dev_ptr(g, "g", _F32), GDR_DECAY_TOKEN
+    if g.shape == (H,):
+        return _dev_ptr(g, "g", _F32), GDR_DECAY_HEAD
+    raise GdrError(f"{who}: g must have shape {(tokens, H)} or {(H,)}")
+
+
+def _same_device(who, *tensors):
+    """The one device of the tensors, as a context in which to launch."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise GdrError(f"{who}: tensors are on {dev} and {t.device}")
+    return torch.cuda.device(dev)
+
+
+def gdr_linear_decode(q, k, v, g, state, o, *, scale=1.0, stream=None) -> None:
+    """One token of linear attention with a decay for each head, S <- e^g S +
+    v k^T, o = scale S q, state updated in place.  q, k [N, Hk, dk], v [N, H,
+    dv] (bf16 or fp32, one dtype; tokens may be rows of wider tensors); g [N, H]
+    or [H] fp32; state [N, H, dv, dk] fp32; o [N, H, dv] bf16 or fp32.  Value
+    head h reads query and key head h // (H // Hk)."""
+    who = "gdr_linear_decode"
+    N, Hk, dk = q.shape
+    H, dv = v.shape[1:]
+    if k.shape != q.shape or v.shape[0] != N or state.shape != (N, H, dv, dk) \
+            or o.shape != (N, H, dv):
+        raise GdrError(f"{who}: inconsistent shapes")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise GdrError(f"{who}: q, k, v must share a dtype")
+    (qp, qs), (kp, ks), (vp, vs) = (_rows_ptr(t, n, _IO) for t, n in ((q, "q"), (k, "k"), (v, "v")))
+    gp, decay = _gates(g, N, H, who)
+    sp, op = _dev_ptr(state, "state", _F32), _dev_ptr(o, "o", _IO)
+    with _same_device(who, q, k, v, g, state, o):
+        st = _load().gdr_linear_decode(qp, kp, vp, gp, sp, op, N, H, Hk, dk, dv, qs, ks, vs, scale,
+                                       decay, _code(q.dtype), _code(o.dtype), _stream(stream))
+    _check(st, who)
+
+
+def gdr_linear_prefill_workspace_bytes(T_total, N, H, dk, dv, in_dtype=GDR_BF16) -> int:
+    """in_dtype: GDR_BF16 / GDR_FP32 or the torch dtype of q, k, v."""
+    if isinstance(in_dtype, torch.dtype):
+        in_dtype = _code(in_dtype)
+    return int(_load().gdr_linear_prefill_workspace_bytes(T_total, N, H, dk, dv, in_dtype))
+
+
+def gdr_linear_backward_workspace_bytes(T_total, N, H, Hk, dk, dv, in_dtype=GDR_BF16) -> int:
+    """in_dtype: GDR_BF16 / GDR_FP32 or the torch dtype of q, k, v."""
+    if isinstance(in_dtype, torch.dtype):
+        in_dtype = _code(in_dtype)
+    return int(_load().gdr_linear_backward_workspace_bytes(T_total, N, H, Hk, dk, dv, in_dtype))
+
+
+def _linear_args(who, q, k, v, g, cu_seqlens, state_in, like_v):
+    """Checks shared by prefill and backward; pointers of q, k, v, g, cu and
+    state_in, their strides, and the sizes."""
+    T, Hk, dk = q.shape
+    H, dv = v.shape[1:]
+    N = cu_seqlens.shape[0] - 1
+    if k.shape != q.shape or v.shape[0] != T or cu_seqlens.dim() != 1 \
+            or any(t.shape != (T, H, dv) for t in like_v):
+        raise GdrError(f"{who}: inconsistent shapes")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise GdrError(f"{who}: q, k, v must share a dtype")
+    if state_in is not None and state_in.shape != (N, H, dv, dk):
+        raise GdrError(f"{who}: state_in must have shape {(N, H, dv, dk)}")
+    (qp, qs), (kp, ks), (vp, vs) = (_rows_ptr(t, n, _IO) for t, n in ((q, "q"), (k, "k"), (v, "v")))
+    gp, decay = _gates(g, T, H, who)
+    ptrs = [qp, kp, vp, gp, _dev_ptr(cu_seqlens, "cu_seqlens", _I32), N,
+            _dev_ptr(state_in, "state_in", _F32, optional=True)]
+    return ptrs, (qs, ks, vs), decay, (T, N, H, Hk, dk, dv)
+
+
+def _workspace(workspace, need, device, stream):
+    """Pointer and size of the caller's workspace, or of one allocated here on
+    the launch stream (none when none is needed), and its tensor."""
+    if workspace is None and need:
+        with torch.cuda.stream(_stream_obj(stream)):
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    if workspace is None:
+        return None, 0, None
+    return _dev_ptr(workspace, "workspace", (torch.uint8,)), workspace.numel(), workspace
+
+
+def gdr_linear_prefill(q, k, v, g, cu_seqlens, state_in, state_out, o, *, scale=1.0,
+                       workspace=None, stream=None) -> None:
+    """Linear attention with a decay for each head over packed sequences: S_t =
+    e^g S_{t-1} + v_t k_t^T, o_t = scale S_t q_t.  q, k [T, Hk, dk], v [T, H, dv]
+    (bf16 or fp32, one dtype; tokens may be rows of wider tensors); g [T, H] or
+    [H] fp32; cu_seqlens [N+1] int32 (device); state_in [N, H, dv, dk] fp32 or
+    None; state_out like it (may be state_in) or None; o [T, H, dv] bf16 or
+    fp32.  workspace: as gdr_chunk_prefill's, by
+    gdr_linear_prefill_workspace_bytes."""
+    who = "gdr_linear_prefill"
+    ptrs, strides, decay, (T, N, H, Hk, dk, dv) = _linear_args(who, q, k, v, g, cu_seqlens,
+                                                               state_in, (o,))
+    if state_out is not None and state_out.shape != (N, H, dv, dk):
+        raise GdrError(f"{who}: state_out must have shape {(N, H, dv, dk)}")
+    sp, op = _dev_ptr(state_out, "state_out", _F32, optional=True), _dev_ptr(o, "o", _IO)
+    code = _code(q.dtype)
+    with _same_device(who, q, k, v, g, cu_seqlens, state_in, state_out, o, workspace):
+        need = _load().gdr_linear_prefill_workspace_bytes(T, N, H, dk, dv, code)
+        wp, wb, workspace = _workspace(workspace, need, q.device, stream)
+        st = _load().gdr_linear_prefill(*ptrs, sp, op, T, H, Hk, dk, dv, *strides, scale, decay,
+                                        code, _code(o.dtype), wp, wb, _stream(stream))
+    _check(st, who)
+
+
+def gdr_linear_backward(q, k, v, g, cu_seqlens, state_in, do, dstate_out, dq, dk, dv, *, dg=None,
+                        dstate_in=None, scale=1.0, workspace=None, stream=None) -> None:
+    """Gradients of gdr_linear_prefill from do [T, H, dv] (the dtype of q) and
+    dstate_out ([N, H, dv, dk] fp32 or None): dq, dk [T, Hk, dk] and dv [T, H,
+    dv] (bf16 or fp32, one dtype), dg (fp32, the shape of g) and dstate_in
+    ([N, H, dv, dk] fp32) where given.  workspace: by
+    gdr_linear_backward_workspace_bytes."""
+    who = "gdr_linear_backward"
+    states = (cu_seqlens.shape[0] - 1, v.shape[1], v.shape[2], q.shape[2])
+    if dq.shape != q.shape or dk.shape != q.shape or (dg is not None and dg.shape != g.shape) \
+            or any(t is not None and t.shape != states for t in (dstate_out, dstate_in)):
+        raise GdrError(f"{who}: inconsistent shapes")
+    ptrs, strides, decay, (T, N, H, Hk, kd, vd) = _linear_args(who, q, k, v, g, cu_seqlens,
+                                                               state_in, (do, dv))
+    if dk.dtype != dq.dtype or dv.dtype != dq.dtype:
+        raise GdrError(f"{who}: dq, dk, dv must share a dtype")
+    outs = [_dev_ptr(do, "do", (q.dtype,)), _dev_ptr(dstate_out, "dstate_out", _F32, optional=True),
+            _dev_ptr(dq, "dq", _IO), _dev_ptr(dk, "dk", _IO), _dev_ptr(dv, "dv", _IO),
+            _dev_ptr(dg, "dg", _F32, optional=True),
+            _dev_ptr(dstate_in, "dstate_in", _F32, optional=True)]
+    code = _code(q.dtype)
+    with _same_device(who, q, k, v, g, cu_seqlens, state_in, do, dstate_out, dq, dk, dv, dg,
+                      dstate_in, workspace):
+        need = _load().gdr_linear_backward_workspace_bytes(T, N, H, Hk, kd, vd, code)
+        wp, wb, workspace = _workspace(workspace, need, q.device, stream)
+        st = _load().gdr_linear_backward(*ptrs, *outs, T, H, Hk, kd, vd, *strides, scale, decay,
+                                         code, _code(dq.dtype), wp, wb, _stream(stream))
+    _check(st, who)

@@ -140,4 +140,69 @@ hipError_t launch_segment_starts(const float* state_in, const float* seg_end,
                                  const int32_t* seg_idx, int max_segs, int H, int d,
                                  float* seg_start, hipStream_t stream);
 
+// ---- linear attention with a decay for each head (linear.hip)
+
+// Decays: one value for each token and head ([T, H]) or for each head ([H]).
+struct LinearGates {
+  const float* g;
+  int per_token;
+};
+
+// One pass of the recurrence over packed sequences, in either direction.  With
+// a state Z [od, kd] per (sequence, head), rows x, y of kd and w of od values:
+//   forward:   Z_t = alpha_t Z_{t-1} + us w_t y_t^T,  out_t = os Z_t x_t
+//   backward:  Z_t = alpha_{t+1} Z_{t+1} + us w_t y_t^T,  out_t = os Z_t x_t
+// The prompt pass is (x, y, w) = (q, k, v) forward; the gradients are
+// dq: (do, v, k) forward, dv: (k, q, do) backward, dk: (v, do, q) backward.
+// Head h reads head h / group of a tensor; a token's row starts at
+// token * stride + head * width elements.
+struct LinearRows {
+  const void* p;
+  int64_t stride;
+  int group;
+};
+struct LinearPass {
+  LinearRows x, y, w;
+  LinearRows e;        // rows of od values to dot with the outputs (dot != NULL)
+  void* out;           // [T, H, od]
+  float* dot;          // [od / 16][T * H] partial sums of e_t . out_t without the
+                       // token's own term, or NULL
+  const float* start;  // states the walk starts from, NULL for zero
+  float* end;          // states at the end of the walk, NULL: not written
+  const float* end_with;  // states to dot with those at the end, or NULL
+  float* end_dot;         // [od / 16][N * H] partial sums of that dot product
+  int64_t row, col;    // element strides of a state row and column, in start,
+                       // end and end_with ([N * H] states of od * kd elements)
+  float us, os;
+  int od, kd, backward, out_dtype;
+};
+
+struct LinearBatch {
+  const int32_t* cu;
+  int N, H, T_total, in_dtype;
+  LinearGates gates;
+};
+
+hipError_t launch_linear_decode(const void* q, const void* k, const void* v,
+                                const LinearGates& g, float* state, void* o, int N, int H, int Hk,
+                                int dk, int dv, int64_t qs, int64_t ks, int64_t vs, float scale,
+                                int in_dtype, int out_dtype, hipStream_t stream);
+
+hipError_t launch_linear_pass(const LinearBatch& b, const LinearPass& p, hipStream_t stream);
+
+// dg_t = dg_{t+1} + row_t - col_t, starting from the end's dot product; row and
+// col are [parts][T * H] partial sums, end_dot [parts][N * H].
+hipError_t launch_linear_dg(const LinearBatch& b, const float* row, int row_parts,
+                            const float* col, int col_parts, const float* end_dot, int end_parts,
+                            float* dg, hipStream_t stream);
+
+// dg[h] = sum over tokens of dg_t, [T, H] -> [H].
+hipError_t launch_linear_dg_heads(const LinearBatch& b, const float* dg_t, float* dg,
+                                  hipStream_t stream);
+
+// Sum of [T, H, d] fp32 over groups of heads to [T, H / group, d] of out_dtype,
+// for the tokens of the batch's sequences.
+hipError_t launch_linear_group_sum(const LinearBatch& b, const float* part, int group, int d,
+                                   void* out, int out_dtype, hipStream_t stream);
+
 }  // namespace gdr

@@ -38,7 +38,8 @@
  *     non-decreasing, start at 0 and end at T_total (resp. the chunk count);
  *     kernels clamp every index they derive from them to the buffer sizes
  *     given, so bad values give wrong results but no out-of-bounds access.
- *   - Supported shapes: (dk, dv) in {(64, 64), (128, 128)}; chunk in {16, 64}.
+ *   - Supported shapes of the gated delta rule: (dk, dv) in {(64, 64),
+ *     (128, 128)}; chunk in {16, 64}.
  *   - Dtypes: q, k, v are bf16 or fp32 (in_dtype); o is bf16 or fp32
  *     (out_dtype; bf16 is round-to-nearest-even of the fp32 result).  g, beta,
  *     states, L, M and fixed states are always fp32.
@@ -283,6 +284,113 @@ gdr_status gdr_chunk_prefill_noalloc(const void* q, const void* k, const void* v
 gdr_status gdr_state_fixup(const float* L, const float* M, const float* state_in,
                            const int32_t* chunk_offsets, int N, float* fixed,
                            int n_chunks, int H, int dk, int dv, gdr_stream_t stream);
+
+/*
+ * Linear attention with a decay for each head -- the recurrence of retention
+ * and of scalar-gate state-space layers, the gated delta rule without its
+ * delta term:
+ *
+ *     S_t = alpha_t * S_{t-1} + v_t k_t^T,   o_t = scale * S_t q_t
+ *     alpha_t = exp(g)
+ *
+ * g is one value for each token and head (GDR_DECAY_TOKEN) or one for each
+ * head (GDR_DECAY_HEAD, the same at every token).  g <= 0 is expected, and g
+ * below -110, -inf among it, counts as -110: a decay of exactly zero in fp32.
+ * Value head h reads query and key head h / (H / Hk), with H a multiple of Hk.
+ *
+ * Beyond the conventions above, for gdr_linear_*:
+ *   - (dk, dv) may be any of {64, 128} x {64, 128}.
+ *   - q, k and v may be slices of wider token rows: q_stride, k_stride and
+ *     v_stride are the elements from one token's row to the next, 0 for dense
+ *     ([T, heads, d] contiguous).  The heads of one token are always
+ *     contiguous, and a stride is a multiple of 16 bytes and not below the
+ *     heads' width.
+ *   - cu_seqlens[N] may be below T_total: rows behind the last sequence are
+ *     neither read nor written.
+ *   - An infinity or NaN in a token's q, k or v may make the outputs of its
+ *     own chunk of 64 tokens non-finite as well as those after it; other
+ *     sequences are not affected.
+ *   - Every result is deterministic: no atomics.
+ */
+typedef enum { GDR_DECAY_TOKEN = 0, GDR_DECAY_HEAD = 1 } gdr_decay;
+
+/*
+ * gdr_linear_decode -- one token for N x H states, updated IN PLACE.
+ *
+ *   q, k      [N, Hk, dk]     in_dtype, rows q_stride / k_stride apart
+ *   v         [N, H, dv]      in_dtype, rows v_stride apart
+ *   g         [N, H] or [H]   fp32, by `decay`
+ *   state     [N, H, dv, dk]  fp32, read and overwritten with S_t
+ *   o         [N, H, dv]      out_dtype
+ *   N, H, Hk  > 0, H % Hk == 0
+ * No tensor may overlap `state`.
+ */
+gdr_status gdr_linear_decode(const void* q, const void* k, const void* v, const float* g,
+                             float* state, void* o, int N, int H, int Hk, int dk, int dv,
+                             int64_t q_stride, int64_t k_stride, int64_t v_stride, float scale,
+                             gdr_decay decay, gdr_dtype in_dtype, gdr_dtype out_dtype,
+                             gdr_stream_t stream);
+
+/*
+ * gdr_linear_prefill -- prompts: packed variable-length sequences.
+ *
+ *   q, k        [T_total, Hk, dk]  in_dtype, rows q_stride / k_stride apart
+ *   v           [T_total, H, dv]   in_dtype, rows v_stride apart
+ *   g           [T_total, H] or [H] fp32, by `decay`
+ *   cu_seqlens  [N+1] int32        device; sequence n is tokens [cu[n], cu[n+1])
+ *   state_in    [N, H, dv, dk]     fp32, or NULL for zero states
+ *   state_out   [N, H, dv, dk]     fp32 final states; may equal state_in; NULL:
+ *                                  not written.  A sequence of length 0 passes
+ *                                  its initial state on
+ *   o           [T_total, H, dv]   out_dtype
+ *   workspace   gdr_linear_prefill_workspace_bytes(...) bytes of device scratch
+ *               (NULL when that is 0); its contents do not matter
+ * o must not overlap any input.
+ */
+gdr_status gdr_linear_prefill(const void* q, const void* k, const void* v, const float* g,
+                              const int32_t* cu_seqlens, int N, const float* state_in,
+                              float* state_out, void* o, int T_total, int H, int Hk, int dk,
+                              int dv, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                              float scale, gdr_decay decay, gdr_dtype in_dtype,
+                              gdr_dtype out_dtype, void* workspace, size_t workspace_bytes,
+                              gdr_stream_t stream);
+
+/* Device workspace of gdr_linear_prefill; 0 also on bad arguments. */
+size_t gdr_linear_prefill_workspace_bytes(int T_total, int N, int H, int dk, int dv,
+                                          gdr_dtype in_dtype);
+
+/*
+ * gdr_linear_backward -- gradients of gdr_linear_prefill.  With d_o the
+ * gradient of o and dstate_out that of state_out, and R_t the gradient of S_t,
+ *     R_t  = scale d_o_t q_t^T + alpha_{t+1} R_{t+1}
+ *     dq_t = scale S_t^T d_o_t,  dk_t = R_t^T v_t,  dv_t = R_t k_t
+ *     dg_t = alpha_t <R_t, S_{t-1}>,  dstate_in = alpha_1 R_1
+ *
+ *   q, k, v, g, cu_seqlens, state_in   as given to gdr_linear_prefill
+ *   d_o          [T_total, H, dv]   in_dtype, dense
+ *   dstate_out   [N, H, dv, dk]     fp32, or NULL for zero
+ *   dq, dk_out   [T_total, Hk, dk]  grad_dtype: summed over the value heads that
+ *                                   share the head, in fp32
+ *   dv_out       [T_total, H, dv]   grad_dtype
+ *   dg           fp32, the shape of g, or NULL.  For GDR_DECAY_HEAD the sum over
+ *                all tokens.  Where g is below -110 the gradient is that of a
+ *                decay of zero: 0
+ *   dstate_in    [N, H, dv, dk]     fp32, or NULL
+ *   workspace    gdr_linear_backward_workspace_bytes(...) bytes
+ * No output may overlap an input or another output (dstate_in not dstate_out).
+ */
+gdr_status gdr_linear_backward(const void* q, const void* k, const void* v, const float* g,
+                               const int32_t* cu_seqlens, int N, const float* state_in,
+                               const void* d_o, const float* dstate_out, void* dq, void* dk_out,
+                               void* dv_out, float* dg, float* dstate_in, int T_total, int H,
+                               int Hk, int dk, int dv, int64_t q_stride, int64_t k_stride,
+                               int64_t v_stride, float scale, gdr_decay decay,
+                               gdr_dtype in_dtype, gdr_dtype grad_dtype, void* workspace,
+                               size_t workspace_bytes, gdr_stream_t stream);
+
+/* Device workspace of gdr_linear_backward; 0 also on bad arguments. */
+size_t gdr_linear_backward_workspace_bytes(int T_total, int N, int H, int Hk, int dk, int dv,
+                                           gdr_dtype in_dtype);
 
 /* Static text for a status code. */
 const char* gdr_status_string(gdr_status s);
