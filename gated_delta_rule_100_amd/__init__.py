@@ -35,6 +35,9 @@ __all__ = [
     "gdr_linear_prefill_workspace_bytes",
     "gdr_linear_backward",
     "gdr_linear_backward_workspace_bytes",
+    "gdr_block_norm",
+    "gdr_block_norm_backward",
+    "gdr_block_norm_backward_workspace_bytes",
     "gdr_status_string",
     "gdr_last_error",
 ]
@@ -43,6 +46,7 @@ GDR_BF16 = 0
 GDR_FP32 = 1
 GDR_DECAY_TOKEN = 0
 GDR_DECAY_HEAD = 1
+GDR_GATES = {"silu": 0, "sigmoid": 1}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libgdr.so")
@@ -97,6 +101,12 @@ def _load():
     lib.gdr_linear_backward.restype = I
     lib.gdr_linear_backward_workspace_bytes.argtypes = [I, I, I, I, I, I, I]
     lib.gdr_linear_backward_workspace_bytes.restype = S
+    lib.gdr_block_norm.argtypes = [P] * 7 + [L, I, F, F, I, I, I, I, P]
+    lib.gdr_block_norm.restype = I
+    lib.gdr_block_norm_backward.argtypes = [P] * 12 + [L, I, F, F, I, I, I, I, P, S, P]
+    lib.gdr_block_norm_backward.restype = I
+    lib.gdr_block_norm_backward_workspace_bytes.argtypes = [L, I]
+    lib.gdr_block_norm_backward_workspace_bytes.restype = S
     lib.gdr_status_string.argtypes = [I]
     lib.gdr_status_string.restype = ctypes.c_char_p
     lib.gdr_last_error.argtypes = []
@@ -467,4 +477,75 @@ def gdr_linear_backward(q, k, v, g, cu_seqlens, state_in, do, dstate_out, dq, dk
         wp, wb, workspace = _workspace(workspace, need, q.device, stream)
         st = _load().gdr_linear_backward(*ptrs, *outs, T, H, Hk, kd, vd, *strides, scale, decay,
                                          code, _code(dq.dtype), wp, wb, _stream(stream))
+    _check(st, who)
+
+
+def _norm_args(who, x, w_after, gate, act, residual, w_before, like_x, outs):
+    """Checks shared by the norm and its gradient: row operands like x, outputs
+    of one dtype, weights [D] of one dtype.  Returns rows, D and the codes of
+    gate, input, weights and outputs."""
+    D = x.shape[-1] if x.dim() else 0
+    for t in (gate, residual, *like_x):
+        if t is not None and (t.shape != x.shape or t.dtype != x.dtype):
+            raise GdrError(f"{who}: row operands must have the shape and dtype of x")
+    outs = [t for t in outs if t is not None]
+    if any(t.shape != x.shape or t.dtype != outs[0].dtype for t in outs):
+        raise GdrError(f"{who}: outputs must have the shape of x and one dtype")
+    weights = [w for w in (w_after, w_before) if w is not None]
+    if any(w.shape != (D,) or w.dtype != weights[0].dtype for w in weights):
+        raise GdrError(f"{who}: weights must have shape {(D,)} and one dtype")
+    if gate is not None and act not in GDR_GATES:
+        raise GdrError(f"{who}: act must be one of {sorted(GDR_GATES)}")
+    return (x.numel() // D if D else 0, D, GDR_GATES.get(act, 0), _code(x.dtype),
+            _code(weights[0].dtype) if weights else GDR_FP32,
+            _code(outs[0].dtype) if outs else GDR_FP32)
+
+
+def gdr_block_norm(x, h=None, y=None, *, w_after=None, gate=None, act="silu", residual=None,
+                   scale=1.0, w_before=None, eps=1e-6, stream=None) -> None:
+    """Norms around a block with its gate and scaled residual, per row of x
+    [..., D]: u = x / rms(x) * w_after, u *= act(gate), h = residual + scale * u,
+    y = h / rms(h) * w_before, each part where its operand is given.  gate and
+    residual like x; weights [D]; h and y [..., D] (h may be left out where y is
+    wanted; y exactly with w_before).  bf16 or fp32 each."""
+    who = "gdr_block_norm"
+    rows, D, ac, ic, wc, oc = _norm_args(who, x, w_after, gate, act, residual, w_before, (), (h, y))
+    p = [_dev_ptr(x, "x", _IO)] + [_dev_ptr(t, n, _IO, optional=True) for t, n in (
+        (w_after, "w_after"), (gate, "gate"), (residual, "residual"), (w_before, "w_before"),
+        (h, "h"), (y, "y"))]
+    with _same_device(who, x, w_after, gate, residual, w_before, h, y):
+        st = _load().gdr_block_norm(*p, rows, D, scale, eps, ac, ic, wc, oc, _stream(stream))
+    _check(st, who)
+
+
+def gdr_block_norm_backward_workspace_bytes(rows, D) -> int:
+    return int(_load().gdr_block_norm_backward_workspace_bytes(rows, D))
+
+
+def gdr_block_norm_backward(x, dh, dy, dx, *, w_after=None, gate=None, act="silu", residual=None,
+                            scale=1.0, w_before=None, eps=1e-6, dgate=None, dresidual=None,
+                            dw_after=None, dw_before=None, workspace=None, stream=None) -> None:
+    """Gradients of gdr_block_norm from dh and dy (like x; dh None: zero, dy
+    exactly with w_before): dx, and dgate, dresidual (like x) and dw_after,
+    dw_before ([D] fp32) where given.  workspace: a uint8 device tensor of
+    gdr_block_norm_backward_workspace_bytes(rows, D) bytes, or None to allocate
+    one here on the launch stream."""
+    who = "gdr_block_norm_backward"
+    rows, D, ac, ic, wc, oc = _norm_args(who, x, w_after, gate, act, residual, w_before, (dh, dy),
+                                         (dx, dgate, dresidual))
+    if any(t is not None and t.shape != (D,) for t in (dw_after, dw_before)):
+        raise GdrError(f"{who}: weight gradients must have shape {(D,)}")
+    p = [_dev_ptr(x, "x", _IO)] + [_dev_ptr(t, n, _IO, optional=True) for t, n in (
+        (w_after, "w_after"), (gate, "gate"), (residual, "residual"), (w_before, "w_before"),
+        (dh, "dh"), (dy, "dy"), (dx, "dx"), (dgate, "dgate"), (dresidual, "dresidual"))]
+    p += [_dev_ptr(t, n, _F32, optional=True) for t, n in ((dw_after, "dw_after"),
+                                                          (dw_before, "dw_before"))]
+    with _same_device(who, x, w_after, gate, residual, w_before, dh, dy, dx, dgate, dresidual,
+                      dw_after, dw_before, workspace):
+        need = 0
+        if dw_after is not None or dw_before is not None:
+            need = _load().gdr_block_norm_backward_workspace_bytes(rows, D)
+        wp, wb, workspace = _workspace(workspace, need, x.device, stream)
+        st = _load().gdr_block_norm_backward(*p, rows, D, scale, eps, ac, ic, wc, oc, wp, wb,
+                                             _stream(stream))
     _check(st, who)

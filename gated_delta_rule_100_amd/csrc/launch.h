@@ -205,4 +205,25 @@ hipError_t launch_linear_dg_heads(const LinearBatch& b, const float* dg_t, float
 hipError_t launch_linear_group_sum(const LinearBatch& b, const float* part, int group, int d,
                                    void* out, int out_dtype, hipStream_t stream);
 
+// ---- norms around a block (norm.hip)
+
+// Operands of gdr_block_norm and its gradient (gdr.h); unused ones are NULL.
+struct BlockNorm {
+  const void *x, *w_after, *gate, *residual, *w_before;
+  void *h, *y;
+  const void *dh, *dy;
+  void *dx, *dgate, *dresidual;
+  float *part_after, *part_before;  // [block_norm_backward_blocks][D]
+  int64_t rows;
+  int D, act, in_dtype, w_dtype, out_dtype;
+  float scale, eps;
+};
+
+// Workgroups of the gradient kernel, and so rows of its partial sums.
+int block_norm_backward_blocks(int64_t rows, int D);
+
+hipError_t launch_block_norm(const BlockNorm& p, hipStream_t stream);
+hipError_t launch_block_norm_backward(const BlockNorm& p, float* dw_after, float* dw_before,
+                                      hipStream_t stream);
+
 }  // namespace gdr

@@ -1,0 +1,364 @@
+// norm.hip -- the norms around a block with its gate and scaled residual
+// (gdr_block_norm in gdr.h), and their gradient, on gfx950.
+//
+// Both are streams: every operand is read once and every result written once,
+// and a row stays in the registers of its threads between the sums.  TPR
+// threads hold a row, E elements each; rows of up to 1024 values are summed
+// inside a wave, longer ones across the waves of a workgroup.  The gradient
+// runs a fixed number of workgroups over the rows, so that each thread keeps
+// the weight gradients of its columns in registers; one workgroup's sums go to
+// the workspace and a second kernel adds them in order.
+#include <type_traits>
+
+#include "gdr_device.h"
+#include "launch.h"
+
+namespace gdr {
+namespace {
+
+// Row layout: D % 8 == 0 gives each thread pieces of 8 consecutive elements
+// (16-byte accesses), other D single elements TPR apart.
+template <int TPR>
+__device__ __forceinline__ int element(int i, int t, bool vec) {
+  return vec ? ((i >> 3) * TPR + t) * 8 + (i & 7) : i * TPR + t;
+}
+
+template <Dt IN, int TPR, int E>
+__device__ __forceinline__ void load_row(const void* base, size_t row, int D, int t, bool vec,
+                                         float (&out)[E]) {
+  const size_t at = row * D;
+  if (vec) {
+#pragma unroll
+    for (int j = 0; j < E / 8; ++j) {
+      const int c = (j * TPR + t) * 8;
+      float x[8];
+      if (c < D) {
+        load_vec<IN, 8>(base, at + c, x);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) out[8 * j + e] = x[e];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int c = i * TPR + t;
+      out[i] = c < D ? load_scalar<IN>(base, at + c) : 0.f;
+    }
+  }
+}
+
+template <int TPR, int E>
+__device__ __forceinline__ void load_weight(const void* w, int dtype, int D, int t, bool vec,
+                                            float (&out)[E]) {
+  if (dtype == 0) load_row<Dt::BF16, TPR, E>(w, 0, D, t, vec, out);
+  else load_row<Dt::F32, TPR, E>(w, 0, D, t, vec, out);
+}
+
+template <int TPR, int E>
+__device__ __forceinline__ void store_row(void* base, int dtype, size_t row, int D, int t, bool vec,
+                                          const float (&x)[E]) {
+  typedef float f32x8 __attribute__((ext_vector_type(8)));
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  const size_t at = row * D;
+  if (vec) {
+#pragma unroll
+    for (int j = 0; j < E / 8; ++j) {
+      const int c = (j * TPR + t) * 8;
+      if (c >= D) continue;
+      if (dtype == 0) {
+        f32x8 v;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = x[8 * j + e];
+        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(base) + at + c) =
+            __builtin_bit_cast(u32x4, __builtin_convertvector(v, bf16x8));
+      } else {
+        floatx4* p = reinterpret_cast<floatx4*>(static_cast<float*>(base) + at + c);
+        p[0] = floatx4{x[8 * j], x[8 * j + 1], x[8 * j + 2], x[8 * j + 3]};
+        p[1] = floatx4{x[8 * j + 4], x[8 * j + 5], x[8 * j + 6], x[8 * j + 7]};
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int c = i * TPR + t;
+      if (c >= D) continue;
+      if (dtype == 0) store_scalar<Dt::BF16>(base, at + c, x[i]);
+      else store_scalar<Dt::F32>(base, at + c, x[i]);
+    }
+  }
+}
+
+// Sum of x over the TPR threads of a row, the same bits in each of them.  Rows
+// of several waves go through LDS; two slots alternate, so that one barrier a
+// sum is enough.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float x, float (*lds)[16], int& slot) {
+  constexpr int W = TPR < 64 ? TPR : 64;
+#pragma unroll
+  for (int s = 1; s < W; s <<= 1) x += __shfl_xor(x, s);
+  if constexpr (TPR > 64) {
+    slot ^= 1;
+    if ((threadIdx.x & 63) == 0) lds[slot][threadIdx.x >> 6] = x;
+    __syncthreads();
+    x = 0.f;
+#pragma unroll
+    for (int i = 0; i < TPR / 64; ++i) x += lds[slot][i];
+  }
+  return x;
+}
+
+__device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
+
+template <Dt IN, int TPR, int E>
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_kernel(BlockNorm p) {
+  constexpr int THREADS = TPR > 256 ? TPR : 256, RPB = THREADS / TPR;
+  __shared__ float lds[2][16];
+  int slot = 0;
+  const int t = threadIdx.x % TPR;
+  const bool vec = p.D % 8 == 0;
+  const float inv_d = 1.f / static_cast<float>(p.D);
+  const size_t row = static_cast<size_t>(blockIdx.x) * RPB + threadIdx.x / TPR;
+  if (row >= static_cast<size_t>(p.rows)) return;  // whole rows: no barrier is missed (RPB > 1
+                                                   // only where a row is inside one wave)
+  float x[E], z[E], r[E];
+  load_row<IN, TPR, E>(p.x, row, p.D, t, vec, x);
+  if (p.gate) load_row<IN, TPR, E>(p.gate, row, p.D, t, vec, z);
+  if (p.residual) load_row<IN, TPR, E>(p.residual, row, p.D, t, vec, r);
+  if (p.w_after) {
+    float w[E];
+    load_weight<TPR, E>(p.w_after, p.w_dtype, p.D, t, vec, w);
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) ss = fmaf(x[i], x[i], ss);
+    const float inv = rsqrtf(row_sum<TPR>(ss, lds, slot) * inv_d + p.eps);
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[i] = x[i] * inv * w[i];
+  }
+  if (p.gate) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[i] *= sigmoid(z[i]) * (p.act == 0 ? z[i] : 1.f);
+  }
+#pragma unroll
+  for (int i = 0; i < E; ++i) x[i] = p.residual ? fmaf(p.scale, x[i], r[i]) : p.scale * x[i];
+  if (p.w_before) {
+    float w[E], y[E];
+    load_weight<TPR, E>(p.w_before, p.w_dtype, p.D, t, vec, w);
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) ss = fmaf(x[i], x[i], ss);
+    const float inv = rsqrtf(row_sum<TPR>(ss, lds, slot) * inv_d + p.eps);
+#pragma unroll
+    for (int i = 0; i < E; ++i) y[i] = x[i] * inv * w[i];
+    store_row<TPR, E>(p.y, p.out_dtype, row, p.D, t, vec, y);
+  }
+  if (p.h) store_row<TPR, E>(p.h, p.out_dtype, row, p.D, t, vec, x);
+}
+
+template <Dt IN, int TPR, int E>
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_backward_kernel(BlockNorm p) {
+  constexpr int THREADS = TPR > 256 ? TPR : 256, RPB = THREADS / TPR;
+  __shared__ float lds[2][16];
+  int slot = 0;
+  const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  const bool vec = p.D % 8 == 0;
+  const float inv_d = 1.f / static_cast<float>(p.D);
+  float wa[E], wb[E], ga[E], gb[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) wa[i] = wb[i] = ga[i] = gb[i] = 0.f;
+  if (p.w_after) load_weight<TPR, E>(p.w_after, p.w_dtype, p.D, t, vec, wa);
+  if (p.w_before) load_weight<TPR, E>(p.w_before, p.w_dtype, p.D, t, vec, wb);
+  for (size_t row = static_cast<size_t>(blockIdx.x) * RPB + sub; row < static_cast<size_t>(p.rows);
+       row += static_cast<size_t>(gridDim.x) * RPB) {
+    float x[E], z[E], d[E];
+    load_row<IN, TPR, E>(p.x, row, p.D, t, vec, x);
+    if (p.gate) load_row<IN, TPR, E>(p.gate, row, p.D, t, vec, z);
+    if (p.dh) {
+      load_row<IN, TPR, E>(p.dh, row, p.D, t, vec, d);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) d[i] = 0.f;
+    }
+    float ix = 1.f;
+    if (p.w_after) {
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < E; ++i) ss = fmaf(x[i], x[i], ss);
+      ix = rsqrtf(row_sum<TPR>(ss, lds, slot) * inv_d + p.eps);
+    }
+    if (p.w_before) {
+      float h[E], dy[E];
+      load_row<IN, TPR, E>(p.dy, row, p.D, t, vec, dy);
+      if (p.residual) {
+        load_row<IN, TPR, E>(p.residual, row, p.D, t, vec, h);
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) h[i] = 0.f;
+      }
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        float u = p.w_after ? x[i] * ix * wa[i] : x[i];
+        if (p.gate) u *= sigmoid(z[i]) * (p.act == 0 ? z[i] : 1.f);
+        h[i] = fmaf(p.scale, u, h[i]);
+        ss = fmaf(h[i], h[i], ss);
+      }
+      const float ih = rsqrtf(row_sum<TPR>(ss, lds, slot) * inv_d + p.eps);
+      float dot = 0.f;
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        h[i] *= ih;
+        gb[i] = fmaf(dy[i], h[i], gb[i]);
+        dy[i] *= wb[i];
+        dot = fmaf(dy[i], h[i], dot);
+      }
+      dot = row_sum<TPR>(dot, lds, slot) * inv_d;
+#pragma unroll
+      for (int i = 0; i < E; ++i) d[i] = fmaf(ih, fmaf(-h[i], dot, dy[i]), d[i]);
+    }
+    if (p.dresidual) store_row<TPR, E>(p.dresidual, p.out_dtype, row, p.D, t, vec, d);
+#pragma unroll
+    for (int i = 0; i < E; ++i) d[i] *= p.scale;
+    if (p.gate) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const float n = p.w_after ? x[i] * ix * wa[i] : x[i];
+        const float s = sigmoid(z[i]);
+        const float slope = p.act == 0 ? s * fmaf(z[i], 1.f - s, 1.f) : s * (1.f - s);
+        const float a = p.act == 0 ? s * z[i] : s;
+        z[i] = d[i] * n * slope;
+        d[i] *= a;
+      }
+      if (p.dgate) store_row<TPR, E>(p.dgate, p.out_dtype, row, p.D, t, vec, z);
+    }
+    if (p.w_after) {
+      float dot = 0.f;
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        x[i] *= ix;
+        ga[i] = fmaf(d[i], x[i], ga[i]);
+        d[i] *= wa[i];
+        dot = fmaf(d[i], x[i], dot);
+      }
+      dot = row_sum<TPR>(dot, lds, slot) * inv_d;
+#pragma unroll
+      for (int i = 0; i < E; ++i) d[i] = ix * fmaf(-x[i], dot, d[i]);
+    }
+    store_row<TPR, E>(p.dx, p.out_dtype, row, p.D, t, vec, d);
+  }
+  // this workgroup's weight gradients: rows of one column added in order
+  __shared__ float cols[RPB > 1 ? THREADS * E : 1];
+  auto partial = [&](const float (&g)[E], float* to) {
+    if constexpr (RPB > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < E; ++i) cols[(sub * TPR + t) * E + i] = g[i];
+      __syncthreads();
+      for (int i = threadIdx.x; i < TPR * E; i += THREADS) {
+        float sum = 0.f;
+        for (int s = 0; s < RPB; ++s) sum += cols[s * TPR * E + i];
+        const int c = element<TPR>(i % E, i / E, vec);
+        if (c < p.D) to[static_cast<size_t>(blockIdx.x) * p.D + c] = sum;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const int c = element<TPR>(i, t, vec);
+        if (c < p.D) to[static_cast<size_t>(blockIdx.x) * p.D + c] = g[i];
+      }
+    }
+  };
+  if (p.part_after) partial(ga, p.part_after);
+  if (p.part_before) partial(gb, p.part_before);
+}
+
+// dw[c] = sum over the workgroups' rows of part[., c]: 32 columns a workgroup,
+// 8 threads to a column.
+__global__ __launch_bounds__(256) void block_norm_weights_kernel(const float* pa, const float* pb,
+                                                                 float* dwa, float* dwb, int parts,
+                                                                 int D) {
+  const float* part = blockIdx.y == 0 ? pa : pb;
+  float* dw = blockIdx.y == 0 ? dwa : dwb;
+  if (!dw) return;
+  __shared__ float lds[8][33];
+  const int cc = threadIdx.x & 31, rr = threadIdx.x >> 5, c = blockIdx.x * 32 + cc;
+  float sum = 0.f;
+  if (c < D)
+    for (int i = rr; i < parts; i += 8) sum += part[static_cast<size_t>(i) * D + c];
+  lds[rr][cc] = sum;
+  __syncthreads();
+  if (rr == 0 && c < D) {
+    sum = 0.f;
+    for (int i = 0; i < 8; ++i) sum += lds[i][cc];
+    dw[c] = sum;
+  }
+}
+
+// Calls go(TPR, E) for a row of D values.
+template <class F>
+hipError_t by_width(int D, F&& go) {
+  using std::integral_constant;
+#define GDR_WIDTH(most, tpr, e) \
+  if (D <= most) return go(integral_constant<int, tpr>(), integral_constant<int, e>())
+  GDR_WIDTH(64, 8, 8);
+  GDR_WIDTH(128, 16, 8);
+  GDR_WIDTH(256, 32, 8);
+  GDR_WIDTH(512, 64, 8);
+  GDR_WIDTH(1024, 64, 16);
+  GDR_WIDTH(2048, 256, 8);
+  GDR_WIDTH(4096, 256, 16);
+  GDR_WIDTH(8192, 1024, 8);
+  return go(integral_constant<int, 1024>(), integral_constant<int, 16>());
+#undef GDR_WIDTH
+}
+
+// Rows held at once by a workgroup of by_width's shape.
+int rows_per_block(int D) { return D <= 64 ? 32 : D <= 128 ? 16 : D <= 256 ? 8 : D <= 1024 ? 4 : 1; }
+
+}  // namespace
+
+int block_norm_backward_blocks(int64_t rows, int D) {
+  const int64_t rpb = rows_per_block(D), n = (rows + rpb - 1) / rpb;
+  return static_cast<int>(n < 512 ? n : 512);
+}
+
+hipError_t launch_block_norm(const BlockNorm& p, hipStream_t stream) {
+  const int64_t rpb = rows_per_block(p.D);
+  const dim3 grid(static_cast<unsigned>((p.rows + rpb - 1) / rpb));
+  return by_width(p.D, [&](auto tpr, auto e) {
+    constexpr int T = decltype(tpr)::value, E = decltype(e)::value;
+    const dim3 block(T > 256 ? T : 256);
+    if (p.in_dtype == 0)
+      hipLaunchKernelGGL((block_norm_kernel<Dt::BF16, T, E>), grid, block, 0, stream, p);
+    else
+      hipLaunchKernelGGL((block_norm_kernel<Dt::F32, T, E>), grid, block, 0, stream, p);
+    return hipGetLastError();
+  });
+}
+
+hipError_t launch_block_norm_backward(const BlockNorm& p, float* dw_after, float* dw_before,
+                                      hipStream_t stream) {
+  const int blocks = block_norm_backward_blocks(p.rows, p.D);
+  if (blocks > 0) {
+    const hipError_t e = by_width(p.D, [&](auto tpr, auto el) {
+      constexpr int T = decltype(tpr)::value, E = decltype(el)::value;
+      const dim3 block(T > 256 ? T : 256);
+      if (p.in_dtype == 0)
+        hipLaunchKernelGGL((block_norm_backward_kernel<Dt::BF16, T, E>), dim3(blocks), block, 0,
+                           stream, p);
+      else
+        hipLaunchKernelGGL((block_norm_backward_kernel<Dt::F32, T, E>), dim3(blocks), block, 0,
+                           stream, p);
+      return hipGetLastError();
+    });
+    if (e != hipSuccess) return e;
+  }
+  if (!dw_after && !dw_before) return hipSuccess;
+  hipLaunchKernelGGL(block_norm_weights_kernel, dim3((p.D + 31) / 32, 2), dim3(256), 0, stream,
+                     p.part_after, p.part_before, dw_after, dw_before, blocks, p.D);
+  return hipGetLastError();
+}
+
+}  // namespace gdr

@@ -392,6 +392,67 @@ gdr_status gdr_linear_backward(const void* q, const void* k, const void* v, cons
 size_t gdr_linear_backward_workspace_bytes(int T_total, int N, int H, int Hk, int dk, int dv,
                                            gdr_dtype in_dtype);
 
+/*
+ * gdr_block_norm -- the norms around a block, fused with its gate and its
+ * scaled residual.  Per row of D values, with rms(a) = sqrt(mean(a^2) + eps):
+ *
+ *     u = x / rms(x) * w_after            (x itself without w_after)
+ *     u = u * act(gate)                   (where gate is given)
+ *     h = residual + scale * u            (scale * u without residual)
+ *     y = h / rms(h) * w_before           (where w_before is given)
+ *
+ * w_after is the norm after the block that produced x (for the outputs o of
+ * the recurrences: rows = tokens * heads, D = dv), w_before the norm before
+ * the next block.  All arithmetic is fp32 and y comes from the unrounded h.
+ * A row of zeros gives zeros (eps > 0 keeps rms above zero; eps = 0 is the
+ * caller's choice).
+ *
+ *   x, gate, residual  [rows, D]   in_dtype; gate and residual may be NULL
+ *   w_after, w_before  [D]         w_dtype; may be NULL
+ *   h, y               [rows, D]   out_dtype; h may be NULL where y is given;
+ *                                  y is given exactly when w_before is.  h or y
+ *                                  may be the buffer of x, gate or residual when
+ *                                  the dtypes agree (not both the same one)
+ *   act                GDR_GATE_SILU: z sigmoid(z), GDR_GATE_SIGMOID: sigmoid(z)
+ *   rows >= 0, 1 <= D <= 16384; rows * D may pass 2^31
+ * For D a multiple of 8 every row is read with 16-byte loads; other D take
+ * single-element accesses.
+ */
+typedef enum { GDR_GATE_SILU = 0, GDR_GATE_SIGMOID = 1 } gdr_gate;
+
+gdr_status gdr_block_norm(const void* x, const void* w_after, const void* gate,
+                          const void* residual, const void* w_before, void* h, void* y,
+                          int64_t rows, int D, float scale, float eps, gdr_gate act,
+                          gdr_dtype in_dtype, gdr_dtype w_dtype, gdr_dtype out_dtype,
+                          gdr_stream_t stream);
+
+/*
+ * gdr_block_norm_backward -- gradients of gdr_block_norm.
+ *
+ *   x, w_after, gate, residual, w_before   as given to gdr_block_norm (residual
+ *                is read only with w_before, where h is formed again)
+ *   dh           [rows, D]  in_dtype: gradient of h, or NULL for zero
+ *   dy           [rows, D]  in_dtype: gradient of y, given exactly when w_before is
+ *   dx           [rows, D]  out_dtype
+ *   dgate        [rows, D]  out_dtype; NULL: not written
+ *   dresidual    [rows, D]  out_dtype; NULL: not written
+ *   dw_after, dw_before  [D] fp32, sums over all rows; NULL: not written
+ *   workspace    gdr_block_norm_backward_workspace_bytes(rows, D) bytes (needed
+ *                only when a dw is asked for): the sums of single workgroups,
+ *                added in a fixed order by a second kernel (deterministic)
+ * No output may overlap an input or another output.
+ */
+gdr_status gdr_block_norm_backward(const void* x, const void* w_after, const void* gate,
+                                   const void* residual, const void* w_before, const void* dh,
+                                   const void* dy, void* dx, void* dgate, void* dresidual,
+                                   float* dw_after, float* dw_before, int64_t rows, int D,
+                                   float scale, float eps, gdr_gate act, gdr_dtype in_dtype,
+                                   gdr_dtype w_dtype, gdr_dtype out_dtype, void* workspace,
+                                   size_t workspace_bytes, gdr_stream_t stream);
+
+/* Device workspace of gdr_block_norm_backward; 0 also on bad arguments. */
+size_t gdr_block_norm_backward_workspace_bytes(int64_t rows, int D);
+
 /* Static text for a status code. */
 const char* gdr_status_string(gdr_status s);
 
