@@ -165,7 +165,7 @@ struct LinearPass {
   LinearRows x, y, w;
   LinearRows e;        // rows of od values to dot with the outputs (dot != NULL)
   void* out;           // [T, H, od]
-  float* dot;          // [od / 16][T * H] partial sums of e_t . out_t without the
+  float* dot;          // [od / 16][H][T] partial sums of e_t . out_t without the
                        // token's own term, or NULL
   const float* start;  // states the walk starts from, NULL for zero
   float* end;          // states at the end of the walk, NULL: not written
@@ -191,7 +191,7 @@ hipError_t launch_linear_decode(const void* q, const void* k, const void* v,
 hipError_t launch_linear_pass(const LinearBatch& b, const LinearPass& p, hipStream_t stream);
 
 // dg_t = dg_{t+1} + row_t - col_t, starting from the end's dot product; row and
-// col are [parts][T * H] partial sums, end_dot [parts][N * H].
+// col are [parts][H][T] partial sums, end_dot [parts][N * H].
 hipError_t launch_linear_dg(const LinearBatch& b, const float* row, int row_parts,
                             const float* col, int col_parts, const float* end_dot, int end_parts,
                             float* dg, hipStream_t stream);

@@ -1,93 +1,493 @@
-// linear.hip -- linear attention with a decay for each head on gfx950.
+// linear.hip -- linear attention with a decay for each head on gfx950: prompts
+// and gradients in chunks of tokens on the matrix cores, single tokens as a
+// stream.
 //
-// One kernel computes a pass of the recurrence (launch.h, LinearPass) token by
-// token: a 256-thread workgroup holds 16 state rows of one (sequence, head),
-// 16 lanes to a row, and walks the sequence's tokens.
-#include "gdr_device.h"
+// A pass of the recurrence (launch.h, LinearPass) over one chunk, with G_t the
+// prefix sums of the chunk's gates, C its last token and Z the state before it:
+//   out_t = os ( sum_{s <= t} e^{G_t - G_s} us (x_t . y_s) w_s + e^{G_t} Z x_t )
+//   Z    <- e^{G_C} Z + us sum_s e^{G_C - G_s} w_s y_s^T
+// and walking backwards, with Z the state behind the chunk,
+//   out_t = os ( sum_{s >= t} e^{G_s - G_t} us (x_t . y_s) w_s + e^{G_C - G_t} Z x_t )
+//   Z    <- e^{G_C} Z + us sum_s e^{G_s} w_s y_s^T.
+// All exponents are <= 0 for g <= 0.
+#include <type_traits>
+
 #include "launch.h"
+#include "mfma_planes.h"
 
 namespace gdr {
 namespace {
 
 constexpr float kMinGate = -110.f;  // e^-110 is zero in fp32: stands for every smaller g
+constexpr int kXcds = 8;
+constexpr int kCopyWaves = 4;
 
-__device__ __forceinline__ float load_gate(const LinearGates& g, size_t t, int h, int H) {
-  const float x = g.per_token ? g.g[t * H + h] : g.g[h];
-  return x < kMinGate ? kMinGate : x;
-}
+__device__ __forceinline__ float clamp_gate(float g) { return g < kMinGate ? kMinGate : g; }
 
-template <Dt IN>
-__global__ __launch_bounds__(256) void linear_walk_kernel(LinearBatch b, LinearPass p) {
-  const int blocks = p.od / 16;
-  const int rb = blockIdx.x % blocks, nh = blockIdx.x / blocks;
-  const int n = nh / b.H, h = nh % b.H;
-  const int lane16 = threadIdx.x & 15, rr = threadIdx.x >> 4, row = 16 * rb + rr;
-  const int cpl = p.kd / 16;  // 4 or 8 columns a lane
-  int tb = b.cu[n], te = b.cu[n + 1];
+__device__ __forceinline__ void token_range(const LinearBatch& b, int n, int& tb, int& te) {
+  tb = b.cu[n];
+  te = b.cu[n + 1];
   tb = tb < 0 ? 0 : (tb > b.T_total ? b.T_total : tb);
   te = te < tb ? tb : (te > b.T_total ? b.T_total : te);
-  const size_t sbase = static_cast<size_t>(nh) * p.od * p.kd + row * p.row;
-  float z[8];
+}
+
+// ---- operands
+//
+// A fragment is eight elements of the contraction index for one row or column
+// (lane (c, g) = (lane % 16, lane / 16)): one bf16x8 for bf16 inputs, eight
+// floats for fp32 ones, multiplied by one 16x16x32 bf16 product or eight
+// 16x16x4 fp32 products.  fp32 values beside bf16 inputs (P, the state, the
+// decayed w) are PL bf16 planes.
+struct F32x8 {
+  float v[8];
+};
+template <Dt IN>
+struct FragOf { using type = bf16x8; };
+template <>
+struct FragOf<Dt::F32> { using type = F32x8; };
+template <Dt IN>
+using Frag = typename FragOf<IN>::type;
+
+template <Dt IN, int PL>
+struct Planes {
+  static constexpr int N = IN == Dt::F32 ? 1 : PL;
+  Frag<IN> p[N];
+};
+
+__device__ __forceinline__ floatx4 mma(const bf16x8& a, const bf16x8& b, floatx4 acc) {
+  return mfma16x16x32(a, b, acc);
+}
+__device__ __forceinline__ floatx4 mma(const F32x8& a, const F32x8& b, floatx4 acc) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    z[i] = i < cpl && p.start ? p.start[sbase + (lane16 + 16 * i) * p.col] : 0.f;
-  __shared__ float part[16];
-  for (int s = 0; s < te - tb; ++s) {
-    const size_t t = p.backward ? te - 1 - s : tb + s;
-    const size_t xi = t * p.x.stride + static_cast<size_t>(h / p.x.group) * p.kd + lane16;
-    const size_t yi = t * p.y.stride + static_cast<size_t>(h / p.y.group) * p.kd + lane16;
-    const float w = load_scalar<IN>(p.w.p, t * p.w.stride +
-                                               static_cast<size_t>(h / p.w.group) * p.od + row);
-    const float alpha = expf(load_gate(b.gates, t, h, b.H));
-    float before = 0.f, own = 0.f;
+  for (int i = 0; i < 8; ++i) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[i], b.v[i], acc, 0, 0, 0);
+  return acc;
+}
+// Products of a planes operand, smallest plane first.
+template <Dt IN, int PL>
+__device__ __forceinline__ floatx4 mma(const Planes<IN, PL>& a, const Frag<IN>& b, floatx4 acc) {
+#pragma unroll
+  for (int i = Planes<IN, PL>::N - 1; i >= 0; --i) acc = mma(a.p[i], b, acc);
+  return acc;
+}
+template <Dt IN, int PL>
+__device__ __forceinline__ floatx4 mma(const Frag<IN>& a, const Planes<IN, PL>& b, floatx4 acc) {
+#pragma unroll
+  for (int i = Planes<IN, PL>::N - 1; i >= 0; --i) acc = mma(a, b.p[i], acc);
+  return acc;
+}
+template <Dt IN, int PL>
+__device__ __forceinline__ Planes<IN, PL> to_planes(const float (&x)[8]) {
+  Planes<IN, PL> r;
+  if constexpr (IN == Dt::F32) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.p[0].v[i] = x[i];
+  } else {
+    split8<PL>(x, r.p);
+  }
+  return r;
+}
+
+// ---- tiles in LDS
+//
+// Rows of CH 16-byte pieces; piece i of row r lies at i ^ perm(r).  perm gives
+// the 16 rows of a row fragment distinct 16-byte banks, and the four rows of a
+// transposing read distinct groups of four pieces.
+template <int CH>
+__device__ __forceinline__ int perm(int r) {
+  if constexpr (CH >= 16) return ((r & 3) << 2) | ((r >> 2) & 3);
+  else return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+}
+
+// Row fragment: elements 32 kb + 8 g .. + 7 of row r.
+template <Dt IN, int CH>
+__device__ __forceinline__ Frag<IN> row_frag(const unsigned char* tile, int r, int kb, int g) {
+  const unsigned char* row = tile + r * CH * 16;
+  if constexpr (IN == Dt::BF16) {
+    return *reinterpret_cast<const bf16x8*>(row + 16 * ((4 * kb + g) ^ perm<CH>(r)));
+  } else {
+    const int i = 8 * kb + 2 * g;
+    const floatx4 a = *reinterpret_cast<const floatx4*>(row + 16 * (i ^ perm<CH>(r)));
+    const floatx4 b = *reinterpret_cast<const floatx4*>(row + 16 * ((i + 1) ^ perm<CH>(r)));
+    return {{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
+  }
+}
+
+// Column fragment of the 32 rows r0 ..: rows r0 + 4g + e in slots e and r0 + 16 + 4g + e in
+// slots 4 + e (the order in which two stacked output tiles present their rows), of column
+// col + c (WIDE = false) or col + 8 (c / 4) + c % 4 (WIDE; col a multiple of 4).
+template <Dt IN, int CH, bool WIDE>
+__device__ __forceinline__ Frag<IN> col_frag(const unsigned char* tile, int r0, int col, int c, int g) {
+  if constexpr (IN == Dt::BF16) {
+    // ds_read_b64_tr_b16: element e of lane c comes from input lane 4e + c/4, element c % 4
+    const int at = col + (WIDE ? 8 : 4) * (c & 3);
+    shortx4 h[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = r0 + 16 * i + 4 * g + (c >> 2);
+      const unsigned char* p = tile + r * CH * 16 + 16 * ((at >> 3) ^ perm<CH>(r)) + 2 * (at & 7);
+      h[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) shortx4*)p);
+    }
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+  } else {
+    const int at = col + (WIDE ? 8 * (c >> 2) + (c & 3) : c);
+    F32x8 f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if (i >= cpl) continue;
-      const float xv = load_scalar<IN>(p.x.p, xi + 16 * i);
-      const float yv = load_scalar<IN>(p.y.p, yi + 16 * i);
-      if (!p.backward) z[i] *= alpha;
-      before = fmaf(z[i], xv, before);
-      const float add = p.us * w * yv;
-      own = fmaf(add, xv, own);
-      z[i] += add;
-      if (p.backward) z[i] *= alpha;
+      const int r = r0 + 16 * (i >> 2) + 4 * g + (i & 3);
+      f.v[i] = *reinterpret_cast<const float*>(tile + r * CH * 16 + 16 * ((at >> 2) ^ perm<CH>(r)) +
+                                               4 * (at & 3));
     }
-    before = row16_sum(before) * p.os;
-    own = row16_sum(own) * p.os;
-    const size_t oi = (t * b.H + h) * p.od + row;
-    if (lane16 == 0) {
-      if (p.out_dtype == 0) store_scalar<Dt::BF16>(p.out, oi, before + own);
-      else store_scalar<Dt::F32>(p.out, oi, before + own);
-    }
-    if (p.dot) {
-      if (lane16 == 0)
-        part[rr] = before * load_scalar<IN>(p.e.p, t * p.e.stride +
-                                                       static_cast<size_t>(h / p.e.group) * p.od + row);
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        float sum = 0.f;
-        for (int i = 0; i < 16; ++i) sum += part[i];
-        p.dot[static_cast<size_t>(rb) * b.T_total * b.H + t * b.H + h] = sum;
-      }
-      __syncthreads();
-    }
+    return f;
   }
+}
+
+// Four elements col .. col + 3 of row r, widened (col a multiple of 4).
+template <Dt IN, int CH>
+__device__ __forceinline__ floatx4 row4(const unsigned char* tile, int r, int col) {
+  const unsigned char* row = tile + r * CH * 16;
+  if constexpr (IN == Dt::BF16) {
+    const uint2 u = *reinterpret_cast<const uint2*>(row + 16 * ((col >> 3) ^ perm<CH>(r)) + 2 * (col & 7));
+    return floatx4{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                   __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u)};
+  } else {
+    return *reinterpret_cast<const floatx4*>(row + 16 * ((col >> 2) ^ perm<CH>(r)));
+  }
+}
+
+__device__ __forceinline__ float frag_value(const bf16x8& f, int i) { return static_cast<float>(f[i]); }
+__device__ __forceinline__ float frag_value(const F32x8& f, int i) { return f.v[i]; }
+
+// Workgroup barriers.  The copy waves wait for their own loads; the compute
+// waves wait for their LDS accesses only (their global stores stay in flight).
+__device__ __forceinline__ void bare_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+__device__ __forceinline__ void copy16(const void* src, void* lds) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(src),
+                                   (__attribute__((address_space(3))) void*)(lds), 16, 0, 0);
+}
+
+// ---- the chunk scan
+//
+// One workgroup per (unit, head, 16 W columns of w): a unit is a sequence, or a
+// segment of one.  W compute waves hold 16 state rows each, for the whole walk,
+// as output tiles of the state update: lane (c, g) holds Z[c][32 j + 8 g + 0..7],
+// which is also the fragment of Z in the product with x.  The scores x.y of a
+// chunk are formed once a workgroup, a few 16 x 16 tiles a wave, and shared
+// through LDS as P^T fragments; everything else stays in the wave's registers.
+// kCopyWaves more waves copy the next chunk's x, y, w rows to the other LDS
+// buffer (global-to-LDS loads) and form its gate factors.  Two barriers a
+// chunk: P is complete; the chunk is done.
+template <Dt IN, int KD, int W>
+struct ScanCfg {
+  static constexpr int ES = IN == Dt::BF16 ? 2 : 4;
+  static constexpr int C = IN == Dt::BF16 ? 64 : 32;  // tokens a chunk (fp32: half, for LDS)
+  static constexpr int NT = C / 16, NB = C / 32;
+  static constexpr int KB = KD / 32;          // 32-deep blocks over kd
+  static constexpr int VS = 16 * W;           // columns of w a workgroup
+  static constexpr int CHK = KD * ES / 16, CHV = VS * ES / 16;
+  static constexpr int X_BYTES = C * KD * ES, W_BYTES = C * VS * ES;
+  static constexpr int OFF_X = 0, OFF_Y = X_BYTES, OFF_W = 2 * X_BYTES;
+  static constexpr int BUF = 2 * X_BYTES + W_BYTES;
+  // gate factors of a chunk: G in log2 units as a sum of two floats, the
+  // factors of Z x_t and of the update, e^{G_C}
+  static constexpr int GATE_BYTES = (4 * C + 4) * 4;
+  static constexpr int OFF_G = 2 * BUF;
+  // P^T fragments (row tile, 32-deep block) and the scores of a token with itself
+  static constexpr int FRAG = IN == Dt::BF16 ? 1024 : 2048;
+  static constexpr int TILES = NT * (NT + 1) / 2;
+};
+
+template <Dt IN, int KD, int W, int PZ>
+struct ScanLds {
+  using Cfg = ScanCfg<IN, KD, W>;
+  static constexpr int PL = IN == Dt::F32 ? 1 : PZ;
+  static constexpr int OFF_P = Cfg::OFF_G + 2 * Cfg::GATE_BYTES;
+  static constexpr int OFF_DIAG = OFF_P + Cfg::NT * Cfg::NB * PL * Cfg::FRAG;
+  static constexpr int BYTES = OFF_DIAG + Cfg::C * 4;
+  static_assert(BYTES <= 160 * 1024, "LDS");
+};
+
+template <Dt IN, int KD, int W, int PZ, bool DOT>
+__global__ __launch_bounds__(64 * (W + kCopyWaves)) void linear_scan_kernel(LinearBatch b, LinearPass p) {
+  using Cfg = ScanCfg<IN, KD, W>;
+  using Lds = ScanLds<IN, KD, W, PZ>;
+  constexpr int C = Cfg::C, NT = Cfg::NT, NB = Cfg::NB, KB = Cfg::KB, ES = Cfg::ES, PL = Lds::PL;
+  __shared__ __align__(1024) unsigned char lds[Lds::BYTES];
+  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // the workgroups of one (unit, head) read the same x and y rows: one XCD
+  const int slices = p.od / Cfg::VS, xcd = blockIdx.x % kXcds, k0 = blockIdx.x / kXcds;
+  const int slice = k0 % slices, pair = (k0 / slices) * kXcds + xcd;
+  if (pair >= b.N * b.H) return;
+  const int n = pair / b.H, h = pair % b.H;
+  int tb, te;
+  token_range(b, n, tb, te);
+  const int chunks = (te - tb + C - 1) / C;
+
+  if (wave >= W) {  // ---- copy waves
+    if (chunks == 0) return;
+    const int cw = wave - W;
+    auto rows = [&](const LinearRows& r, int width, int skip) {
+      return static_cast<const char*>(r.p) + (static_cast<size_t>(h / r.group) * width + skip) * ES;
+    };
+    const char* xs = rows(p.x, KD, 0);
+    const char* ys = rows(p.y, KD, 0);
+    const char* ws = rows(p.w, p.od, slice * Cfg::VS);
+    const size_t xst = p.x.stride * ES, yst = p.y.stride * ES, wst = p.w.stride * ES;
+    // Rows past the end of a short chunk repeat its last token: nothing outside
+    // the sequence is read, and their factors are zero.
+    auto chunk_at = [&](int s, int& tok) {
+      tok = tb + (p.backward ? chunks - 1 - s : s) * C;
+      return te - tok < C ? te - tok : C;
+    };
+    float gate = 0.f;
+    auto load_gate = [&](int s) {
+      int tok;
+      const int len = chunk_at(s, tok);
+      if (cw != 0) return;
+      if (!b.gates.per_token) gate = b.gates.g[h];
+      else if (lane < len) gate = b.gates.g[static_cast<size_t>(tok + lane) * b.H + h];
+    };
+    auto copy_chunk = [&](int s) {
+      int tok;
+      const int len = chunk_at(s, tok);
+      unsigned char* buf = lds + (s & 1) * Cfg::BUF;
+      auto tile = [&](const char* src, size_t stride, unsigned char* to, auto ch) {
+        constexpr int CH = decltype(ch)::value;
+        const char* base = src + static_cast<size_t>(tok) * stride;
+#pragma unroll
+        for (int i = 0; i < C * CH / 64 / kCopyWaves; ++i) {
+          const int q = 64 * (cw + kCopyWaves * i) + lane, r = q / CH, pc = q % CH;
+          const int rr = r < len ? r : len - 1;
+          copy16(base + rr * stride + 16 * (pc ^ perm<CH>(r)), to + 1024 * (cw + kCopyWaves * i));
+        }
+      };
+      tile(xs, xst, buf + Cfg::OFF_X, std::integral_constant<int, Cfg::CHK>());
+      tile(ys, yst, buf + Cfg::OFF_Y, std::integral_constant<int, Cfg::CHK>());
+      tile(ws, wst, buf + Cfg::OFF_W, std::integral_constant<int, Cfg::CHV>());
+    };
+    // Prefix sums in fp64, so that a decay's error does not grow with |G|.
+    auto put_gates = [&](int s) {
+      if (cw != 0) return;
+      int tok;
+      const int len = chunk_at(s, tok);
+      double G;
+      if (b.gates.per_token) {
+        G = lane < len ? static_cast<double>(clamp_gate(gate)) : 0.0;
+#pragma unroll
+        for (int d = 1; d < C; d <<= 1) {
+          const double up = __shfl_up(G, d);
+          if (lane >= d) G += up;
+        }
+      } else {
+        G = static_cast<double>(clamp_gate(gate)) * (lane < len ? lane + 1 : len);
+      }
+      G *= 1.4426950408889634;
+      const double end = __shfl(G, C - 1);
+      float* f = reinterpret_cast<float*>(lds + Cfg::OFF_G + (s & 1) * Cfg::GATE_BYTES);
+      if (lane < C) {
+        const float hi = static_cast<float>(G), lo = static_cast<float>(G - hi);
+        const float from = exp2f(hi) * fmaf(lo, 0.69314718f, 1.f);
+        const double rest = end - G;
+        const float to = exp2f(static_cast<float>(rest));
+        f[lane] = hi;
+        f[C + lane] = lo;
+        f[2 * C + lane] = p.os * (p.backward ? to : from);
+        f[3 * C + lane] = lane < len ? p.us * (p.backward ? from : to) : 0.f;
+        if (lane == 0) f[4 * C] = exp2f(static_cast<float>(end));
+      }
+    };
+    load_gate(0);
+    copy_chunk(0);
+    put_gates(0);
+    __builtin_amdgcn_s_waitcnt(0);
+    bare_barrier();
+    for (int s = 0; s < chunks; ++s) {
+      if (s + 1 < chunks) {
+        load_gate(s + 1);
+        copy_chunk(s + 1);
+      }
+      bare_barrier();
+      if (s + 1 < chunks) put_gates(s + 1);
+      __builtin_amdgcn_s_waitcnt(0);
+      bare_barrier();
+    }
+    return;
+  }
+
+  // ---- compute waves
+  const int od = slice * Cfg::VS + 16 * wave;  // this wave's columns of w
+  const size_t zbase = static_cast<size_t>(pair) * p.od * KD + (od + c) * p.row;
+  floatx4 z[KD / 16];  // z[2 j + i][e] = Z[od + c][32 j + 8 g + 4 i + e]
+#pragma unroll
+  for (int j = 0; j < KD / 16; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int k = 32 * (j >> 1) + 8 * g + 4 * (j & 1) + e;
+      z[j][e] = p.start ? p.start[zbase + k * p.col] : 0.f;
+    }
+  if (chunks > 0) {
+    // fragment halves above the diagonal stay zero
+    for (int i = threadIdx.x; i < (Lds::OFF_DIAG - Lds::OFF_P) / 16; i += 64 * W)
+      *reinterpret_cast<uint4*>(lds + Lds::OFF_P + 16 * i) = make_uint4(0, 0, 0, 0);
+    lds_barrier();
+  }
+  for (int s = 0; s < chunks; ++s) {
+    const int tok = tb + (p.backward ? chunks - 1 - s : s) * C;
+    const int len = te - tok < C ? te - tok : C;
+    const unsigned char* buf = lds + (s & 1) * Cfg::BUF;
+    const unsigned char *X = buf + Cfg::OFF_X, *Y = buf + Cfg::OFF_Y, *Wt = buf + Cfg::OFF_W;
+    const float* gate = reinterpret_cast<const float*>(lds + Cfg::OFF_G + (s & 1) * Cfg::GATE_BYTES);
+    float* diag = reinterpret_cast<float*>(lds + Lds::OFF_DIAG);
+
+    // P^T tiles (columns t of row tile tt, rows s of tile st), W of them at a time
+    const float ps = p.us * p.os;
+    for (int i = wave; i < Cfg::TILES; i += W) {
+      int tt = 0, st = i;  // i-th pair st <= tt (forward), or its mirror (backward)
+      while (st > tt) { st -= tt + 1; ++tt; }
+      if (p.backward) { tt = NT - 1 - tt; st = NT - 1 - st; }
+      floatx4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
+        acc = mma(row_frag<IN, Cfg::CHK>(Y, 16 * st + c, kb, g),
+                  row_frag<IN, Cfg::CHK>(X, 16 * tt + c, kb, g), acc);
+      const int t = 16 * tt + c, s4 = 16 * st + 4 * g;
+      const float gh = gate[t], gl = gate[C + t];
+      const floatx4 sh = *reinterpret_cast<const floatx4*>(gate + s4);
+      const floatx4 sl = *reinterpret_cast<const floatx4*>(gate + C + s4);
+      float v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float d = (gh - sh[e]) + (gl - sl[e]);
+        const float x = acc[e] * ps * __builtin_amdgcn_exp2f(p.backward ? -d : d);
+        const int sc = s4 + e;
+        if (DOT && sc == t) diag[t] = x;
+        const bool in = p.backward ? (DOT ? sc > t : sc >= t) && sc < len : (DOT ? sc < t : sc <= t);
+        v[e] = in ? x : 0.f;
+      }
+      unsigned char* to = lds + Lds::OFF_P + (tt * NB + (st >> 1)) * PL * Cfg::FRAG;
+      if constexpr (IN == Dt::F32) {
+        *reinterpret_cast<floatx4*>(to + lane * 32 + 16 * (st & 1)) = floatx4{v[0], v[1], v[2], v[3]};
+      } else {
+        uint32_t lo[PL], hi[PL];
+        split2<PL>(v[0], v[1], lo);
+        split2<PL>(v[2], v[3], hi);
+#pragma unroll
+        for (int q = 0; q < PL; ++q)
+          *reinterpret_cast<uint2*>(to + q * Cfg::FRAG + lane * 16 + 8 * (st & 1)) = make_uint2(lo[q], hi[q]);
+      }
+    }
+
+    // out^T = Z x^T, rows od, columns t
+    floatx4 o[NT];
+#pragma unroll
+    for (int tt = 0; tt < NT; ++tt) o[tt] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      const float zz[8] = {z[2 * kb][0], z[2 * kb][1], z[2 * kb][2], z[2 * kb][3],
+                           z[2 * kb + 1][0], z[2 * kb + 1][1], z[2 * kb + 1][2], z[2 * kb + 1][3]};
+      const Planes<IN, PZ> zp = to_planes<IN, PZ>(zz);
+#pragma unroll
+      for (int tt = 0; tt < NT; ++tt)
+        o[tt] = mma(zp, row_frag<IN, Cfg::CHK>(X, 16 * tt + c, kb, g), o[tt]);
+    }
+#pragma unroll
+    for (int tt = 0; tt < NT; ++tt) o[tt] *= gate[2 * C + 16 * tt + c];
+
+    Frag<IN> wf[NB];
+#pragma unroll
+    for (int sb = 0; sb < NB; ++sb) wf[sb] = col_frag<IN, Cfg::CHV, false>(Wt, 32 * sb, 16 * wave, c, g);
+    lds_barrier();  // P is complete
+
+#pragma unroll
+    for (int tt = 0; tt < NT; ++tt) {
+#pragma unroll
+      for (int sb = 0; sb < NB; ++sb) {
+        if (p.backward ? sb < (tt >> 1) : sb > (tt >> 1)) continue;
+        const unsigned char* from = lds + Lds::OFF_P + (tt * NB + sb) * PL * Cfg::FRAG;
+        Planes<IN, PZ> pp;
+        if constexpr (IN == Dt::F32) {
+          const floatx4 a = *reinterpret_cast<const floatx4*>(from + lane * 32);
+          const floatx4 d = *reinterpret_cast<const floatx4*>(from + lane * 32 + 16);
+          pp.p[0] = {{a[0], a[1], a[2], a[3], d[0], d[1], d[2], d[3]}};
+        } else {
+#pragma unroll
+          for (int q = 0; q < PL; ++q) pp.p[q] = *reinterpret_cast<const bf16x8*>(from + q * Cfg::FRAG + lane * 16);
+        }
+        o[tt] = mma(wf[sb], pp, o[tt]);
+      }
+      const int t = 16 * tt + c;
+      const bool live = t < len;
+      const size_t th = static_cast<size_t>(tok + t) * b.H + h;
+      if constexpr (DOT) {
+        float dot = 0.f;
+        if (live) {
+          const size_t ei = static_cast<size_t>(tok + t) * p.e.stride +
+                            static_cast<size_t>(h / p.e.group) * p.od + od + 4 * g;
+          float ev[4];
+          load_vec<IN, 4>(p.e.p, ei, ev);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) dot = fmaf(ev[e], o[tt][e], dot);
+        }
+        dot += __shfl_xor(dot, 16);
+        dot += __shfl_xor(dot, 32);
+        if (live && g == 0)
+          p.dot[(static_cast<size_t>(od / 16) * b.H + h) * b.T_total + tok + t] = dot;
+        const floatx4 own = row4<IN, Cfg::CHV>(Wt, t, 16 * wave + 4 * g);
+        o[tt] += diag[t] * own;
+      }
+      if (live) {
+        const size_t oi = th * p.od + od + 4 * g;
+        if (p.out_dtype == 0) {
+          uint32_t lo[1], hi[1];
+          split2<1>(o[tt][0], o[tt][1], lo);
+          split2<1>(o[tt][2], o[tt][3], hi);
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + oi) = make_uint2(lo[0], hi[0]);
+        } else {
+          *reinterpret_cast<floatx4*>(static_cast<float*>(p.out) + oi) = o[tt];
+        }
+      }
+    }
+
+    // Z <- e^{G_C} Z + (update factors . w)^T y
+    const float gc = gate[4 * C];
+#pragma unroll
+    for (int j = 0; j < KD / 16; ++j) z[j] *= gc;
+#pragma unroll
+    for (int sb = 0; sb < NB; ++sb) {
+      const floatx4 f0 = *reinterpret_cast<const floatx4*>(gate + 3 * C + 32 * sb + 4 * g);
+      const floatx4 f1 = *reinterpret_cast<const floatx4*>(gate + 3 * C + 32 * sb + 16 + 4 * g);
+      float u[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        u[e] = frag_value(wf[sb], e) * f0[e];
+        u[4 + e] = frag_value(wf[sb], 4 + e) * f1[e];
+      }
+      const Planes<IN, 3> up = to_planes<IN, 3>(u);
+#pragma unroll
+      for (int j = 0; j < KD / 16; ++j)
+        z[j] = mma(col_frag<IN, Cfg::CHK, true>(Y, 32 * sb, 32 * (j >> 1) + 4 * (j & 1), c, g), up, z[j]);
+    }
+    lds_barrier();  // the chunk is done
+  }
+
   float ed = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (i >= cpl) continue;
-    if (p.end) p.end[sbase + (lane16 + 16 * i) * p.col] = z[i];
-    if (p.end_with) ed = fmaf(z[i], p.end_with[sbase + (lane16 + 16 * i) * p.col], ed);
-  }
-  if (p.end_with) {
-    ed = row16_sum(ed);
-    if (lane16 == 0) part[rr] = ed;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      float sum = 0.f;
-      for (int i = 0; i < 16; ++i) sum += part[i];
-      p.end_dot[static_cast<size_t>(rb) * b.N * b.H + nh] = sum;
+  for (int j = 0; j < KD / 16; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const size_t at = zbase + (32 * (j >> 1) + 8 * g + 4 * (j & 1) + e) * p.col;
+      if (p.end_with) ed = fmaf(z[j][e], p.end_with[at], ed);
+      if (p.end) p.end[at] = z[j][e];
     }
+  if (p.end_with) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) ed += __shfl_xor(ed, d);
+    if (lane == 0) p.end_dot[static_cast<size_t>(od / 16) * b.N * b.H + pair] = ed;
   }
 }
 
@@ -98,20 +498,19 @@ __global__ __launch_bounds__(64) void linear_dg_kernel(LinearBatch b, const floa
   const int nh = blockIdx.x * 64 + threadIdx.x;
   if (nh >= b.N * b.H) return;
   const int n = nh / b.H, h = nh % b.H;
-  int tb = b.cu[n], te = b.cu[n + 1];
-  tb = tb < 0 ? 0 : (tb > b.T_total ? b.T_total : tb);
-  te = te < tb ? tb : (te > b.T_total ? b.T_total : te);
+  int tb, te;
+  token_range(b, n, tb, te);
   const size_t th = static_cast<size_t>(b.T_total) * b.H;
-  float acc = 0.f;
+  double acc = 0.;
   if (end_dot)
     for (int i = 0; i < end_parts; ++i) acc += end_dot[static_cast<size_t>(i) * b.N * b.H + nh];
   for (int t = te - 1; t >= tb; --t) {
-    const size_t at = static_cast<size_t>(t) * b.H + h;
+    const size_t at = static_cast<size_t>(h) * b.T_total + t;
     float r = 0.f, c = 0.f;
     for (int i = 0; i < row_parts; ++i) r += row[i * th + at];
     for (int i = 0; i < col_parts; ++i) c += col[i * th + at];
     acc += r - c;
-    dg[at] = acc;
+    dg[static_cast<size_t>(t) * b.H + h] = static_cast<float>(acc);
   }
 }
 
@@ -162,7 +561,7 @@ __global__ __launch_bounds__(256) void linear_decode_kernel(
   const int rb = blockIdx.x % blocks, nh = blockIdx.x / blocks;
   const int n = nh / H, h = nh % H;
   const int lane16 = threadIdx.x & 15, row = 16 * rb + (threadIdx.x >> 4);
-  const float alpha = expf(load_gate(g, n, h, H));
+  const float alpha = expf(clamp_gate(g.per_token ? g.g[nh] : g.g[h]));
   const float vv = load_scalar<IN>(v, n * vs + static_cast<size_t>(h) * dv + row);
   float* s = state + (static_cast<size_t>(nh) * dv + row) * dk + lane16;
   float acc = 0.f;
@@ -196,12 +595,25 @@ hipError_t launch_linear_decode(const void* q, const void* k, const void* v,
 }
 
 hipError_t launch_linear_pass(const LinearBatch& b, const LinearPass& p, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(b.N) * b.H * (p.od / 16));
-  if (b.in_dtype == 0)
-    hipLaunchKernelGGL(linear_walk_kernel<Dt::BF16>, grid, dim3(256), 0, stream, b, p);
-  else
-    hipLaunchKernelGGL(linear_walk_kernel<Dt::F32>, grid, dim3(256), 0, stream, b, p);
-  return hipGetLastError();
+  auto go = [&](auto in, auto kd, auto w, auto dot) {
+    constexpr Dt IN = decltype(in)::value;
+    constexpr int KD = decltype(kd)::value, W = decltype(w)::value;
+    constexpr bool DOT = decltype(dot)::value;
+    const int slices = p.od / (16 * W), pairs = (b.N * b.H + kXcds - 1) / kXcds * kXcds;
+    hipLaunchKernelGGL((linear_scan_kernel<IN, KD, W, DOT ? 3 : 2, DOT>), dim3(pairs * slices),
+                       dim3(64 * (W + kCopyWaves)), 0, stream, b, p);
+    return hipGetLastError();
+  };
+  auto by_dot = [&](auto in, auto kd) {
+    const std::integral_constant<int, 4> w;
+    return p.dot ? go(in, kd, w, std::true_type()) : go(in, kd, w, std::false_type());
+  };
+  auto by_kd = [&](auto in) {
+    return p.kd == 64 ? by_dot(in, std::integral_constant<int, 64>())
+                      : by_dot(in, std::integral_constant<int, 128>());
+  };
+  return b.in_dtype == 0 ? by_kd(std::integral_constant<Dt, Dt::BF16>())
+                         : by_kd(std::integral_constant<Dt, Dt::F32>());
 }
 
 hipError_t launch_linear_dg(const LinearBatch& b, const float* row, int row_parts,

@@ -219,8 +219,8 @@ def test_backward_gates(dtype, gate):
     d = ref.make([200, 65, 3], 4, 2, 128, 128, dtype, "token", gate, True, seed=32)
     out = backward(d, torch.float32)
     check_backward(d, out)
-    without = backward(d, torch.float32, dg=False)
-    assert all(torch.equal(without[n], out[n]) for n in without)
+    # without dg another kernel forms dq and dv (fewer planes): the same bound, not the same bits
+    check_backward(d, backward(d, torch.float32, dg=False))
 
 
 @pytest.mark.parametrize("state_in, dstate_out", [(True, False), (False, True)])
