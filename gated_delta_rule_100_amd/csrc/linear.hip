@@ -20,7 +20,6 @@ namespace {
 
 constexpr float kMinGate = -110.f;  // e^-110 is zero in fp32: stands for every smaller g
 constexpr int kXcds = 8;
-constexpr int kCopyWaves = 4;
 
 __device__ __forceinline__ float clamp_gate(float g) { return g < kMinGate ? kMinGate : g; }
 
@@ -173,15 +172,24 @@ __device__ __forceinline__ void copy16(const void* src, void* lds) {
 // ---- the chunk scan
 //
 // One workgroup per (unit, head, 16 W columns of w): a unit is a sequence, or a
-// segment of one.  W compute waves hold 16 state rows each, for the whole walk,
-// as output tiles of the state update: lane (c, g) holds Z[c][32 j + 8 g + 0..7],
-// which is also the fragment of Z in the product with x.  The scores x.y of a
-// chunk are formed once a workgroup, a few 16 x 16 tiles a wave, and shared
-// through LDS as P^T fragments; everything else stays in the wave's registers.
-// kCopyWaves more waves copy the next chunk's x, y, w rows to the other LDS
-// buffer (global-to-LDS loads) and form its gate factors.  Two barriers a
-// chunk: P is complete; the chunk is done.
-template <Dt IN, int KD, int W>
+// segment of one.  Its waves have three roles and meet at one barrier a chunk:
+//   - W compute waves hold 16 state rows each for the whole walk, as output
+//     tiles of the state update: lane (c, g) holds Z[c][32 j + 8 g + 0..7],
+//     which is also the fragment of Z in the product with x.  In step s they
+//     form out = Z x + P w and the update of Z for chunk s;
+//   - 4 score waves form the scores x.y of chunk s + 1, with their decays, as
+//     P^T fragments in LDS: they do not depend on the state, and their
+//     arithmetic fills the issue slots that the compute waves' chain leaves;
+//   - 4 copy waves copy the x and y rows of chunk s + 2 and the w rows of chunk
+//     s + 1 to LDS (global-to-LDS loads) and form the gate factors of s + 2.
+//     They are waves of their own because a wave's LDS reads wait for all its
+//     global-to-LDS loads in flight.
+// One wave a SIMD doing all three took 8900 cycles a chunk (4 x 4096 tokens, 16
+// heads), 3500 of them for the scores.
+constexpr int kScoreWaves = 4;
+constexpr int kCopyWaves = 4;
+
+template <Dt IN, int KD, int W, int PZ>
 struct ScanCfg {
   static constexpr int ES = IN == Dt::BF16 ? 2 : 4;
   static constexpr int C = IN == Dt::BF16 ? 64 : 32;  // tokens a chunk (fp32: half, for LDS)
@@ -189,34 +197,40 @@ struct ScanCfg {
   static constexpr int KB = KD / 32;          // 32-deep blocks over kd
   static constexpr int VS = 16 * W;           // columns of w a workgroup
   static constexpr int CHK = KD * ES / 16, CHV = VS * ES / 16;
+  static constexpr int THREADS = 64 * (W + kScoreWaves + kCopyWaves);
+  // three buffers of x and y rows, two of w rows
   static constexpr int X_BYTES = C * KD * ES, W_BYTES = C * VS * ES;
-  static constexpr int OFF_X = 0, OFF_Y = X_BYTES, OFF_W = 2 * X_BYTES;
-  static constexpr int BUF = 2 * X_BYTES + W_BYTES;
-  // gate factors of a chunk: G in log2 units as a sum of two floats, the
-  // factors of Z x_t and of the update, e^{G_C}
+  static constexpr int OFF_W = 3 * 2 * X_BYTES;
+  // three of gate factors: G in log2 units as a sum of two floats, the factors
+  // of Z x_t and of the update, e^{G_C}
   static constexpr int GATE_BYTES = (4 * C + 4) * 4;
-  static constexpr int OFF_G = 2 * BUF;
-  // P^T fragments (row tile, 32-deep block) and the scores of a token with itself
-  static constexpr int FRAG = IN == Dt::BF16 ? 1024 : 2048;
-  static constexpr int TILES = NT * (NT + 1) / 2;
-};
-
-template <Dt IN, int KD, int W, int PZ>
-struct ScanLds {
-  using Cfg = ScanCfg<IN, KD, W>;
+  static constexpr int OFF_G = OFF_W + 2 * W_BYTES;
+  // two of P^T fragments (row tile, 32-deep block) on the walked side of the
+  // diagonal, PL planes each, and of the scores of a token with itself
   static constexpr int PL = IN == Dt::F32 ? 1 : PZ;
-  static constexpr int OFF_P = Cfg::OFF_G + 2 * Cfg::GATE_BYTES;
-  static constexpr int OFF_DIAG = OFF_P + Cfg::NT * Cfg::NB * PL * Cfg::FRAG;
-  static constexpr int BYTES = OFF_DIAG + Cfg::C * 4;
+  static constexpr int FRAG = IN == Dt::BF16 ? 1024 : 2048;
+  static constexpr int FRAGS = NB == 2 ? 6 : 2;
+  static constexpr int P_BYTES = FRAGS * PL * FRAG;
+  static constexpr int OFF_P = OFF_G + 3 * GATE_BYTES;
+  static constexpr int OFF_DIAG = OFF_P + 2 * P_BYTES;
+  static constexpr int BYTES = OFF_DIAG + 2 * C * 4;
   static_assert(BYTES <= 160 * 1024, "LDS");
 };
 
+// Index of the P^T fragment of row tile tt and block sb.
+template <int NB>
+__device__ __forceinline__ int p_frag(int tt, int sb, bool backward) {
+  if constexpr (NB == 1) return tt;
+  else if (backward) return tt < 2 ? 2 * tt + sb : tt + 2;
+  else return tt < 2 ? tt : 2 * tt - 2 + sb;
+}
+
 template <Dt IN, int KD, int W, int PZ, bool DOT>
-__global__ __launch_bounds__(64 * (W + kCopyWaves)) void linear_scan_kernel(LinearBatch b, LinearPass p) {
-  using Cfg = ScanCfg<IN, KD, W>;
-  using Lds = ScanLds<IN, KD, W, PZ>;
-  constexpr int C = Cfg::C, NT = Cfg::NT, NB = Cfg::NB, KB = Cfg::KB, ES = Cfg::ES, PL = Lds::PL;
-  __shared__ __align__(1024) unsigned char lds[Lds::BYTES];
+__global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_scan_kernel(
+    LinearBatch b, LinearPass p) {
+  using Cfg = ScanCfg<IN, KD, W, PZ>;
+  constexpr int C = Cfg::C, NT = Cfg::NT, NB = Cfg::NB, KB = Cfg::KB, ES = Cfg::ES, PL = Cfg::PL;
+  __shared__ __align__(1024) unsigned char lds[Cfg::BYTES];
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // the workgroups of one (unit, head) read the same x and y rows: one XCD
@@ -227,10 +241,20 @@ __global__ __launch_bounds__(64 * (W + kCopyWaves)) void linear_scan_kernel(Line
   int tb, te;
   token_range(b, n, tb, te);
   const int chunks = (te - tb + C - 1) / C;
+  const bool backward = p.backward;
+  // token range of the s-th chunk of the walk
+  auto chunk_at = [&](int s, int& tok) {
+    tok = tb + (backward ? chunks - 1 - s : s) * C;
+    return te - tok < C ? te - tok : C;
+  };
+  auto x_tile = [&](int s) { return lds + (s % 3) * 2 * Cfg::X_BYTES; };
+  auto gate_row = [&](int s) {
+    return reinterpret_cast<float*>(lds + Cfg::OFF_G + (s % 3) * Cfg::GATE_BYTES);
+  };
 
-  if (wave >= W) {  // ---- copy waves
+  if (wave >= W + kScoreWaves) {  // ---- copy waves
     if (chunks == 0) return;
-    const int cw = wave - W;
+    const int cw = wave - W - kScoreWaves;
     auto rows = [&](const LinearRows& r, int width, int skip) {
       return static_cast<const char*>(r.p) + (static_cast<size_t>(h / r.group) * width + skip) * ES;
     };
@@ -240,38 +264,35 @@ __global__ __launch_bounds__(64 * (W + kCopyWaves)) void linear_scan_kernel(Line
     const size_t xst = p.x.stride * ES, yst = p.y.stride * ES, wst = p.w.stride * ES;
     // Rows past the end of a short chunk repeat its last token: nothing outside
     // the sequence is read, and their factors are zero.
-    auto chunk_at = [&](int s, int& tok) {
-      tok = tb + (p.backward ? chunks - 1 - s : s) * C;
-      return te - tok < C ? te - tok : C;
-    };
-    float gate = 0.f;
-    auto load_gate = [&](int s) {
+    auto copy_rows = [&](int s, const char* src, size_t stride, unsigned char* to, auto ch) {
+      constexpr int CH = decltype(ch)::value;
       int tok;
       const int len = chunk_at(s, tok);
-      if (cw != 0) return;
-      if (!b.gates.per_token) gate = b.gates.g[h];
-      else if (lane < len) gate = b.gates.g[static_cast<size_t>(tok + lane) * b.H + h];
-    };
-    auto copy_chunk = [&](int s) {
-      int tok;
-      const int len = chunk_at(s, tok);
-      unsigned char* buf = lds + (s & 1) * Cfg::BUF;
-      auto tile = [&](const char* src, size_t stride, unsigned char* to, auto ch) {
-        constexpr int CH = decltype(ch)::value;
-        const char* base = src + static_cast<size_t>(tok) * stride;
+      const char* base = src + static_cast<size_t>(tok) * stride;
 #pragma unroll
-        for (int i = 0; i < C * CH / 64 / kCopyWaves; ++i) {
-          const int q = 64 * (cw + kCopyWaves * i) + lane, r = q / CH, pc = q % CH;
-          const int rr = r < len ? r : len - 1;
-          copy16(base + rr * stride + 16 * (pc ^ perm<CH>(r)), to + 1024 * (cw + kCopyWaves * i));
-        }
-      };
-      tile(xs, xst, buf + Cfg::OFF_X, std::integral_constant<int, Cfg::CHK>());
-      tile(ys, yst, buf + Cfg::OFF_Y, std::integral_constant<int, Cfg::CHK>());
-      tile(ws, wst, buf + Cfg::OFF_W, std::integral_constant<int, Cfg::CHV>());
+      for (int i = 0; i < C * CH / 64 / kCopyWaves; ++i) {
+        const int q = 64 * (cw + kCopyWaves * i) + lane, r = q / CH, pc = q % CH;
+        const int rr = r < len ? r : len - 1;
+        copy16(base + rr * stride + 16 * (pc ^ perm<CH>(r)), to + 1024 * (cw + kCopyWaves * i));
+      }
+    };
+    auto copy_xy = [&](int s) {
+      copy_rows(s, xs, xst, x_tile(s), std::integral_constant<int, Cfg::CHK>());
+      copy_rows(s, ys, yst, x_tile(s) + Cfg::X_BYTES, std::integral_constant<int, Cfg::CHK>());
+    };
+    auto copy_w = [&](int s) {
+      copy_rows(s, ws, wst, lds + Cfg::OFF_W + (s & 1) * Cfg::W_BYTES,
+                std::integral_constant<int, Cfg::CHV>());
+    };
+    auto load_gate = [&](int s) {
+      if (cw != 0) return 0.f;
+      int tok;
+      const int len = chunk_at(s, tok);
+      if (!b.gates.per_token) return b.gates.g[h];
+      return lane < len ? b.gates.g[static_cast<size_t>(tok + lane) * b.H + h] : 0.f;
     };
     // Prefix sums in fp64, so that a decay's error does not grow with |G|.
-    auto put_gates = [&](int s) {
+    auto put_gates = [&](int s, float gate) {
       if (cw != 0) return;
       int tok;
       const int len = chunk_at(s, tok);
@@ -288,33 +309,120 @@ __global__ __launch_bounds__(64 * (W + kCopyWaves)) void linear_scan_kernel(Line
       }
       G *= 1.4426950408889634;
       const double end = __shfl(G, C - 1);
-      float* f = reinterpret_cast<float*>(lds + Cfg::OFF_G + (s & 1) * Cfg::GATE_BYTES);
+      float* f = gate_row(s);
       if (lane < C) {
         const float hi = static_cast<float>(G), lo = static_cast<float>(G - hi);
         const float from = exp2f(hi) * fmaf(lo, 0.69314718f, 1.f);
-        const double rest = end - G;
-        const float to = exp2f(static_cast<float>(rest));
+        const float to = exp2f(static_cast<float>(end - G));
         f[lane] = hi;
         f[C + lane] = lo;
-        f[2 * C + lane] = p.os * (p.backward ? to : from);
-        f[3 * C + lane] = lane < len ? p.us * (p.backward ? from : to) : 0.f;
+        f[2 * C + lane] = p.os * (backward ? to : from);
+        f[3 * C + lane] = lane < len ? p.us * (backward ? from : to) : 0.f;
         if (lane == 0) f[4 * C] = exp2f(static_cast<float>(end));
       }
     };
-    load_gate(0);
-    copy_chunk(0);
-    put_gates(0);
+    const float g0 = load_gate(0), g1 = chunks > 1 ? load_gate(1) : 0.f;
+    copy_xy(0);
+    copy_w(0);
+    if (chunks > 1) copy_xy(1);
+    put_gates(0, g0);
+    if (chunks > 1) put_gates(1, g1);
     __builtin_amdgcn_s_waitcnt(0);
     bare_barrier();
+    bare_barrier();
     for (int s = 0; s < chunks; ++s) {
-      if (s + 1 < chunks) {
-        load_gate(s + 1);
-        copy_chunk(s + 1);
+      float gate = 0.f;
+      if (s + 2 < chunks) gate = load_gate(s + 2);
+      if (s + 1 < chunks) copy_w(s + 1);
+      if (s + 2 < chunks) {
+        copy_xy(s + 2);
+        put_gates(s + 2, gate);
       }
-      bare_barrier();
-      if (s + 1 < chunks) put_gates(s + 1);
       __builtin_amdgcn_s_waitcnt(0);
       bare_barrier();
+    }
+    return;
+  }
+
+  if (wave >= W) {  // ---- score waves
+    if (chunks == 0) return;
+    const int sw = wave - W;
+    // Tiles (row tile, column tile) of this wave.  Of the ten on the walked side
+    // of the diagonal each wave has two of one row tile and a third one; the
+    // last wave forms tiles that another forms as well (the same values).
+    constexpr int PER = NB == 2 ? 3 : 1;
+    int tts[PER], sts[PER];
+    if constexpr (NB == 2) {
+      tts[0] = tts[1] = 3 - sw;
+      sts[0] = 0;
+      sts[1] = sw < 3 ? 1 : 0;
+      tts[2] = sw == 1 ? 2 : 3;
+      sts[2] = sw < 2 ? 2 : 3;
+    } else {
+      tts[0] = sw == 0 ? 0 : 1;
+      sts[0] = sw < 2 ? 0 : 1;
+    }
+    if (backward)
+      for (int i = 0; i < PER; ++i) {
+        tts[i] = NT - 1 - tts[i];
+        sts[i] = NT - 1 - sts[i];
+      }
+    const float ps = p.us * p.os;
+    auto scores = [&](int s) {
+      int tok;
+      const int len = chunk_at(s, tok);
+      const unsigned char *X = x_tile(s), *Y = X + Cfg::X_BYTES;
+      const float* gate = gate_row(s);
+      float* diag = reinterpret_cast<float*>(lds + Cfg::OFF_DIAG) + (s & 1) * C;
+      floatx4 acc[PER];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) acc[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        Frag<IN> xf = row_frag<IN, Cfg::CHK>(X, 16 * tts[0] + c, kb, g);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          if (i == 2) xf = row_frag<IN, Cfg::CHK>(X, 16 * tts[i] + c, kb, g);
+          acc[i] = mma(row_frag<IN, Cfg::CHK>(Y, 16 * sts[i] + c, kb, g), xf, acc[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int t = 16 * tts[i] + c, s4 = 16 * sts[i] + 4 * g;
+        const float gh = gate[t], gl = gate[C + t];
+        const floatx4 sh = *reinterpret_cast<const floatx4*>(gate + s4);
+        const floatx4 sl = *reinterpret_cast<const floatx4*>(gate + C + s4);
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float d = (gh - sh[e]) + (gl - sl[e]);
+          const float x = acc[i][e] * ps * __builtin_amdgcn_exp2f(backward ? -d : d);
+          const int sc = s4 + e;
+          if (DOT && sc == t) diag[t] = x;
+          const bool in = backward ? (DOT ? sc > t : sc >= t) && sc < len : (DOT ? sc < t : sc <= t);
+          v[e] = in ? x : 0.f;
+        }
+        const int half = sts[i] & 1;
+        unsigned char* to = lds + Cfg::OFF_P + (s & 1) * Cfg::P_BYTES +
+                            p_frag<NB>(tts[i], sts[i] >> 1, backward) * PL * Cfg::FRAG;
+        if constexpr (IN == Dt::F32) {
+          *reinterpret_cast<floatx4*>(to + lane * 32 + 16 * half) = floatx4{v[0], v[1], v[2], v[3]};
+        } else {
+          uint32_t lo[PL], hi[PL];
+          split2<PL>(v[0], v[1], lo);
+          split2<PL>(v[2], v[3], hi);
+#pragma unroll
+          for (int q = 0; q < PL; ++q)
+            *reinterpret_cast<uint2*>(to + q * Cfg::FRAG + lane * 16 + 8 * half) = make_uint2(lo[q], hi[q]);
+        }
+      }
+    };
+    bare_barrier();
+    scores(0);
+    lds_barrier();
+    for (int s = 0; s < chunks; ++s) {
+      if (s + 1 < chunks) scores(s + 1);
+      lds_barrier();
     }
     return;
   }
@@ -331,56 +439,23 @@ __global__ __launch_bounds__(64 * (W + kCopyWaves)) void linear_scan_kernel(Line
       z[j][e] = p.start ? p.start[zbase + k * p.col] : 0.f;
     }
   if (chunks > 0) {
-    // fragment halves above the diagonal stay zero
-    for (int i = threadIdx.x; i < (Lds::OFF_DIAG - Lds::OFF_P) / 16; i += 64 * W)
-      *reinterpret_cast<uint4*>(lds + Lds::OFF_P + 16 * i) = make_uint4(0, 0, 0, 0);
+    // the halves of P^T fragments beyond the diagonal stay zero
+    for (int i = threadIdx.x; i < 2 * Cfg::P_BYTES / 16; i += 64 * W)
+      *reinterpret_cast<uint4*>(lds + Cfg::OFF_P + 16 * i) = make_uint4(0, 0, 0, 0);
     lds_barrier();
+    bare_barrier();
   }
+  const size_t out_es = p.out_dtype == 0 ? 2 : 4;
+  const uint32_t out_row = static_cast<uint32_t>(b.H * p.od * out_es);
+  const uint32_t out_lane = c * out_row + static_cast<uint32_t>(4 * g * out_es);
   for (int s = 0; s < chunks; ++s) {
-    const int tok = tb + (p.backward ? chunks - 1 - s : s) * C;
-    const int len = te - tok < C ? te - tok : C;
-    const unsigned char* buf = lds + (s & 1) * Cfg::BUF;
-    const unsigned char *X = buf + Cfg::OFF_X, *Y = buf + Cfg::OFF_Y, *Wt = buf + Cfg::OFF_W;
-    const float* gate = reinterpret_cast<const float*>(lds + Cfg::OFF_G + (s & 1) * Cfg::GATE_BYTES);
-    float* diag = reinterpret_cast<float*>(lds + Lds::OFF_DIAG);
-
-    // P^T tiles (columns t of row tile tt, rows s of tile st), W of them at a time
-    const float ps = p.us * p.os;
-    for (int i = wave; i < Cfg::TILES; i += W) {
-      int tt = 0, st = i;  // i-th pair st <= tt (forward), or its mirror (backward)
-      while (st > tt) { st -= tt + 1; ++tt; }
-      if (p.backward) { tt = NT - 1 - tt; st = NT - 1 - st; }
-      floatx4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb)
-        acc = mma(row_frag<IN, Cfg::CHK>(Y, 16 * st + c, kb, g),
-                  row_frag<IN, Cfg::CHK>(X, 16 * tt + c, kb, g), acc);
-      const int t = 16 * tt + c, s4 = 16 * st + 4 * g;
-      const float gh = gate[t], gl = gate[C + t];
-      const floatx4 sh = *reinterpret_cast<const floatx4*>(gate + s4);
-      const floatx4 sl = *reinterpret_cast<const floatx4*>(gate + C + s4);
-      float v[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float d = (gh - sh[e]) + (gl - sl[e]);
-        const float x = acc[e] * ps * __builtin_amdgcn_exp2f(p.backward ? -d : d);
-        const int sc = s4 + e;
-        if (DOT && sc == t) diag[t] = x;
-        const bool in = p.backward ? (DOT ? sc > t : sc >= t) && sc < len : (DOT ? sc < t : sc <= t);
-        v[e] = in ? x : 0.f;
-      }
-      unsigned char* to = lds + Lds::OFF_P + (tt * NB + (st >> 1)) * PL * Cfg::FRAG;
-      if constexpr (IN == Dt::F32) {
-        *reinterpret_cast<floatx4*>(to + lane * 32 + 16 * (st & 1)) = floatx4{v[0], v[1], v[2], v[3]};
-      } else {
-        uint32_t lo[PL], hi[PL];
-        split2<PL>(v[0], v[1], lo);
-        split2<PL>(v[2], v[3], hi);
-#pragma unroll
-        for (int q = 0; q < PL; ++q)
-          *reinterpret_cast<uint2*>(to + q * Cfg::FRAG + lane * 16 + 8 * (st & 1)) = make_uint2(lo[q], hi[q]);
-      }
-    }
+    int tok;
+    const int len = chunk_at(s, tok);
+    const unsigned char *X = x_tile(s), *Y = X + Cfg::X_BYTES;
+    const unsigned char* Wt = lds + Cfg::OFF_W + (s & 1) * Cfg::W_BYTES;
+    const unsigned char* P = lds + Cfg::OFF_P + (s & 1) * Cfg::P_BYTES;
+    const float* gate = gate_row(s);
+    const float* diag = reinterpret_cast<const float*>(lds + Cfg::OFF_DIAG) + (s & 1) * C;
 
     // out^T = Z x^T, rows od, columns t
     floatx4 o[NT];
@@ -398,31 +473,40 @@ __global__ __launch_bounds__(64 * (W + kCopyWaves)) void linear_scan_kernel(Line
 #pragma unroll
     for (int tt = 0; tt < NT; ++tt) o[tt] *= gate[2 * C + 16 * tt + c];
 
+    // + w^T P^T
     Frag<IN> wf[NB];
 #pragma unroll
     for (int sb = 0; sb < NB; ++sb) wf[sb] = col_frag<IN, Cfg::CHV, false>(Wt, 32 * sb, 16 * wave, c, g);
-    lds_barrier();  // P is complete
+    auto add_scores = [&](auto back) {
+      constexpr bool BACK = decltype(back)::value;
+#pragma unroll
+      for (int tt = 0; tt < NT; ++tt)
+#pragma unroll
+        for (int sb = 0; sb < NB; ++sb) {
+          if (BACK ? sb < (tt >> 1) : sb > (tt >> 1)) continue;
+          const unsigned char* from = P + p_frag<NB>(tt, sb, BACK) * PL * Cfg::FRAG;
+          Planes<IN, PZ> pp;
+          if constexpr (IN == Dt::F32) {
+            const floatx4 a = *reinterpret_cast<const floatx4*>(from + lane * 32);
+            const floatx4 d = *reinterpret_cast<const floatx4*>(from + lane * 32 + 16);
+            pp.p[0] = {{a[0], a[1], a[2], a[3], d[0], d[1], d[2], d[3]}};
+          } else {
+#pragma unroll
+            for (int q = 0; q < PL; ++q)
+              pp.p[q] = *reinterpret_cast<const bf16x8*>(from + q * Cfg::FRAG + lane * 16);
+          }
+          o[tt] = mma(wf[sb], pp, o[tt]);
+        }
+    };
+    if (backward) add_scores(std::true_type());
+    else add_scores(std::false_type());
 
+    char* out = static_cast<char*>(p.out) +
+                ((static_cast<size_t>(tok) * b.H + h) * p.od + od) * out_es;
 #pragma unroll
     for (int tt = 0; tt < NT; ++tt) {
-#pragma unroll
-      for (int sb = 0; sb < NB; ++sb) {
-        if (p.backward ? sb < (tt >> 1) : sb > (tt >> 1)) continue;
-        const unsigned char* from = lds + Lds::OFF_P + (tt * NB + sb) * PL * Cfg::FRAG;
-        Planes<IN, PZ> pp;
-        if constexpr (IN == Dt::F32) {
-          const floatx4 a = *reinterpret_cast<const floatx4*>(from + lane * 32);
-          const floatx4 d = *reinterpret_cast<const floatx4*>(from + lane * 32 + 16);
-          pp.p[0] = {{a[0], a[1], a[2], a[3], d[0], d[1], d[2], d[3]}};
-        } else {
-#pragma unroll
-          for (int q = 0; q < PL; ++q) pp.p[q] = *reinterpret_cast<const bf16x8*>(from + q * Cfg::FRAG + lane * 16);
-        }
-        o[tt] = mma(wf[sb], pp, o[tt]);
-      }
       const int t = 16 * tt + c;
       const bool live = t < len;
-      const size_t th = static_cast<size_t>(tok + t) * b.H + h;
       if constexpr (DOT) {
         float dot = 0.f;
         if (live) {
@@ -441,14 +525,14 @@ __global__ __launch_bounds__(64 * (W + kCopyWaves)) void linear_scan_kernel(Line
         o[tt] += diag[t] * own;
       }
       if (live) {
-        const size_t oi = th * p.od + od + 4 * g;
+        const uint32_t at = out_lane + 16 * tt * out_row;
         if (p.out_dtype == 0) {
           uint32_t lo[1], hi[1];
           split2<1>(o[tt][0], o[tt][1], lo);
           split2<1>(o[tt][2], o[tt][3], hi);
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + oi) = make_uint2(lo[0], hi[0]);
+          *reinterpret_cast<uint2*>(out + at) = make_uint2(lo[0], hi[0]);
         } else {
-          *reinterpret_cast<floatx4*>(static_cast<float*>(p.out) + oi) = o[tt];
+          *reinterpret_cast<floatx4*>(out + at) = o[tt];
         }
       }
     }
@@ -601,7 +685,7 @@ hipError_t launch_linear_pass(const LinearBatch& b, const LinearPass& p, hipStre
     constexpr bool DOT = decltype(dot)::value;
     const int slices = p.od / (16 * W), pairs = (b.N * b.H + kXcds - 1) / kXcds * kXcds;
     hipLaunchKernelGGL((linear_scan_kernel<IN, KD, W, DOT ? 3 : 2, DOT>), dim3(pairs * slices),
-                       dim3(64 * (W + kCopyWaves)), 0, stream, b, p);
+                       dim3(64 * (W + kScoreWaves + kCopyWaves)), 0, stream, b, p);
     return hipGetLastError();
   };
   auto by_dot = [&](auto in, auto kd) {
