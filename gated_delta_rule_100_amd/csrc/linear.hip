@@ -218,14 +218,14 @@ struct ScanCfg {
 };
 
 // Index of the P^T fragment of row tile tt and block sb.
-template <int NB>
-__device__ __forceinline__ int p_frag(int tt, int sb, bool backward) {
+template <int NB, bool BACK>
+__device__ __forceinline__ int p_frag(int tt, int sb) {
   if constexpr (NB == 1) return tt;
-  else if (backward) return tt < 2 ? 2 * tt + sb : tt + 2;
+  else if constexpr (BACK) return tt < 2 ? 2 * tt + sb : tt + 2;
   else return tt < 2 ? tt : 2 * tt - 2 + sb;
 }
 
-template <Dt IN, int KD, int W, int PZ, bool DOT>
+template <Dt IN, int KD, int W, int PZ, bool DOT, bool BACK>
 __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_scan_kernel(
     LinearBatch b, LinearPass p) {
   using Cfg = ScanCfg<IN, KD, W, PZ>;
@@ -241,10 +241,9 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
   int tb, te;
   token_range(b, n, tb, te);
   const int chunks = (te - tb + C - 1) / C;
-  const bool backward = p.backward;
   // token range of the s-th chunk of the walk
   auto chunk_at = [&](int s, int& tok) {
-    tok = tb + (backward ? chunks - 1 - s : s) * C;
+    tok = tb + (BACK ? chunks - 1 - s : s) * C;
     return te - tok < C ? te - tok : C;
   };
   auto x_tile = [&](int s) { return lds + (s % 3) * 2 * Cfg::X_BYTES; };
@@ -316,8 +315,8 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
         const float to = exp2f(static_cast<float>(end - G));
         f[lane] = hi;
         f[C + lane] = lo;
-        f[2 * C + lane] = p.os * (backward ? to : from);
-        f[3 * C + lane] = lane < len ? p.us * (backward ? from : to) : 0.f;
+        f[2 * C + lane] = p.os * (BACK ? to : from);
+        f[3 * C + lane] = lane < len ? p.us * (BACK ? from : to) : 0.f;
         if (lane == 0) f[4 * C] = exp2f(static_cast<float>(end));
       }
     };
@@ -362,7 +361,7 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
       tts[0] = sw == 0 ? 0 : 1;
       sts[0] = sw < 2 ? 0 : 1;
     }
-    if (backward)
+    if (BACK)
       for (int i = 0; i < PER; ++i) {
         tts[i] = NT - 1 - tts[i];
         sts[i] = NT - 1 - sts[i];
@@ -396,15 +395,15 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float d = (gh - sh[e]) + (gl - sl[e]);
-          const float x = acc[i][e] * ps * __builtin_amdgcn_exp2f(backward ? -d : d);
+          const float x = acc[i][e] * ps * __builtin_amdgcn_exp2f(BACK ? -d : d);
           const int sc = s4 + e;
           if (DOT && sc == t) diag[t] = x;
-          const bool in = backward ? (DOT ? sc > t : sc >= t) && sc < len : (DOT ? sc < t : sc <= t);
+          const bool in = BACK ? (DOT ? sc > t : sc >= t) && sc < len : (DOT ? sc < t : sc <= t);
           v[e] = in ? x : 0.f;
         }
         const int half = sts[i] & 1;
         unsigned char* to = lds + Cfg::OFF_P + (s & 1) * Cfg::P_BYTES +
-                            p_frag<NB>(tts[i], sts[i] >> 1, backward) * PL * Cfg::FRAG;
+                            p_frag<NB, BACK>(tts[i], sts[i] >> 1) * PL * Cfg::FRAG;
         if constexpr (IN == Dt::F32) {
           *reinterpret_cast<floatx4*>(to + lane * 32 + 16 * half) = floatx4{v[0], v[1], v[2], v[3]};
         } else {
@@ -448,6 +447,7 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
   const size_t out_es = p.out_dtype == 0 ? 2 : 4;
   const uint32_t out_row = static_cast<uint32_t>(b.H * p.od * out_es);
   const uint32_t out_lane = c * out_row + static_cast<uint32_t>(4 * g * out_es);
+  const size_t e_col = DOT ? static_cast<size_t>(h / p.e.group) * p.od + od + 4 * g : 0;
   for (int s = 0; s < chunks; ++s) {
     int tok;
     const int len = chunk_at(s, tok);
@@ -457,90 +457,86 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
     const float* gate = gate_row(s);
     const float* diag = reinterpret_cast<const float*>(lds + Cfg::OFF_DIAG) + (s & 1) * C;
 
-    // out^T = Z x^T, rows od, columns t
+    // the rows to dot with the outputs: loaded first, used last
+    float ev[DOT ? NT : 1][4];
+    if constexpr (DOT) {
+#pragma unroll
+      for (int tt = 0; tt < NT; ++tt) {
+        const int t = 16 * tt + c, row = tok + (t < len ? t : len - 1);
+        load_vec<IN, 4>(p.e.p, static_cast<size_t>(row) * p.e.stride + e_col, ev[tt]);
+      }
+    }
+
+    // out^T = Z x^T, rows od, columns t: the x fragments of a block are read
+    // while the block before it is multiplied, and the row tiles' chains alternate
     floatx4 o[NT];
 #pragma unroll
     for (int tt = 0; tt < NT; ++tt) o[tt] = floatx4{0.f, 0.f, 0.f, 0.f};
+    Frag<IN> xf[2][NT];
+#pragma unroll
+    for (int tt = 0; tt < NT; ++tt) xf[0][tt] = row_frag<IN, Cfg::CHK>(X, 16 * tt + c, 0, g);
+    Frag<IN> wf[NB];
+    Planes<IN, PZ> pf[Cfg::FRAGS];
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
+      if (kb + 1 < KB) {
+#pragma unroll
+        for (int tt = 0; tt < NT; ++tt)
+          xf[(kb + 1) & 1][tt] = row_frag<IN, Cfg::CHK>(X, 16 * tt + c, kb + 1, g);
+      } else {
+#pragma unroll
+        for (int sb = 0; sb < NB; ++sb)
+          wf[sb] = col_frag<IN, Cfg::CHV, false>(Wt, 32 * sb, 16 * wave, c, g);
+#pragma unroll
+        for (int i = 0; i < Cfg::FRAGS; ++i) {
+          const unsigned char* from = P + i * PL * Cfg::FRAG;
+          if constexpr (IN == Dt::F32) {
+            const floatx4 a = *reinterpret_cast<const floatx4*>(from + lane * 32);
+            const floatx4 d = *reinterpret_cast<const floatx4*>(from + lane * 32 + 16);
+            pf[i].p[0] = {{a[0], a[1], a[2], a[3], d[0], d[1], d[2], d[3]}};
+          } else {
+#pragma unroll
+            for (int q = 0; q < PL; ++q)
+              pf[i].p[q] = *reinterpret_cast<const bf16x8*>(from + q * Cfg::FRAG + lane * 16);
+          }
+        }
+      }
       const float zz[8] = {z[2 * kb][0], z[2 * kb][1], z[2 * kb][2], z[2 * kb][3],
                            z[2 * kb + 1][0], z[2 * kb + 1][1], z[2 * kb + 1][2], z[2 * kb + 1][3]};
       const Planes<IN, PZ> zp = to_planes<IN, PZ>(zz);
 #pragma unroll
-      for (int tt = 0; tt < NT; ++tt)
-        o[tt] = mma(zp, row_frag<IN, Cfg::CHK>(X, 16 * tt + c, kb, g), o[tt]);
+      for (int q = PL - 1; q >= 0; --q)
+#pragma unroll
+        for (int tt = 0; tt < NT; ++tt) o[tt] = mma(zp.p[q], xf[kb & 1][tt], o[tt]);
     }
 #pragma unroll
     for (int tt = 0; tt < NT; ++tt) o[tt] *= gate[2 * C + 16 * tt + c];
 
     // + w^T P^T
-    Frag<IN> wf[NB];
 #pragma unroll
-    for (int sb = 0; sb < NB; ++sb) wf[sb] = col_frag<IN, Cfg::CHV, false>(Wt, 32 * sb, 16 * wave, c, g);
-    auto add_scores = [&](auto back) {
-      constexpr bool BACK = decltype(back)::value;
+    for (int sb = 0; sb < NB; ++sb)
 #pragma unroll
-      for (int tt = 0; tt < NT; ++tt)
+      for (int q = PL - 1; q >= 0; --q)
 #pragma unroll
-        for (int sb = 0; sb < NB; ++sb) {
+        for (int tt = 0; tt < NT; ++tt) {
           if (BACK ? sb < (tt >> 1) : sb > (tt >> 1)) continue;
-          const unsigned char* from = P + p_frag<NB>(tt, sb, BACK) * PL * Cfg::FRAG;
-          Planes<IN, PZ> pp;
-          if constexpr (IN == Dt::F32) {
-            const floatx4 a = *reinterpret_cast<const floatx4*>(from + lane * 32);
-            const floatx4 d = *reinterpret_cast<const floatx4*>(from + lane * 32 + 16);
-            pp.p[0] = {{a[0], a[1], a[2], a[3], d[0], d[1], d[2], d[3]}};
-          } else {
-#pragma unroll
-            for (int q = 0; q < PL; ++q)
-              pp.p[q] = *reinterpret_cast<const bf16x8*>(from + q * Cfg::FRAG + lane * 16);
-          }
-          o[tt] = mma(wf[sb], pp, o[tt]);
+          o[tt] = mma(wf[sb], pf[p_frag<NB, BACK>(tt, sb)].p[q], o[tt]);
         }
-    };
-    if (backward) add_scores(std::true_type());
-    else add_scores(std::false_type());
 
-    char* out = static_cast<char*>(p.out) +
-                ((static_cast<size_t>(tok) * b.H + h) * p.od + od) * out_es;
-#pragma unroll
-    for (int tt = 0; tt < NT; ++tt) {
-      const int t = 16 * tt + c;
-      const bool live = t < len;
-      if constexpr (DOT) {
-        float dot = 0.f;
-        if (live) {
-          const size_t ei = static_cast<size_t>(tok + t) * p.e.stride +
-                            static_cast<size_t>(h / p.e.group) * p.od + od + 4 * g;
-          float ev[4];
-          load_vec<IN, 4>(p.e.p, ei, ev);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) dot = fmaf(ev[e], o[tt][e], dot);
-        }
-        dot += __shfl_xor(dot, 16);
-        dot += __shfl_xor(dot, 32);
-        if (live && g == 0)
-          p.dot[(static_cast<size_t>(od / 16) * b.H + h) * b.T_total + tok + t] = dot;
-        const floatx4 own = row4<IN, Cfg::CHV>(Wt, t, 16 * wave + 4 * g);
-        o[tt] += diag[t] * own;
-      }
-      if (live) {
-        const uint32_t at = out_lane + 16 * tt * out_row;
-        if (p.out_dtype == 0) {
-          uint32_t lo[1], hi[1];
-          split2<1>(o[tt][0], o[tt][1], lo);
-          split2<1>(o[tt][2], o[tt][3], hi);
-          *reinterpret_cast<uint2*>(out + at) = make_uint2(lo[0], hi[0]);
-        } else {
-          *reinterpret_cast<floatx4*>(out + at) = o[tt];
-        }
-      }
-    }
-
-    // Z <- e^{G_C} Z + (update factors . w)^T y
+    // Z <- e^{G_C} Z + (update factors . w)^T y, four tiles' y fragments at a time
     const float gc = gate[4 * C];
 #pragma unroll
     for (int j = 0; j < KD / 16; ++j) z[j] *= gc;
+    constexpr int JG = 4, GROUPS = KD / 16 / JG * NB;
+    Frag<IN> yf[2][JG];
+    auto read_y = [&](int i, Frag<IN> (&f)[JG]) {
+      const int sb = i / (KD / 16 / JG), j0 = i % (KD / 16 / JG) * JG;
+#pragma unroll
+      for (int j = 0; j < JG; ++j)
+        f[j] = col_frag<IN, Cfg::CHK, true>(Y, 32 * sb, 32 * ((j0 + j) >> 1) + 4 * (j & 1), c, g);
+    };
+    read_y(0, yf[0]);
+    Planes<IN, 3> up[NB];
 #pragma unroll
     for (int sb = 0; sb < NB; ++sb) {
       const floatx4 f0 = *reinterpret_cast<const floatx4*>(gate + 3 * C + 32 * sb + 4 * g);
@@ -551,10 +547,47 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
         u[e] = frag_value(wf[sb], e) * f0[e];
         u[4 + e] = frag_value(wf[sb], 4 + e) * f1[e];
       }
-      const Planes<IN, 3> up = to_planes<IN, 3>(u);
+      up[sb] = to_planes<IN, 3>(u);
+    }
 #pragma unroll
-      for (int j = 0; j < KD / 16; ++j)
-        z[j] = mma(col_frag<IN, Cfg::CHK, true>(Y, 32 * sb, 32 * (j >> 1) + 4 * (j & 1), c, g), up, z[j]);
+    for (int i = 0; i < GROUPS; ++i) {
+      if (i + 1 < GROUPS) read_y(i + 1, yf[(i + 1) & 1]);
+      const int sb = i / (KD / 16 / JG), j0 = i % (KD / 16 / JG) * JG;
+#pragma unroll
+      for (int q = Planes<IN, 3>::N - 1; q >= 0; --q)
+#pragma unroll
+        for (int j = 0; j < JG; ++j) z[j0 + j] = mma(yf[i & 1][j], up[sb].p[q], z[j0 + j]);
+    }
+
+    // outputs
+    if constexpr (DOT) {
+#pragma unroll
+      for (int tt = 0; tt < NT; ++tt) {
+        const int t = 16 * tt + c;
+        float dot = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dot = fmaf(ev[tt][e], o[tt][e], dot);
+        dot += __shfl_xor(dot, 16);
+        dot += __shfl_xor(dot, 32);
+        if (t < len && g == 0)
+          p.dot[(static_cast<size_t>(od / 16) * b.H + h) * b.T_total + tok + t] = dot;
+        o[tt] += diag[t] * row4<IN, Cfg::CHV>(Wt, t, 16 * wave + 4 * g);
+      }
+    }
+    char* out = static_cast<char*>(p.out) +
+                ((static_cast<size_t>(tok) * b.H + h) * p.od + od) * out_es;
+#pragma unroll
+    for (int tt = 0; tt < NT; ++tt) {
+      if (16 * tt + c >= len) continue;
+      const uint32_t at = out_lane + 16 * tt * out_row;
+      if (p.out_dtype == 0) {
+        uint32_t lo[1], hi[1];
+        split2<1>(o[tt][0], o[tt][1], lo);
+        split2<1>(o[tt][2], o[tt][3], hi);
+        *reinterpret_cast<uint2*>(out + at) = make_uint2(lo[0], hi[0]);
+      } else {
+        *reinterpret_cast<floatx4*>(out + at) = o[tt];
+      }
     }
     lds_barrier();  // the chunk is done
   }
@@ -679,18 +712,20 @@ hipError_t launch_linear_decode(const void* q, const void* k, const void* v,
 }
 
 hipError_t launch_linear_pass(const LinearBatch& b, const LinearPass& p, hipStream_t stream) {
-  auto go = [&](auto in, auto kd, auto w, auto dot) {
+  auto go = [&](auto in, auto kd, auto dot, auto back) {
     constexpr Dt IN = decltype(in)::value;
-    constexpr int KD = decltype(kd)::value, W = decltype(w)::value;
-    constexpr bool DOT = decltype(dot)::value;
+    constexpr int KD = decltype(kd)::value, W = 4;
+    constexpr bool DOT = decltype(dot)::value, BACK = decltype(back)::value;
     const int slices = p.od / (16 * W), pairs = (b.N * b.H + kXcds - 1) / kXcds * kXcds;
-    hipLaunchKernelGGL((linear_scan_kernel<IN, KD, W, DOT ? 3 : 2, DOT>), dim3(pairs * slices),
+    hipLaunchKernelGGL((linear_scan_kernel<IN, KD, W, DOT ? 3 : 2, DOT, BACK>), dim3(pairs * slices),
                        dim3(64 * (W + kScoreWaves + kCopyWaves)), 0, stream, b, p);
     return hipGetLastError();
   };
+  auto by_way = [&](auto in, auto kd, auto dot) {
+    return p.backward ? go(in, kd, dot, std::true_type()) : go(in, kd, dot, std::false_type());
+  };
   auto by_dot = [&](auto in, auto kd) {
-    const std::integral_constant<int, 4> w;
-    return p.dot ? go(in, kd, w, std::true_type()) : go(in, kd, w, std::false_type());
+    return p.dot ? by_way(in, kd, std::true_type()) : by_way(in, kd, std::false_type());
   };
   auto by_kd = [&](auto in) {
     return p.kd == 64 ? by_dot(in, std::integral_constant<int, 64>())
