@@ -97,46 +97,74 @@ __device__ __forceinline__ int perm(int r) {
   else return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
 }
 
-// Row fragment: elements 32 kb + 8 g .. + 7 of row r.
+// Byte offset of a lane's part of a row fragment (elements 32 kb + 8 g .. + 7 of
+// row c) and of a transposing read (rows 4 g + c / 4, columns 32 jb + 8 (c % 4)).
+// perm has period 16 in the row, so other rows are a constant further on.
+template <int CH>
+__device__ __forceinline__ int row_lane(int c, int g, int kb) {
+  return c * CH * 16 + 16 * ((4 * kb + g) ^ perm<CH>(c));
+}
+template <int CH>
+__device__ __forceinline__ int col_lane(int c, int g, int jb) {
+  const int r = 4 * g + (c >> 2);
+  return r * CH * 16 + 16 * ((4 * jb + (c & 3)) ^ perm<CH>(r));
+}
+
+// Row fragment: elements 32 kb + 8 g .. + 7 of row r0 + c (r0 a multiple of 16;
+// lane: row_lane of kb, used for bf16).
 template <Dt IN, int CH>
-__device__ __forceinline__ Frag<IN> row_frag(const unsigned char* tile, int r, int kb, int g) {
-  const unsigned char* row = tile + r * CH * 16;
+__device__ __forceinline__ Frag<IN> row_frag(const unsigned char* tile, int r0, int kb, int c, int g,
+                                             int lane) {
   if constexpr (IN == Dt::BF16) {
-    return *reinterpret_cast<const bf16x8*>(row + 16 * ((4 * kb + g) ^ perm<CH>(r)));
+    return *reinterpret_cast<const bf16x8*>(tile + lane + r0 * CH * 16);
   } else {
+    const unsigned char* row = tile + (r0 + c) * CH * 16;
     const int i = 8 * kb + 2 * g;
-    const floatx4 a = *reinterpret_cast<const floatx4*>(row + 16 * (i ^ perm<CH>(r)));
-    const floatx4 b = *reinterpret_cast<const floatx4*>(row + 16 * ((i + 1) ^ perm<CH>(r)));
+    const floatx4 a = *reinterpret_cast<const floatx4*>(row + 16 * (i ^ perm<CH>(c)));
+    const floatx4 b = *reinterpret_cast<const floatx4*>(row + 16 * ((i + 1) ^ perm<CH>(c)));
     return {{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
   }
 }
 
-// Column fragment of the 32 rows r0 ..: rows r0 + 4g + e in slots e and r0 + 16 + 4g + e in
-// slots 4 + e (the order in which two stacked output tiles present their rows), of column
-// col + c (WIDE = false) or col + 8 (c / 4) + c % 4 (WIDE; col a multiple of 4).
-template <Dt IN, int CH, bool WIDE>
-__device__ __forceinline__ Frag<IN> col_frag(const unsigned char* tile, int r0, int col, int c, int g) {
+// Two transposing reads, 16 rows apart (ds_read_b64_tr_b16: element e of lane c
+// comes from input lane 4 e + c / 4, element c % 4).
+template <int CH>
+__device__ __forceinline__ bf16x8 read_tr_pair(const unsigned char* p) {
+  const shortx4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) shortx4*)p);
+  const shortx4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      (__attribute__((address_space(3))) shortx4*)(p + 16 * CH * 16));
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+template <int CH>
+__device__ __forceinline__ F32x8 read_columns(const unsigned char* tile, int r0, int col, int g) {
+  F32x8 f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = r0 + 16 * (i >> 2) + 4 * g + (i & 3);
+    f.v[i] = *reinterpret_cast<const float*>(tile + r * CH * 16 + 16 * ((col >> 2) ^ perm<CH>(r)) +
+                                             4 * (col & 3));
+  }
+  return f;
+}
+
+// Column fragments of the 32 rows r0 ..: rows r0 + 4g + e in slots e and r0 +
+// 16 + 4g + e in slots 4 + e (the order in which two stacked output tiles
+// present their rows).  wide: of column 32 jb + 8 (c / 4) + c % 4 + 4 half (lane:
+// col_lane of jb); narrow: of column col + c.
+template <Dt IN, int CH>
+__device__ __forceinline__ Frag<IN> col_frag_wide(const unsigned char* tile, int r0, int jb, int half,
+                                                  int c, int g, int lane) {
+  if constexpr (IN == Dt::BF16) return read_tr_pair<CH>(tile + lane + r0 * CH * 16 + 8 * half);
+  else return read_columns<CH>(tile, r0, 32 * jb + 4 * half + 8 * (c >> 2) + (c & 3), g);
+}
+template <Dt IN, int CH>
+__device__ __forceinline__ Frag<IN> col_frag_narrow(const unsigned char* tile, int r0, int col, int c,
+                                                    int g) {
   if constexpr (IN == Dt::BF16) {
-    // ds_read_b64_tr_b16: element e of lane c comes from input lane 4e + c/4, element c % 4
-    const int at = col + (WIDE ? 8 : 4) * (c & 3);
-    shortx4 h[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = r0 + 16 * i + 4 * g + (c >> 2);
-      const unsigned char* p = tile + r * CH * 16 + 16 * ((at >> 3) ^ perm<CH>(r)) + 2 * (at & 7);
-      h[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) shortx4*)p);
-    }
-    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+    const int r = 4 * g + (c >> 2), at = col + 4 * (c & 3);
+    return read_tr_pair<CH>(tile + (r0 + r) * CH * 16 + 16 * ((at >> 3) ^ perm<CH>(r)) + 2 * (at & 7));
   } else {
-    const int at = col + (WIDE ? 8 * (c >> 2) + (c & 3) : c);
-    F32x8 f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = r0 + 16 * (i >> 2) + 4 * g + (i & 3);
-      f.v[i] = *reinterpret_cast<const float*>(tile + r * CH * 16 + 16 * ((at >> 2) ^ perm<CH>(r)) +
-                                               4 * (at & 3));
-    }
-    return f;
+    return read_columns<CH>(tile, r0, col + c, g);
   }
 }
 
@@ -246,10 +274,12 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
     tok = tb + (BACK ? chunks - 1 - s : s) * C;
     return te - tok < C ? te - tok : C;
   };
-  auto x_tile = [&](int s) { return lds + (s % 3) * 2 * Cfg::X_BYTES; };
-  auto gate_row = [&](int s) {
-    return reinterpret_cast<float*>(lds + Cfg::OFF_G + (s % 3) * Cfg::GATE_BYTES);
+  // buffer i of x and y rows and of gate factors (chunk s uses buffer s % 3)
+  auto x_tile = [&](int i) { return lds + i * 2 * Cfg::X_BYTES; };
+  auto gate_row = [&](int i) {
+    return reinterpret_cast<float*>(lds + Cfg::OFF_G + i * Cfg::GATE_BYTES);
   };
+  auto next = [](int i) { return i == 2 ? 0 : i + 1; };
 
   if (wave >= W + kScoreWaves) {  // ---- copy waves
     if (chunks == 0) return;
@@ -261,27 +291,58 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
     const char* ys = rows(p.y, KD, 0);
     const char* ws = rows(p.w, p.od, slice * Cfg::VS);
     const size_t xst = p.x.stride * ES, yst = p.y.stride * ES, wst = p.w.stride * ES;
-    // Rows past the end of a short chunk repeat its last token: nothing outside
-    // the sequence is read, and their factors are zero.
-    auto copy_rows = [&](int s, const char* src, size_t stride, unsigned char* to, auto ch) {
+    // Byte offsets of this lane's 16-byte pieces inside a chunk: 64 rows apart
+    // they stay below 2^32 (strides are at most 2^24 elements).  In a chunk
+    // shorter than C the rows past its end repeat its last token: nothing
+    // outside the sequence is read, and their factors are zero.
+    constexpr int NX = C * Cfg::CHK / 64 / kCopyWaves, NW = C * Cfg::CHV / 64 / kCopyWaves;
+    uint32_t xo[NX], yo[NX], wo[NW];
+    auto piece = [&](int i, auto ch, int len, size_t stride) {
       constexpr int CH = decltype(ch)::value;
+      const int q = 64 * (cw + kCopyWaves * i) + lane, r = q / CH, pc = q % CH;
+      return static_cast<uint32_t>((r < len ? r : len - 1) * stride + 16 * (pc ^ perm<CH>(r)));
+    };
+    const std::integral_constant<int, Cfg::CHK> chk;
+    const std::integral_constant<int, Cfg::CHV> chv;
+#pragma unroll
+    for (int i = 0; i < NX; ++i) {
+      xo[i] = piece(i, chk, C, xst);
+      yo[i] = piece(i, chk, C, yst);
+    }
+#pragma unroll
+    for (int i = 0; i < NW; ++i) wo[i] = piece(i, chv, C, wst);
+    auto copy_xy = [&](int s, int buf) {
       int tok;
       const int len = chunk_at(s, tok);
-      const char* base = src + static_cast<size_t>(tok) * stride;
+      const char* xb = xs + static_cast<size_t>(tok) * xst;
+      const char* yb = ys + static_cast<size_t>(tok) * yst;
+      unsigned char* to = x_tile(buf) + 1024 * cw;
+      if (len == C) {
 #pragma unroll
-      for (int i = 0; i < C * CH / 64 / kCopyWaves; ++i) {
-        const int q = 64 * (cw + kCopyWaves * i) + lane, r = q / CH, pc = q % CH;
-        const int rr = r < len ? r : len - 1;
-        copy16(base + rr * stride + 16 * (pc ^ perm<CH>(r)), to + 1024 * (cw + kCopyWaves * i));
+        for (int i = 0; i < NX; ++i) {
+          copy16(xb + xo[i], to + 1024 * kCopyWaves * i);
+          copy16(yb + yo[i], to + Cfg::X_BYTES + 1024 * kCopyWaves * i);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+          copy16(xb + piece(i, chk, len, xst), to + 1024 * kCopyWaves * i);
+          copy16(yb + piece(i, chk, len, yst), to + Cfg::X_BYTES + 1024 * kCopyWaves * i);
+        }
       }
     };
-    auto copy_xy = [&](int s) {
-      copy_rows(s, xs, xst, x_tile(s), std::integral_constant<int, Cfg::CHK>());
-      copy_rows(s, ys, yst, x_tile(s) + Cfg::X_BYTES, std::integral_constant<int, Cfg::CHK>());
-    };
     auto copy_w = [&](int s) {
-      copy_rows(s, ws, wst, lds + Cfg::OFF_W + (s & 1) * Cfg::W_BYTES,
-                std::integral_constant<int, Cfg::CHV>());
+      int tok;
+      const int len = chunk_at(s, tok);
+      const char* wb = ws + static_cast<size_t>(tok) * wst;
+      unsigned char* to = lds + Cfg::OFF_W + (s & 1) * Cfg::W_BYTES + 1024 * cw;
+      if (len == C) {
+#pragma unroll
+        for (int i = 0; i < NW; ++i) copy16(wb + wo[i], to + 1024 * kCopyWaves * i);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NW; ++i) copy16(wb + piece(i, chv, len, wst), to + 1024 * kCopyWaves * i);
+      }
     };
     auto load_gate = [&](int s) {
       if (cw != 0) return 0.f;
@@ -291,7 +352,7 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
       return lane < len ? b.gates.g[static_cast<size_t>(tok + lane) * b.H + h] : 0.f;
     };
     // Prefix sums in fp64, so that a decay's error does not grow with |G|.
-    auto put_gates = [&](int s, float gate) {
+    auto put_gates = [&](int s, int buf, float gate) {
       if (cw != 0) return;
       int tok;
       const int len = chunk_at(s, tok);
@@ -308,7 +369,7 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
       }
       G *= 1.4426950408889634;
       const double end = __shfl(G, C - 1);
-      float* f = gate_row(s);
+      float* f = gate_row(buf);
       if (lane < C) {
         const float hi = static_cast<float>(G), lo = static_cast<float>(G - hi);
         const float from = exp2f(hi) * fmaf(lo, 0.69314718f, 1.f);
@@ -321,21 +382,21 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
       }
     };
     const float g0 = load_gate(0), g1 = chunks > 1 ? load_gate(1) : 0.f;
-    copy_xy(0);
+    copy_xy(0, 0);
     copy_w(0);
-    if (chunks > 1) copy_xy(1);
-    put_gates(0, g0);
-    if (chunks > 1) put_gates(1, g1);
+    if (chunks > 1) copy_xy(1, 1);
+    put_gates(0, 0, g0);
+    if (chunks > 1) put_gates(1, 1, g1);
     __builtin_amdgcn_s_waitcnt(0);
     bare_barrier();
     bare_barrier();
-    for (int s = 0; s < chunks; ++s) {
+    for (int s = 0, buf = 2; s < chunks; ++s, buf = next(buf)) {
       float gate = 0.f;
       if (s + 2 < chunks) gate = load_gate(s + 2);
       if (s + 1 < chunks) copy_w(s + 1);
       if (s + 2 < chunks) {
-        copy_xy(s + 2);
-        put_gates(s + 2, gate);
+        copy_xy(s + 2, buf);
+        put_gates(s + 2, buf, gate);
       }
       __builtin_amdgcn_s_waitcnt(0);
       bare_barrier();
@@ -366,36 +427,40 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
         tts[i] = NT - 1 - tts[i];
         sts[i] = NT - 1 - sts[i];
       }
-    const float ps = p.us * p.os;
-    auto scores = [&](int s) {
+    // the scale goes into the exponent: log2 of its size, and its sign
+    const float ps = p.us * p.os, ps2 = __builtin_amdgcn_logf(fabsf(ps));
+    int kl[KB];
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) kl[kb] = row_lane<Cfg::CHK>(c, g, kb);
+    auto scores = [&](int s, int buf) {
       int tok;
       const int len = chunk_at(s, tok);
-      const unsigned char *X = x_tile(s), *Y = X + Cfg::X_BYTES;
-      const float* gate = gate_row(s);
+      const unsigned char *X = x_tile(buf), *Y = X + Cfg::X_BYTES;
+      const float* gate = gate_row(buf);
       float* diag = reinterpret_cast<float*>(lds + Cfg::OFF_DIAG) + (s & 1) * C;
       floatx4 acc[PER];
 #pragma unroll
       for (int i = 0; i < PER; ++i) acc[i] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
-        Frag<IN> xf = row_frag<IN, Cfg::CHK>(X, 16 * tts[0] + c, kb, g);
+        Frag<IN> xf = row_frag<IN, Cfg::CHK>(X, 16 * tts[0], kb, c, g, kl[kb]);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-          if (i == 2) xf = row_frag<IN, Cfg::CHK>(X, 16 * tts[i] + c, kb, g);
-          acc[i] = mma(row_frag<IN, Cfg::CHK>(Y, 16 * sts[i] + c, kb, g), xf, acc[i]);
+          if (i == 2) xf = row_frag<IN, Cfg::CHK>(X, 16 * tts[i], kb, c, g, kl[kb]);
+          acc[i] = mma(row_frag<IN, Cfg::CHK>(Y, 16 * sts[i], kb, c, g, kl[kb]), xf, acc[i]);
         }
       }
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         const int t = 16 * tts[i] + c, s4 = 16 * sts[i] + 4 * g;
-        const float gh = gate[t], gl = gate[C + t];
+        const float gh = gate[t], gl = BACK ? gate[C + t] - ps2 : gate[C + t] + ps2;
         const floatx4 sh = *reinterpret_cast<const floatx4*>(gate + s4);
         const floatx4 sl = *reinterpret_cast<const floatx4*>(gate + C + s4);
         float v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float d = (gh - sh[e]) + (gl - sl[e]);
-          const float x = acc[i][e] * ps * __builtin_amdgcn_exp2f(BACK ? -d : d);
+          const float x = (ps < 0.f ? -acc[i][e] : acc[i][e]) * __builtin_amdgcn_exp2f(BACK ? -d : d);
           const int sc = s4 + e;
           if (DOT && sc == t) diag[t] = x;
           const bool in = BACK ? (DOT ? sc > t : sc >= t) && sc < len : (DOT ? sc < t : sc <= t);
@@ -417,10 +482,10 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
       }
     };
     bare_barrier();
-    scores(0);
+    scores(0, 0);
     lds_barrier();
-    for (int s = 0; s < chunks; ++s) {
-      if (s + 1 < chunks) scores(s + 1);
+    for (int s = 0, buf = 1; s < chunks; ++s, buf = next(buf)) {
+      if (s + 1 < chunks) scores(s + 1, buf);
       lds_barrier();
     }
     return;
@@ -448,13 +513,19 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
   const uint32_t out_row = static_cast<uint32_t>(b.H * p.od * out_es);
   const uint32_t out_lane = c * out_row + static_cast<uint32_t>(4 * g * out_es);
   const size_t e_col = DOT ? static_cast<size_t>(h / p.e.group) * p.od + od + 4 * g : 0;
-  for (int s = 0; s < chunks; ++s) {
+  int kl[KB], jl[KD / 32];
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb) {
+    kl[kb] = row_lane<Cfg::CHK>(c, g, kb);
+    jl[kb] = col_lane<Cfg::CHK>(c, g, kb);
+  }
+  for (int s = 0, buf = 0; s < chunks; ++s, buf = next(buf)) {
     int tok;
     const int len = chunk_at(s, tok);
-    const unsigned char *X = x_tile(s), *Y = X + Cfg::X_BYTES;
+    const unsigned char *X = x_tile(buf), *Y = X + Cfg::X_BYTES;
     const unsigned char* Wt = lds + Cfg::OFF_W + (s & 1) * Cfg::W_BYTES;
     const unsigned char* P = lds + Cfg::OFF_P + (s & 1) * Cfg::P_BYTES;
-    const float* gate = gate_row(s);
+    const float* gate = gate_row(buf);
     const float* diag = reinterpret_cast<const float*>(lds + Cfg::OFF_DIAG) + (s & 1) * C;
 
     // the rows to dot with the outputs: loaded first, used last
@@ -474,7 +545,7 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
     for (int tt = 0; tt < NT; ++tt) o[tt] = floatx4{0.f, 0.f, 0.f, 0.f};
     Frag<IN> xf[2][NT];
 #pragma unroll
-    for (int tt = 0; tt < NT; ++tt) xf[0][tt] = row_frag<IN, Cfg::CHK>(X, 16 * tt + c, 0, g);
+    for (int tt = 0; tt < NT; ++tt) xf[0][tt] = row_frag<IN, Cfg::CHK>(X, 16 * tt, 0, c, g, kl[0]);
     Frag<IN> wf[NB];
     Planes<IN, PZ> pf[Cfg::FRAGS];
 #pragma unroll
@@ -482,11 +553,11 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
       if (kb + 1 < KB) {
 #pragma unroll
         for (int tt = 0; tt < NT; ++tt)
-          xf[(kb + 1) & 1][tt] = row_frag<IN, Cfg::CHK>(X, 16 * tt + c, kb + 1, g);
+          xf[(kb + 1) & 1][tt] = row_frag<IN, Cfg::CHK>(X, 16 * tt, kb + 1, c, g, kl[kb + 1]);
       } else {
 #pragma unroll
         for (int sb = 0; sb < NB; ++sb)
-          wf[sb] = col_frag<IN, Cfg::CHV, false>(Wt, 32 * sb, 16 * wave, c, g);
+          wf[sb] = col_frag_narrow<IN, Cfg::CHV>(Wt, 32 * sb, 16 * wave, c, g);
 #pragma unroll
         for (int i = 0; i < Cfg::FRAGS; ++i) {
           const unsigned char* from = P + i * PL * Cfg::FRAG;
@@ -533,7 +604,7 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
       const int sb = i / (KD / 16 / JG), j0 = i % (KD / 16 / JG) * JG;
 #pragma unroll
       for (int j = 0; j < JG; ++j)
-        f[j] = col_frag<IN, Cfg::CHK, true>(Y, 32 * sb, 32 * ((j0 + j) >> 1) + 4 * (j & 1), c, g);
+        f[j] = col_frag_wide<IN, Cfg::CHK>(Y, 32 * sb, (j0 + j) >> 1, j & 1, c, g, jl[(j0 + j) >> 1]);
     };
     read_y(0, yf[0]);
     Planes<IN, 3> up[NB];
@@ -576,9 +647,7 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
     }
     char* out = static_cast<char*>(p.out) +
                 ((static_cast<size_t>(tok) * b.H + h) * p.od + od) * out_es;
-#pragma unroll
-    for (int tt = 0; tt < NT; ++tt) {
-      if (16 * tt + c >= len) continue;
+    auto store = [&](int tt) {
       const uint32_t at = out_lane + 16 * tt * out_row;
       if (p.out_dtype == 0) {
         uint32_t lo[1], hi[1];
@@ -588,6 +657,14 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
       } else {
         *reinterpret_cast<floatx4*>(out + at) = o[tt];
       }
+    };
+    if (len == C) {
+#pragma unroll
+      for (int tt = 0; tt < NT; ++tt) store(tt);
+    } else {
+#pragma unroll
+      for (int tt = 0; tt < NT; ++tt)
+        if (16 * tt + c < len) store(tt);
     }
     lds_barrier();  // the chunk is done
   }

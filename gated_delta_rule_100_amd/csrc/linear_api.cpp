@@ -54,9 +54,9 @@ gdr_status check_common(const char* who, int tokens, int N, int H, int Hk, int d
       {vs, static_cast<int64_t>(H) * dv, "v_stride"}};
   for (auto& r : rows) {
     if (*r.s == 0) *r.s = r.width;
-    if (*r.s < r.width || *r.s % per16 != 0 || *r.s > (int64_t{1} << 31))
-      return fail(GDR_ERR_INVALID_ARG, "%s: %s=%lld must be 0 or at least %lld and a multiple of %lld", who,
-                  r.name, static_cast<long long>(*r.s), static_cast<long long>(r.width),
+    if (*r.s < r.width || *r.s % per16 != 0 || *r.s > (int64_t{1} << 24))
+      return fail(GDR_ERR_INVALID_ARG,
+                  "%s: %s=%lld must be 0 or from %lld to 2^24 and a multiple of %lld", who, r.name, static_cast<long long>(*r.s), static_cast<long long>(r.width),
                   static_cast<long long>(per16));
   }
   for (const void* p : ptrs)

@@ -303,8 +303,8 @@ gdr_status gdr_state_fixup(const float* L, const float* M, const float* state_in
  *   - q, k and v may be slices of wider token rows: q_stride, k_stride and
  *     v_stride are the elements from one token's row to the next, 0 for dense
  *     ([T, heads, d] contiguous).  The heads of one token are always
- *     contiguous, and a stride is a multiple of 16 bytes and not below the
- *     heads' width.
+ *     contiguous, and a stride is a multiple of 16 bytes, not below the heads'
+ *     width and at most 2^24 elements.
  *   - cu_seqlens[N] may be below T_total: rows behind the last sequence are
  *     neither read nor written.
  *   - An infinity or NaN in a token's q, k or v may make the outputs of its
