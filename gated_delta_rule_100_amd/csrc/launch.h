@@ -148,8 +148,19 @@ struct LinearGates {
   int per_token;
 };
 
-// One pass of the recurrence over packed sequences, in either direction.  With
-// a state Z [od, kd] per (sequence, head), rows x, y of kd and w of od values:
+// A packed batch, and the units its passes walk: the sequences (seg == 0,
+// units = N), or segments of seg tokens of them (launch_layout with seg as its
+// chunk: seg_offs [N + 1], seg_idx [units][2], slots past the real count -1).
+struct LinearBatch {
+  const int32_t* cu;
+  int N, H, T_total, in_dtype;
+  LinearGates gates;
+  int seg, units;
+  const int32_t *seg_offs, *seg_idx;
+};
+
+// One pass of the recurrence over every unit, in either direction.  With a
+// state Z [od, kd] per (unit, head), rows x, y of kd and w of od values:
 //   forward:   Z_t = alpha_t Z_{t-1} + us w_t y_t^T,  out_t = os Z_t x_t
 //   backward:  Z_t = alpha_{t+1} Z_{t+1} + us w_t y_t^T,  out_t = os Z_t x_t
 // The prompt pass is (x, y, w) = (q, k, v) forward; the gradients are
@@ -167,20 +178,15 @@ struct LinearPass {
   void* out;           // [T, H, od]
   float* dot;          // [od / 16][H][T] partial sums of e_t . out_t without the
                        // token's own term, or NULL
-  const float* start;  // states the walk starts from, NULL for zero
-  float* end;          // states at the end of the walk, NULL: not written
-  const float* end_with;  // states to dot with those at the end, or NULL
-  float* end_dot;         // [od / 16][N * H] partial sums of that dot product
+  const float* start;  // [units * H] states the walks start from, NULL for zero
+  float* end;          // [N * H] states where the last walk of a sequence ends,
+                       // NULL: not written; not written for sequences without units
+  const float* end_with;  // [units * H] states to dot with those at a walk's end, or NULL
+  float* end_dot;         // [od / 16][units * H] partial sums of that dot product
   int64_t row, col;    // element strides of a state row and column, in start,
-                       // end and end_with ([N * H] states of od * kd elements)
+                       // end and end_with (od * kd elements a state)
   float us, os;
   int od, kd, backward, out_dtype;
-};
-
-struct LinearBatch {
-  const int32_t* cu;
-  int N, H, T_total, in_dtype;
-  LinearGates gates;
 };
 
 hipError_t launch_linear_decode(const void* q, const void* k, const void* v,
@@ -190,14 +196,25 @@ hipError_t launch_linear_decode(const void* q, const void* k, const void* v,
 
 hipError_t launch_linear_pass(const LinearBatch& b, const LinearPass& p, hipStream_t stream);
 
-// dg_t = dg_{t+1} + row_t - col_t, starting from the end's dot product; row and
-// col are [parts][H][T] partial sums, end_dot [parts][N * H].
+// States at the start of every segment's walk, [units * H] of od rows and kd
+// columns: the segments' own states from zero (y, w, us as in a pass) and their
+// decays [units * H], then the chain over each sequence's segments from `from`
+// ([N * H], NULL for zero).  last ([N * H] or NULL) gets `from` where a sequence
+// has no tokens.
+hipError_t launch_linear_starts(const LinearBatch& b, const LinearRows& y, const LinearRows& w,
+                                float us, int od, int kd, int backward, const float* from,
+                                float* states, float* decays, float* last, hipStream_t stream);
+
+// dg_t = dg_{t+1} + row_t - col_t over every unit, from its end's dot product;
+// row and col are [parts][H][T] partial sums, end_dot [parts][units * H].
+// dg_t goes to dg ([T, H]), or its sum over the unit's tokens to unit_sum
+// ([units * H]).
 hipError_t launch_linear_dg(const LinearBatch& b, const float* row, int row_parts,
                             const float* col, int col_parts, const float* end_dot, int end_parts,
-                            float* dg, hipStream_t stream);
+                            float* dg, double* unit_sum, hipStream_t stream);
 
-// dg[h] = sum over tokens of dg_t, [T, H] -> [H].
-hipError_t launch_linear_dg_heads(const LinearBatch& b, const float* dg_t, float* dg,
+// dg[h] = sum over units of unit_sum.
+hipError_t launch_linear_dg_heads(const LinearBatch& b, const double* unit_sum, float* dg,
                                   hipStream_t stream);
 
 // Sum of [T, H, d] fp32 over groups of heads to [T, H / group, d] of out_dtype,

@@ -30,6 +30,33 @@ __device__ __forceinline__ void token_range(const LinearBatch& b, int n, int& tb
   te = te < tb ? tb : (te > b.T_total ? b.T_total : te);
 }
 
+// Sequence and tokens [tb, te) of a unit, and whether it is the first and the
+// last of its sequence; false for a slot without a segment.
+struct Unit {
+  int n, tb, te;
+  bool first, last;
+};
+__device__ __forceinline__ bool unit_at(const LinearBatch& b, int u, Unit& r) {
+  if (b.seg == 0) {
+    r.n = u;
+    r.first = r.last = true;
+    token_range(b, u, r.tb, r.te);
+    return true;
+  }
+  r.n = b.seg_idx[2 * u];
+  const int j = b.seg_idx[2 * u + 1];
+  if (r.n < 0 || r.n >= b.N || j < 0) return false;
+  int tb, te;
+  token_range(b, r.n, tb, te);
+  const int64_t from = tb + static_cast<int64_t>(j) * b.seg;
+  if (from >= te) return false;
+  r.tb = static_cast<int>(from);
+  r.te = te - r.tb < b.seg ? te : r.tb + b.seg;
+  r.first = j == 0;
+  r.last = r.te == te;
+  return true;
+}
+
 // ---- operands
 //
 // A fragment is eight elements of the contraction index for one row or column
@@ -197,6 +224,37 @@ __device__ __forceinline__ void copy16(const void* src, void* lds) {
                                    (__attribute__((address_space(3))) void*)(lds), 16, 0, 0);
 }
 
+// Gate factors of a chunk, one token a lane: G in log2 units as hi + lo, e^G,
+// e^{G_C - G} and e^{G_C}.  Prefix sums in fp64, so that the error of a decay
+// does not grow with |G|.
+struct Gates {
+  float hi, lo, from_start, to_end, all;
+};
+template <int C>
+__device__ __forceinline__ Gates chunk_gates(float gate, bool per_token, int lane, int len) {
+  double G;
+  if (per_token) {
+    G = lane < len ? static_cast<double>(clamp_gate(gate)) : 0.0;
+#pragma unroll
+    for (int d = 1; d < C; d <<= 1) {
+      const double up = __shfl_up(G, d);
+      if (lane >= d) G += up;
+    }
+  } else {
+    G = static_cast<double>(clamp_gate(gate)) * (lane < len ? lane + 1 : len);
+  }
+  G *= 1.4426950408889634;
+  const double end = __shfl(G, C - 1);
+  Gates r;
+  r.hi = static_cast<float>(G);
+  r.lo = static_cast<float>(G - r.hi);
+  r.from_start = exp2f(r.hi) * fmaf(r.lo, 0.69314718f, 1.f);
+  r.to_end = exp2f(static_cast<float>(end - G));
+  const float eh = static_cast<float>(end), el = static_cast<float>(end - eh);
+  r.all = exp2f(eh) * fmaf(el, 0.69314718f, 1.f);
+  return r;
+}
+
 // ---- the chunk scan
 //
 // One workgroup per (unit, head, 16 W columns of w): a unit is a sequence, or a
@@ -264,10 +322,11 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
   // the workgroups of one (unit, head) read the same x and y rows: one XCD
   const int slices = p.od / Cfg::VS, xcd = blockIdx.x % kXcds, k0 = blockIdx.x / kXcds;
   const int slice = k0 % slices, pair = (k0 / slices) * kXcds + xcd;
-  if (pair >= b.N * b.H) return;
-  const int n = pair / b.H, h = pair % b.H;
-  int tb, te;
-  token_range(b, n, tb, te);
+  if (pair >= b.units * b.H) return;
+  const int h = pair % b.H;
+  Unit unit;
+  if (!unit_at(b, pair / b.H, unit)) return;
+  const int tb = unit.tb, te = unit.te;
   const int chunks = (te - tb + C - 1) / C;
   // token range of the s-th chunk of the walk
   auto chunk_at = [&](int s, int& tok) {
@@ -351,34 +410,18 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
       if (!b.gates.per_token) return b.gates.g[h];
       return lane < len ? b.gates.g[static_cast<size_t>(tok + lane) * b.H + h] : 0.f;
     };
-    // Prefix sums in fp64, so that a decay's error does not grow with |G|.
     auto put_gates = [&](int s, int buf, float gate) {
       if (cw != 0) return;
       int tok;
       const int len = chunk_at(s, tok);
-      double G;
-      if (b.gates.per_token) {
-        G = lane < len ? static_cast<double>(clamp_gate(gate)) : 0.0;
-#pragma unroll
-        for (int d = 1; d < C; d <<= 1) {
-          const double up = __shfl_up(G, d);
-          if (lane >= d) G += up;
-        }
-      } else {
-        G = static_cast<double>(clamp_gate(gate)) * (lane < len ? lane + 1 : len);
-      }
-      G *= 1.4426950408889634;
-      const double end = __shfl(G, C - 1);
       float* f = gate_row(buf);
+      const Gates v = chunk_gates<C>(gate, b.gates.per_token, lane, len);
       if (lane < C) {
-        const float hi = static_cast<float>(G), lo = static_cast<float>(G - hi);
-        const float from = exp2f(hi) * fmaf(lo, 0.69314718f, 1.f);
-        const float to = exp2f(static_cast<float>(end - G));
-        f[lane] = hi;
-        f[C + lane] = lo;
-        f[2 * C + lane] = p.os * (BACK ? to : from);
-        f[3 * C + lane] = lane < len ? p.us * (BACK ? from : to) : 0.f;
-        if (lane == 0) f[4 * C] = exp2f(static_cast<float>(end));
+        f[lane] = v.hi;
+        f[C + lane] = v.lo;
+        f[2 * C + lane] = p.os * (BACK ? v.to_end : v.from_start);
+        f[3 * C + lane] = lane < len ? p.us * (BACK ? v.from_start : v.to_end) : 0.f;
+        if (lane == 0) f[4 * C] = v.all;
       }
     };
     const float g0 = load_gate(0), g1 = chunks > 1 ? load_gate(1) : 0.f;
@@ -670,59 +713,267 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
   }
 
   float ed = 0.f;
+  const bool ends = p.end && (BACK ? unit.first : unit.last);
+  const size_t ebase = (static_cast<size_t>(unit.n) * b.H + h) * p.od * KD + (od + c) * p.row;
 #pragma unroll
   for (int j = 0; j < KD / 16; ++j)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const size_t at = zbase + (32 * (j >> 1) + 8 * g + 4 * (j & 1) + e) * p.col;
-      if (p.end_with) ed = fmaf(z[j][e], p.end_with[at], ed);
-      if (p.end) p.end[at] = z[j][e];
+      const size_t at = (32 * (j >> 1) + 8 * g + 4 * (j & 1) + e) * p.col;
+      if (p.end_with) ed = fmaf(z[j][e], p.end_with[zbase + at], ed);
+      if (ends) p.end[ebase + at] = z[j][e];
     }
   if (p.end_with) {
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) ed += __shfl_xor(ed, d);
-    if (lane == 0) p.end_dot[static_cast<size_t>(od / 16) * b.N * b.H + pair] = ed;
+    if (lane == 0) p.end_dot[static_cast<size_t>(od / 16) * b.units * b.H + pair] = ed;
   }
 }
 
+// ---- states at the starts of segments
+//
+// A segment's own state, from zero: the update of the scan alone, so the copy
+// waves bring y and w rows only.
+template <Dt IN, int KD, int W>
+struct LocalCfg {
+  static constexpr int ES = IN == Dt::BF16 ? 2 : 4;
+  static constexpr int C = IN == Dt::BF16 ? 64 : 32;
+  static constexpr int NB = C / 32;
+  static constexpr int VS = 16 * W;
+  static constexpr int CHK = KD * ES / 16, CHV = VS * ES / 16;
+  static constexpr int THREADS = 64 * (W + kCopyWaves);
+  static constexpr int Y_BYTES = C * KD * ES, W_BYTES = C * VS * ES;
+  static constexpr int BUF = Y_BYTES + W_BYTES;
+  static constexpr int GATE_BYTES = (C + 4) * 4;  // update factors, e^{G_C}
+  static constexpr int OFF_G = 2 * BUF;
+  static constexpr int BYTES = OFF_G + 2 * GATE_BYTES;
+  static_assert(BYTES <= 160 * 1024, "LDS");
+};
+
+template <Dt IN, int KD, int W, bool BACK>
+__global__ __launch_bounds__(64 * (W + kCopyWaves)) void linear_local_kernel(
+    LinearBatch b, LinearRows y, LinearRows w, float us, int od_all, float* states, float* decays) {
+  using Cfg = LocalCfg<IN, KD, W>;
+  constexpr int C = Cfg::C, NB = Cfg::NB, ES = Cfg::ES;
+  __shared__ __align__(1024) unsigned char lds[Cfg::BYTES];
+  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int slices = od_all / Cfg::VS, xcd = blockIdx.x % kXcds, k0 = blockIdx.x / kXcds;
+  const int slice = k0 % slices, pair = (k0 / slices) * kXcds + xcd;
+  if (pair >= b.units * b.H) return;
+  const int h = pair % b.H;
+  Unit unit;
+  if (!unit_at(b, pair / b.H, unit)) return;
+  if (BACK ? unit.first : unit.last) return;  // nothing starts from its end
+  const int tb = unit.tb, te = unit.te, chunks = (te - tb + C - 1) / C;
+  auto chunk_at = [&](int s, int& tok) {
+    tok = tb + (BACK ? chunks - 1 - s : s) * C;
+    return te - tok < C ? te - tok : C;
+  };
+  if (wave >= W) {  // ---- copy waves
+    const int cw = wave - W;
+    const char* ys = static_cast<const char*>(y.p) + static_cast<size_t>(h / y.group) * KD * ES;
+    const char* ws = static_cast<const char*>(w.p) +
+                     (static_cast<size_t>(h / w.group) * od_all + slice * Cfg::VS) * ES;
+    const size_t yst = y.stride * ES, wst = w.stride * ES;
+    constexpr int NY = C * Cfg::CHK / 64 / kCopyWaves, NW = C * Cfg::CHV / 64 / kCopyWaves;
+    auto piece = [&](int i, auto ch, int len, size_t stride) {
+      constexpr int CH = decltype(ch)::value;
+      const int q = 64 * (cw + kCopyWaves * i) + lane, r = q / CH, pc = q % CH;
+      return static_cast<uint32_t>((r < len ? r : len - 1) * stride + 16 * (pc ^ perm<CH>(r)));
+    };
+    const std::integral_constant<int, Cfg::CHK> chk;
+    const std::integral_constant<int, Cfg::CHV> chv;
+    uint32_t yo[NY], wo[NW];
+#pragma unroll
+    for (int i = 0; i < NY; ++i) yo[i] = piece(i, chk, C, yst);
+#pragma unroll
+    for (int i = 0; i < NW; ++i) wo[i] = piece(i, chv, C, wst);
+    auto bring = [&](int s) {
+      int tok;
+      const int len = chunk_at(s, tok);
+      float gate = 0.f;
+      if (cw == 0) {
+        if (!b.gates.per_token) gate = b.gates.g[h];
+        else if (lane < len) gate = b.gates.g[static_cast<size_t>(tok + lane) * b.H + h];
+      }
+      const char* yb = ys + static_cast<size_t>(tok) * yst;
+      const char* wb = ws + static_cast<size_t>(tok) * wst;
+      unsigned char* to = lds + (s & 1) * Cfg::BUF + 1024 * cw;
+      if (len == C) {
+#pragma unroll
+        for (int i = 0; i < NY; ++i) copy16(yb + yo[i], to + 1024 * kCopyWaves * i);
+#pragma unroll
+        for (int i = 0; i < NW; ++i) copy16(wb + wo[i], to + Cfg::Y_BYTES + 1024 * kCopyWaves * i);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NY; ++i) copy16(yb + piece(i, chk, len, yst), to + 1024 * kCopyWaves * i);
+#pragma unroll
+        for (int i = 0; i < NW; ++i)
+          copy16(wb + piece(i, chv, len, wst), to + Cfg::Y_BYTES + 1024 * kCopyWaves * i);
+      }
+      if (cw == 0) {
+        const Gates v = chunk_gates<C>(gate, b.gates.per_token, lane, len);
+        float* f = reinterpret_cast<float*>(lds + Cfg::OFF_G + (s & 1) * Cfg::GATE_BYTES);
+        if (lane < C) f[lane] = lane < len ? us * (BACK ? v.from_start : v.to_end) : 0.f;
+        if (lane == 0) f[C] = v.all;
+      }
+      __builtin_amdgcn_s_waitcnt(0);
+    };
+    bring(0);
+    bare_barrier();
+    for (int s = 0; s < chunks; ++s) {
+      if (s + 1 < chunks) bring(s + 1);
+      bare_barrier();
+    }
+    return;
+  }
+  // ---- compute waves
+  const int od = slice * Cfg::VS + 16 * wave;
+  floatx4 z[KD / 16];
+#pragma unroll
+  for (int j = 0; j < KD / 16; ++j) z[j] = floatx4{0.f, 0.f, 0.f, 0.f};
+  float decay = 1.f;
+  int jl[KD / 32];
+#pragma unroll
+  for (int j = 0; j < KD / 32; ++j) jl[j] = col_lane<Cfg::CHK>(c, g, j);
+  bare_barrier();
+  for (int s = 0; s < chunks; ++s) {
+    const unsigned char* Y = lds + (s & 1) * Cfg::BUF;
+    const float* f = reinterpret_cast<const float*>(lds + Cfg::OFF_G + (s & 1) * Cfg::GATE_BYTES);
+    const float gc = f[C];
+    decay *= gc;
+#pragma unroll
+    for (int j = 0; j < KD / 16; ++j) z[j] *= gc;
+#pragma unroll
+    for (int sb = 0; sb < NB; ++sb) {
+      const Frag<IN> wf = col_frag_narrow<IN, Cfg::CHV>(Y + Cfg::Y_BYTES, 32 * sb, 16 * wave, c, g);
+      const floatx4 f0 = *reinterpret_cast<const floatx4*>(f + 32 * sb + 4 * g);
+      const floatx4 f1 = *reinterpret_cast<const floatx4*>(f + 32 * sb + 16 + 4 * g);
+      float u[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        u[e] = frag_value(wf, e) * f0[e];
+        u[4 + e] = frag_value(wf, 4 + e) * f1[e];
+      }
+      const Planes<IN, 3> up = to_planes<IN, 3>(u);
+#pragma unroll
+      for (int j0 = 0; j0 < KD / 16; j0 += 4) {
+        Frag<IN> yf[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          yf[j] = col_frag_wide<IN, Cfg::CHK>(Y, 32 * sb, (j0 + j) >> 1, j & 1, c, g, jl[(j0 + j) >> 1]);
+#pragma unroll
+        for (int q = Planes<IN, 3>::N - 1; q >= 0; --q)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) z[j0 + j] = mma(yf[j], up.p[q], z[j0 + j]);
+      }
+    }
+    lds_barrier();
+  }
+  float* to = states + (static_cast<size_t>(pair) * od_all + od + c) * KD;
+#pragma unroll
+  for (int j = 0; j < KD / 16; ++j)
+    *reinterpret_cast<floatx4*>(to + 32 * (j >> 1) + 8 * g + 4 * (j & 1)) = z[j];
+  if (od == 0 && lane == 0) decays[pair] = decay;
+}
+
+// The chain over a sequence's segments, elementwise: states[u] becomes the state
+// in front of segment u's walk.  One thread has four elements; kAhead segments
+// are read before the first is needed.
+constexpr int kAhead = 8;
+template <bool BACK>
+__global__ __launch_bounds__(256) void linear_starts_kernel(LinearBatch b, int per, const float* from,
+                                                            float* states, const float* decays,
+                                                            float* last) {
+  const int blocks = per / 1024, nh = blockIdx.x / blocks;
+  const int n = nh / b.H, h = nh % b.H;
+  const size_t at = (blockIdx.x % blocks) * 1024 + 4 * threadIdx.x;
+  int u0 = b.seg_offs[n], u1 = b.seg_offs[n + 1];
+  u0 = u0 < 0 ? 0 : (u0 > b.units ? b.units : u0);
+  u1 = u1 < u0 ? u0 : (u1 > b.units ? b.units : u1);
+  const int count = u1 - u0;
+  floatx4 z = {0.f, 0.f, 0.f, 0.f};
+  if (from) z = *reinterpret_cast<const floatx4*>(from + static_cast<size_t>(nh) * per + at);
+  if (count == 0) {
+    if (last) *reinterpret_cast<floatx4*>(last + static_cast<size_t>(nh) * per + at) = z;
+    return;
+  }
+  for (int i0 = 0; i0 < count; i0 += kAhead) {
+    floatx4 own[kAhead];
+    float d[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (i0 + i >= count - 1) continue;  // the last walk's own state is not needed
+      const int u = BACK ? u1 - 1 - (i0 + i) : u0 + i0 + i;
+      const size_t pair = static_cast<size_t>(u) * b.H + h;
+      own[i] = *reinterpret_cast<const floatx4*>(states + pair * per + at);
+      d[i] = decays[pair];
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (i0 + i >= count) continue;
+      const int u = BACK ? u1 - 1 - (i0 + i) : u0 + i0 + i;
+      *reinterpret_cast<floatx4*>(states + (static_cast<size_t>(u) * b.H + h) * per + at) = z;
+      if (i0 + i < count - 1) z = d[i] * z + own[i];
+    }
+  }
+}
+
+// ---- gate gradient
+//
+// One wave a (unit, head): suffix sums of row - col, 64 tokens at a time from the
+// unit's end, in fp64.
 __global__ __launch_bounds__(64) void linear_dg_kernel(LinearBatch b, const float* row,
                                                        int row_parts, const float* col,
                                                        int col_parts, const float* end_dot,
-                                                       int end_parts, float* dg) {
-  const int nh = blockIdx.x * 64 + threadIdx.x;
-  if (nh >= b.N * b.H) return;
-  const int n = nh / b.H, h = nh % b.H;
-  int tb, te;
-  token_range(b, n, tb, te);
-  const size_t th = static_cast<size_t>(b.T_total) * b.H;
-  double acc = 0.;
-  if (end_dot)
-    for (int i = 0; i < end_parts; ++i) acc += end_dot[static_cast<size_t>(i) * b.N * b.H + nh];
-  for (int t = te - 1; t >= tb; --t) {
-    const size_t at = static_cast<size_t>(h) * b.T_total + t;
-    float r = 0.f, c = 0.f;
-    for (int i = 0; i < row_parts; ++i) r += row[i * th + at];
-    for (int i = 0; i < col_parts; ++i) c += col[i * th + at];
-    acc += r - c;
-    dg[static_cast<size_t>(t) * b.H + h] = static_cast<float>(acc);
+                                                       int end_parts, float* dg, double* unit_sum) {
+  const int pair = blockIdx.x, lane = threadIdx.x, h = pair % b.H;
+  Unit unit;
+  const bool real = unit_at(b, pair / b.H, unit);
+  double total = 0.0;
+  if (real) {
+    const size_t th = static_cast<size_t>(b.T_total) * b.H, units = static_cast<size_t>(b.units) * b.H;
+    double acc = 0.0;
+    if (end_dot)
+      for (int i = 0; i < end_parts; ++i) acc += end_dot[i * units + pair];
+    for (int hi = unit.te; hi > unit.tb; hi -= 64) {
+      const int t = hi - 1 - lane;  // lane 0 has the latest token
+      const bool in = t >= unit.tb;
+      double v = 0.0;
+      if (in) {
+        const size_t at = static_cast<size_t>(h) * b.T_total + t;
+        for (int i = 0; i < row_parts; ++i) v += row[i * th + at];
+        for (int i = 0; i < col_parts; ++i) v -= col[i * th + at];
+      }
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const double up = __shfl_up(v, d);
+        if (lane >= d) v += up;
+      }
+      v += acc;
+      acc = __shfl(v, 63);
+      if (in) {
+        total += v;
+        if (dg) dg[static_cast<size_t>(t) * b.H + h] = static_cast<float>(v);
+      }
+    }
+  }
+  if (unit_sum) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
+    if (lane == 0) unit_sum[pair] = total;
   }
 }
 
-__global__ __launch_bounds__(256) void linear_dg_heads_kernel(LinearBatch b, const float* dg_t,
-                                                              float* dg) {
-  const int h = blockIdx.x;
-  int te = b.cu[b.N];
-  te = te < 0 ? 0 : (te > b.T_total ? b.T_total : te);
-  double acc = 0;
-  for (int t = threadIdx.x; t < te; t += 256) acc += dg_t[static_cast<size_t>(t) * b.H + h];
-  __shared__ double part[256];
-  part[threadIdx.x] = acc;
-  __syncthreads();
-  for (int s = 128; s > 0; s >>= 1) {
-    if (threadIdx.x < s) part[threadIdx.x] += part[threadIdx.x + s];
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) dg[h] = static_cast<float>(part[0]);
+__global__ __launch_bounds__(64) void linear_dg_heads_kernel(LinearBatch b, const double* unit_sum,
+                                                             float* dg) {
+  const int h = blockIdx.x, lane = threadIdx.x;
+  double acc = 0.0;
+  for (int u = lane; u < b.units; u += 64) acc += unit_sum[static_cast<size_t>(u) * b.H + h];
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) acc += __shfl_xor(acc, d);
+  if (lane == 0) dg[h] = static_cast<float>(acc);
 }
 
 __global__ __launch_bounds__(256) void linear_group_sum_kernel(LinearBatch b, const float* part,
@@ -788,41 +1039,80 @@ hipError_t launch_linear_decode(const void* q, const void* k, const void* v,
                         : go(linear_decode_kernel<Dt::F32, Dt::F32>);
 }
 
+namespace {
+
+// Calls go(IN, KD) with the types of a pass.
+template <class F>
+hipError_t by_type(int in_dtype, int kd, F&& go) {
+  const std::integral_constant<Dt, Dt::BF16> bf16;
+  const std::integral_constant<Dt, Dt::F32> f32;
+  const std::integral_constant<int, 64> k64;
+  const std::integral_constant<int, 128> k128;
+  if (in_dtype == 0) return kd == 64 ? go(bf16, k64) : go(bf16, k128);
+  return kd == 64 ? go(f32, k64) : go(f32, k128);
+}
+
+unsigned scan_grid(const LinearBatch& b, int slices) {
+  return static_cast<unsigned>((b.units * b.H + kXcds - 1) / kXcds * kXcds) * slices;
+}
+
+}  // namespace
+
 hipError_t launch_linear_pass(const LinearBatch& b, const LinearPass& p, hipStream_t stream) {
-  auto go = [&](auto in, auto kd, auto dot, auto back) {
+  return by_type(b.in_dtype, p.kd, [&](auto in, auto kd) {
     constexpr Dt IN = decltype(in)::value;
     constexpr int KD = decltype(kd)::value, W = 4;
-    constexpr bool DOT = decltype(dot)::value, BACK = decltype(back)::value;
-    const int slices = p.od / (16 * W), pairs = (b.N * b.H + kXcds - 1) / kXcds * kXcds;
-    hipLaunchKernelGGL((linear_scan_kernel<IN, KD, W, DOT ? 3 : 2, DOT, BACK>), dim3(pairs * slices),
-                       dim3(64 * (W + kScoreWaves + kCopyWaves)), 0, stream, b, p);
-    return hipGetLastError();
-  };
-  auto by_way = [&](auto in, auto kd, auto dot) {
-    return p.backward ? go(in, kd, dot, std::true_type()) : go(in, kd, dot, std::false_type());
-  };
-  auto by_dot = [&](auto in, auto kd) {
-    return p.dot ? by_way(in, kd, std::true_type()) : by_way(in, kd, std::false_type());
-  };
-  auto by_kd = [&](auto in) {
-    return p.kd == 64 ? by_dot(in, std::integral_constant<int, 64>())
-                      : by_dot(in, std::integral_constant<int, 128>());
-  };
-  return b.in_dtype == 0 ? by_kd(std::integral_constant<Dt, Dt::BF16>())
-                         : by_kd(std::integral_constant<Dt, Dt::F32>());
+    auto go = [&](auto dot, auto back) {
+      constexpr bool DOT = decltype(dot)::value, BACK = decltype(back)::value;
+      hipLaunchKernelGGL((linear_scan_kernel<IN, KD, W, DOT ? 3 : 2, DOT, BACK>),
+                         dim3(scan_grid(b, p.od / (16 * W))),
+                         dim3(64 * (W + kScoreWaves + kCopyWaves)), 0, stream, b, p);
+      return hipGetLastError();
+    };
+    const std::true_type yes;
+    const std::false_type no;
+    if (p.dot) return p.backward ? go(yes, yes) : go(yes, no);
+    return p.backward ? go(no, yes) : go(no, no);
+  });
+}
+
+hipError_t launch_linear_starts(const LinearBatch& b, const LinearRows& y, const LinearRows& w,
+                                float us, int od, int kd, int backward, const float* from,
+                                float* states, float* decays, float* last, hipStream_t stream) {
+  hipError_t e = by_type(b.in_dtype, kd, [&](auto in, auto kdim) {
+    constexpr Dt IN = decltype(in)::value;
+    constexpr int KD = decltype(kdim)::value, W = 4;
+    auto go = [&](auto back) {
+      hipLaunchKernelGGL((linear_local_kernel<IN, KD, W, decltype(back)::value>),
+                         dim3(scan_grid(b, od / (16 * W))), dim3(64 * (W + kCopyWaves)), 0, stream,
+                         b, y, w, us, od, states, decays);
+      return hipGetLastError();
+    };
+    return backward ? go(std::true_type()) : go(std::false_type());
+  });
+  if (e != hipSuccess) return e;
+  const int per = od * kd;
+  const dim3 grid(static_cast<unsigned>(b.N) * b.H * (per / 1024));
+  if (backward)
+    hipLaunchKernelGGL(linear_starts_kernel<true>, grid, dim3(256), 0, stream, b, per, from, states,
+                       decays, last);
+  else
+    hipLaunchKernelGGL(linear_starts_kernel<false>, grid, dim3(256), 0, stream, b, per, from, states,
+                       decays, last);
+  return hipGetLastError();
 }
 
 hipError_t launch_linear_dg(const LinearBatch& b, const float* row, int row_parts,
                             const float* col, int col_parts, const float* end_dot, int end_parts,
-                            float* dg, hipStream_t stream) {
-  hipLaunchKernelGGL(linear_dg_kernel, dim3((b.N * b.H + 63) / 64), dim3(64), 0, stream, b, row,
-                     row_parts, col, col_parts, end_dot, end_parts, dg);
+                            float* dg, double* unit_sum, hipStream_t stream) {
+  hipLaunchKernelGGL(linear_dg_kernel, dim3(b.units * b.H), dim3(64), 0, stream, b, row, row_parts,
+                     col, col_parts, end_dot, end_parts, dg, unit_sum);
   return hipGetLastError();
 }
 
-hipError_t launch_linear_dg_heads(const LinearBatch& b, const float* dg_t, float* dg,
+hipError_t launch_linear_dg_heads(const LinearBatch& b, const double* unit_sum, float* dg,
                                   hipStream_t stream) {
-  hipLaunchKernelGGL(linear_dg_heads_kernel, dim3(b.H), dim3(256), 0, stream, b, dg_t, dg);
+  hipLaunchKernelGGL(linear_dg_heads_kernel, dim3(b.H), dim3(64), 0, stream, b, unit_sum, dg);
   return hipGetLastError();
 }
 

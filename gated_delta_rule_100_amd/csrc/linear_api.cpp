@@ -70,22 +70,82 @@ gdr_status hip_fail(hipError_t e, const char* who, const char* what) {
   return fail(GDR_ERR_HIP, "%s: %s: %s", who, what, hipGetErrorString(e));
 }
 
-// Workspace of the gradient: fp32 dq and dk of every value head when heads are
-// shared, the partial sums of dg, and dg of every token for one decay a head.
+// Tokens of a segment, or 0 to walk whole sequences.  Segments cost a second
+// read of y and w and their states' traffic, and make the walks short and even.
+int segment_tokens(int T_total, int N, int H, bool gradient) {
+  (void)N;
+  const int64_t th = static_cast<int64_t>(T_total) * H;
+  int seg = 512;
+  while (seg < 4096 && th / seg > 512) seg *= 2;
+  if (!gradient && static_cast<int64_t>(N) * H >= 512) return 0;
+  return T_total > seg ? seg : 0;
+}
+
+// Segment tables and states of `kinds` directions.
+struct SegmentSizes {
+  int seg = 0, units = 0;
+  size_t offs = 0, idx = 0, states = 0, decays = 0;
+  int kinds = 0;
+  size_t total() const { return offs + idx + kinds * (states + decays); }
+};
+
+SegmentSizes segment_sizes(int T_total, int N, int H, int dk, int dv, int kinds) {
+  SegmentSizes z;
+  z.seg = segment_tokens(T_total, N, H, kinds > 1);
+  z.units = z.seg ? T_total / z.seg + N : N;
+  if (!z.seg) return z;
+  z.kinds = kinds;
+  const size_t pairs = static_cast<size_t>(z.units) * H;
+  z.offs = align_up(sizeof(int32_t) * (static_cast<size_t>(N) + 1));
+  z.idx = align_up(sizeof(int32_t) * 2 * static_cast<size_t>(z.units));
+  z.states = align_up(sizeof(float) * pairs * dk * dv);
+  z.decays = align_up(sizeof(float) * pairs);
+  return z;
+}
+
+// Workspace of the gradient: segments, fp32 dq and dk of every value head when
+// heads are shared, the partial sums of dg, and its sums over units for one
+// decay a head.
 struct BackwardSizes {
-  size_t part_q = 0, part_k = 0, row = 0, col = 0, end = 0, dgt = 0;
-  size_t total() const { return part_q + part_k + row + col + end + dgt; }
+  SegmentSizes seg;
+  size_t part_q = 0, part_k = 0, row = 0, col = 0, end = 0, sums = 0;
+  size_t total() const { return seg.total() + part_q + part_k + row + col + end + sums; }
 };
 
 BackwardSizes backward_sizes(int T_total, int N, int H, int Hk, int dk, int dv) {
   BackwardSizes z;
+  z.seg = segment_sizes(T_total, N, H, dk, dv, 2);
   const size_t th = static_cast<size_t>(T_total) * H * sizeof(float);
+  const size_t pairs = static_cast<size_t>(z.seg.units) * H;
   if (H != Hk) z.part_q = z.part_k = align_up(th * dk);
   z.row = align_up(th * (dk / 16));
   z.col = align_up(th * (dv / 16));
-  z.end = align_up(static_cast<size_t>(N) * H * (dk / 16) * sizeof(float));
-  z.dgt = align_up(th);
+  z.end = align_up(pairs * (dk / 16) * sizeof(float));
+  z.sums = align_up(pairs * sizeof(double));
   return z;
+}
+
+// Workspace pieces in order.
+struct Carver {
+  char* at;
+  template <class T>
+  T* take(size_t bytes) {
+    T* p = reinterpret_cast<T*>(at);
+    at += bytes;
+    return p;
+  }
+};
+
+// Lays out the segments of a batch in the workspace.
+hipError_t make_segments(LinearBatch* b, const SegmentSizes& z, Carver* ws, hipStream_t st) {
+  b->seg = z.seg;
+  b->units = z.units;
+  if (!z.seg) return hipSuccess;
+  int32_t* offs = ws->take<int32_t>(z.offs);
+  int32_t* idx = ws->take<int32_t>(z.idx);
+  b->seg_offs = offs;
+  b->seg_idx = idx;
+  return gdr::launch_layout(b->cu, b->N, z.seg, offs, idx, z.units, st);
 }
 
 }  // namespace
@@ -111,8 +171,9 @@ gdr_status gdr_linear_decode(const void* q, const void* k, const void* v, const 
 
 size_t gdr_linear_prefill_workspace_bytes(int T_total, int N, int H, int dk, int dv,
                                           gdr_dtype in_dtype) {
-  (void)T_total; (void)N; (void)H; (void)dk; (void)dv; (void)in_dtype;
-  return 0;
+  if (T_total < 0 || N <= 0 || H <= 0 || !valid_dim(dk) || !valid_dim(dv) || !valid_dtype(in_dtype))
+    return 0;
+  return segment_sizes(T_total, N, H, dk, dv, 1).total();
 }
 
 gdr_status gdr_linear_prefill(const void* q, const void* k, const void* v, const float* g,
@@ -134,7 +195,12 @@ gdr_status gdr_linear_prefill(const void* q, const void* k, const void* v, const
     return fail(GDR_ERR_INVALID_ARG, "%s: workspace of %zu bytes, need %zu", who, workspace_bytes, need);
   s = check_device();
   if (s != GDR_OK) return s;
-  const LinearBatch b{cu_seqlens, N, H, T_total, in_dtype, {g, decay == GDR_DECAY_TOKEN}};
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  LinearBatch b{cu_seqlens, N, H, T_total, in_dtype, {g, decay == GDR_DECAY_TOKEN}};
+  const SegmentSizes z = segment_sizes(T_total, N, H, dk, dv, 1);
+  Carver ws{static_cast<char*>(workspace)};
+  hipError_t e = make_segments(&b, z, &ws, st);
+  if (e != hipSuccess) return hip_fail(e, who, "segments");
   LinearPass p{};
   p.x = {q, q_stride, H / Hk};
   p.y = {k, k_stride, H / Hk};
@@ -149,7 +215,15 @@ gdr_status gdr_linear_prefill(const void* q, const void* k, const void* v, const
   p.od = dv;
   p.kd = dk;
   p.out_dtype = out_dtype;
-  return hip_fail(gdr::launch_linear_pass(b, p, static_cast<hipStream_t>(stream)), who, "scan");
+  if (z.seg) {
+    float* states = ws.take<float>(z.states);
+    float* decays = ws.take<float>(z.decays);
+    e = gdr::launch_linear_starts(b, p.y, p.w, p.us, dv, dk, 0, state_in, states, decays, state_out,
+                                  st);
+    if (e != hipSuccess) return hip_fail(e, who, "segment states");
+    p.start = states;
+  }
+  return hip_fail(gdr::launch_linear_pass(b, p, st), who, "scan");
 }
 
 size_t gdr_linear_backward_workspace_bytes(int T_total, int N, int H, int Hk, int dk, int dv,
@@ -185,48 +259,63 @@ gdr_status gdr_linear_backward(const void* q, const void* k, const void* v, cons
   s = check_device();
   if (s != GDR_OK) return s;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  const LinearBatch b{cu_seqlens, N, H, T_total, in_dtype, {g, decay == GDR_DECAY_TOKEN}};
-  char* ws = static_cast<char*>(workspace);
-  auto take = [&](size_t bytes) {
-    float* f = reinterpret_cast<float*>(ws);
-    ws += bytes;
-    return f;
-  };
+  LinearBatch b{cu_seqlens, N, H, T_total, in_dtype, {g, decay == GDR_DECAY_TOKEN}};
+  Carver ws{static_cast<char*>(workspace)};
+  hipError_t e = make_segments(&b, z.seg, &ws, st);
+  if (e != hipSuccess) return hip_fail(e, who, "segments");
+  float *starts = nullptr, *ends = nullptr, *decays = nullptr, *decays_back = nullptr;
+  if (z.seg.seg) {
+    starts = ws.take<float>(z.seg.states);
+    ends = ws.take<float>(z.seg.states);
+    decays = ws.take<float>(z.seg.decays);
+    decays_back = ws.take<float>(z.seg.decays);
+  }
   const int group = H / Hk;
-  float* part_q = take(z.part_q);
-  float* part_k = take(z.part_k);
-  float* row = take(z.row);
-  float* col = take(z.col);
-  float* end = take(z.end);
-  float* dgt = take(z.dgt);
+  float* part_q = ws.take<float>(z.part_q);
+  float* part_k = ws.take<float>(z.part_k);
+  float* row = ws.take<float>(z.row);
+  float* col = ws.take<float>(z.col);
+  float* end = ws.take<float>(z.end);
+  double* sums = ws.take<double>(z.sums);
   const LinearRows rq{q, q_stride, group}, rk{k, k_stride, group}, rv{v, v_stride, 1},
       rd{d_o, static_cast<int64_t>(H) * dv, 1};
+  // states in front of every unit's walk: S forwards, R backwards
+  const float *from = state_in, *behind = dstate_out;
+  if (z.seg.seg) {
+    e = gdr::launch_linear_starts(b, rk, rv, 1.f, dv, dk, 0, state_in, starts, decays, nullptr, st);
+    if (e == hipSuccess)
+      e = gdr::launch_linear_starts(b, rq, rd, scale, dv, dk, 1, dstate_out, ends, decays_back,
+                                    dstate_in, st);
+    if (e != hipSuccess) return hip_fail(e, who, "segment states");
+    from = starts;
+    behind = ends;
+  }
   LinearPass pq{}, pv{}, pk{};
   pq.x = rd; pq.y = rv; pq.w = rk; pq.e = rq;
   pq.out = group > 1 ? static_cast<void*>(part_q) : dq;
   pq.out_dtype = group > 1 ? GDR_FP32 : grad_dtype;
-  pq.start = state_in;
+  pq.start = from;
   pq.row = 1; pq.col = dk; pq.od = dk; pq.kd = dv;
   pq.us = 1.f; pq.os = scale;
   if (dg) {
     pq.dot = row;
-    pq.end_with = dstate_out;
+    pq.end_with = behind;
     pq.end_dot = end;
   }
   pv.x = rk; pv.y = rq; pv.w = rd; pv.e = rv;
   pv.out = dv_out; pv.out_dtype = grad_dtype;
   pv.dot = dg ? col : nullptr;
-  pv.start = dstate_out;
+  pv.start = behind;
   pv.end = dstate_in;
   pv.row = dk; pv.col = 1; pv.od = dv; pv.kd = dk;
   pv.us = scale; pv.os = 1.f; pv.backward = 1;
   pk.x = rv; pk.y = rd; pk.w = rq;
   pk.out = group > 1 ? static_cast<void*>(part_k) : dk_out;
   pk.out_dtype = group > 1 ? GDR_FP32 : grad_dtype;
-  pk.start = dstate_out;
+  pk.start = behind;
   pk.row = 1; pk.col = dk; pk.od = dk; pk.kd = dv;
   pk.us = scale; pk.os = 1.f; pk.backward = 1;
-  hipError_t e = gdr::launch_linear_pass(b, pq, st);
+  e = gdr::launch_linear_pass(b, pq, st);
   if (e == hipSuccess) e = gdr::launch_linear_pass(b, pv, st);
   if (e == hipSuccess) e = gdr::launch_linear_pass(b, pk, st);
   if (e != hipSuccess) return hip_fail(e, who, "scan");
@@ -236,10 +325,10 @@ gdr_status gdr_linear_backward(const void* q, const void* k, const void* v, cons
     if (e != hipSuccess) return hip_fail(e, who, "shared heads");
   }
   if (dg) {
-    float* to = decay == GDR_DECAY_TOKEN ? dg : dgt;
-    e = gdr::launch_linear_dg(b, row, dk / 16, col, dv / 16, dstate_out ? end : nullptr, dk / 16,
-                              to, st);
-    if (e == hipSuccess && decay == GDR_DECAY_HEAD) e = gdr::launch_linear_dg_heads(b, dgt, dg, st);
+    const bool heads = decay == GDR_DECAY_HEAD;
+    e = gdr::launch_linear_dg(b, row, dk / 16, col, dv / 16, behind ? end : nullptr, dk / 16,
+                              heads ? nullptr : dg, heads ? sums : nullptr, st);
+    if (e == hipSuccess && heads) e = gdr::launch_linear_dg_heads(b, sums, dg, st);
     if (e != hipSuccess) return hip_fail(e, who, "gate gradient");
   }
   return ok();

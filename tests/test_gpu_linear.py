@@ -37,6 +37,8 @@ def check_prefill(d, o, s, half=None):
         ref.check("state_out", s, want_s, b["state_out"], eps, 2.0 ** -24)
 
 
+# long enough to be cut into segments; one of them starts or ends on a segment's edge
+LONG = [[1100, 0, 513, 1, 1024], [1600], [0, 30, 1025]]
 LENS = [[1], [64], [2, 0, 65], [63, 64, 65, 1, 128], [300, 0, 1, 129]]
 
 
@@ -49,6 +51,19 @@ def test_prefill(lens, dtype, dk, dv, H, Hk):
         say(f"prefill {lens} {dtype} {dk}x{dv} H{H}/{Hk} {decay} {gate}")
         d = ref.make(lens, H, Hk, dk, dv, dtype, decay, gate, state, seed=11)
         check_prefill(d, *prefill(d))
+
+
+@pytest.mark.parametrize("lens", LONG)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dk, dv, decay, gate, state", [(128, 128, "token", "slow", True),
+                                                        (64, 128, "head", "slow", False),
+                                                        (128, 64, "token", "unit", True)])
+def test_prefill_in_segments(lens, dtype, dk, dv, decay, gate, state):
+    say(f"prefill {lens} {dtype} {dk}x{dv} {decay} {gate}")
+    d = ref.make(lens, 2, 1, dk, dv, dtype, decay, gate, state, seed=19)
+    o, s = prefill(d)
+    check_prefill(d, o, s)
+    assert torch.equal(o, prefill(d, state_out=False)[0])
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -210,6 +225,17 @@ def test_backward(lens, dtype, dk, dv, H, Hk):
         say(f"backward {lens} {dtype} {dk}x{dv} H{H}/{Hk} {decay} {gate}")
         d = ref.make(lens, H, Hk, dk, dv, dtype, decay, gate, state, seed=31)
         check_backward(d, backward(d))
+
+
+@pytest.mark.parametrize("lens", LONG)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dk, dv, decay, gate, state", [(128, 128, "token", "slow", True),
+                                                        (64, 128, "head", "slow", False),
+                                                        (128, 64, "token", "unit", True)])
+def test_backward_in_segments(lens, dtype, dk, dv, decay, gate, state):
+    say(f"backward {lens} {dtype} {dk}x{dv} {decay} {gate}")
+    d = ref.make(lens, 2, 1, dk, dv, dtype, decay, gate, state, seed=36)
+    check_backward(d, backward(d))
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
