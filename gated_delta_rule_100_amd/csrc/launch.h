@@ -172,12 +172,15 @@ struct LinearRows {
   int64_t stride;
   int group;
 };
+// Partial sums of a dot product over od columns: one a workgroup.
+inline int linear_parts(int od) { return od == 128 ? 1 : od / 64; }
+
 struct LinearPass {
   LinearRows x, y, w;
   LinearRows e;        // rows of od values to dot with the outputs (dot != NULL)
   void* out;           // [T, H, od]
-  float* dot;          // [od / 16][H][T] partial sums of e_t . out_t without the
-                       // token's own term, or NULL
+  float* dot;          // [linear_parts(od)][H][T] partial sums of e_t . out_t
+                       // without the token's own term, or NULL
   const float* start;  // [units * H] states the walks start from, NULL for zero
   float* end;          // [N * H] states where the last walk of a sequence ends,
                        // NULL: not written; not written for sequences without units

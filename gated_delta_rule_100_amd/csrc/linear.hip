@@ -258,24 +258,25 @@ __device__ __forceinline__ Gates chunk_gates(float gate, bool per_token, int lan
 // ---- the chunk scan
 //
 // One workgroup per (unit, head, 16 W columns of w): a unit is a sequence, or a
-// segment of one.  Its waves have three roles and meet at one barrier a chunk:
+// segment of one.  Its waves have three roles:
 //   - W compute waves hold 16 state rows each for the whole walk, as output
 //     tiles of the state update: lane (c, g) holds Z[c][32 j + 8 g + 0..7],
 //     which is also the fragment of Z in the product with x.  In step s they
 //     form out = Z x + P w and the update of Z for chunk s;
-//   - 4 score waves form the scores x.y of chunk s + 1, with their decays, as
-//     P^T fragments in LDS: they do not depend on the state, and their
-//     arithmetic fills the issue slots that the compute waves' chain leaves;
+//   - 4 score waves form the scores x.y of chunk s + 1, with their decays, in
+//     registers: they do not depend on the state, and their arithmetic fills
+//     the issue slots that the compute waves' chain leaves;
 //   - 4 copy waves copy the x and y rows of chunk s + 2 and the w rows of chunk
 //     s + 1 to LDS (global-to-LDS loads) and form the gate factors of s + 2.
 //     They are waves of their own because a wave's LDS reads wait for all its
 //     global-to-LDS loads in flight.
-// One wave a SIMD doing all three took 8900 cycles a chunk (4 x 4096 tokens, 16
-// heads), 3500 of them for the scores.
+// Two barriers a chunk: one behind its last reads, and one behind the score
+// waves' writing P^T for the next chunk (right after the former, while the
+// compute waves form Z x).
 constexpr int kScoreWaves = 4;
 constexpr int kCopyWaves = 4;
 
-template <Dt IN, int KD, int W, int PZ>
+template <Dt IN, int KD, int W, int PZ, bool DOT>
 struct ScanCfg {
   static constexpr int ES = IN == Dt::BF16 ? 2 : 4;
   static constexpr int C = IN == Dt::BF16 ? 64 : 32;  // tokens a chunk (fp32: half, for LDS)
@@ -291,15 +292,17 @@ struct ScanCfg {
   // of Z x_t and of the update, e^{G_C}
   static constexpr int GATE_BYTES = (4 * C + 4) * 4;
   static constexpr int OFF_G = OFF_W + 2 * W_BYTES;
-  // two of P^T fragments (row tile, 32-deep block) on the walked side of the
-  // diagonal, PL planes each, and of the scores of a token with itself
+  // P^T fragments (row tile, 32-deep block) on the walked side of the diagonal,
+  // PL planes each, and the scores of a token with itself
   static constexpr int PL = IN == Dt::F32 ? 1 : PZ;
   static constexpr int FRAG = IN == Dt::BF16 ? 1024 : 2048;
   static constexpr int FRAGS = NB == 2 ? 6 : 2;
   static constexpr int P_BYTES = FRAGS * PL * FRAG;
   static constexpr int OFF_P = OFF_G + 3 * GATE_BYTES;
-  static constexpr int OFF_DIAG = OFF_P + 2 * P_BYTES;
-  static constexpr int BYTES = OFF_DIAG + 2 * C * 4;
+  static constexpr int OFF_DIAG = OFF_P + P_BYTES;
+  // two of the compute waves' parts of the dot products
+  static constexpr int OFF_DOT = OFF_DIAG + C * 4;
+  static constexpr int BYTES = OFF_DOT + (DOT ? 2 * W * C * 4 : 0);
   static_assert(BYTES <= 160 * 1024, "LDS");
 };
 
@@ -311,10 +314,24 @@ __device__ __forceinline__ int p_frag(int tt, int sb) {
   else return tt < 2 ? tt : 2 * tt - 2 + sb;
 }
 
+// Four consecutive columns of a state row, col elements apart.
+__device__ __forceinline__ floatx4 load_state4(const float* p, int64_t col) {
+  if (col == 1) return *reinterpret_cast<const floatx4*>(p);
+  return floatx4{p[0], p[col], p[2 * col], p[3 * col]};
+}
+__device__ __forceinline__ void store_state4(float* p, int64_t col, const floatx4& z) {
+  if (col == 1) {
+    *reinterpret_cast<floatx4*>(p) = z;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) p[e * col] = z[e];
+  }
+}
+
 template <Dt IN, int KD, int W, int PZ, bool DOT, bool BACK>
-__global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_scan_kernel(
+__global__ __launch_bounds__((ScanCfg<IN, KD, W, PZ, DOT>::THREADS)) void linear_scan_kernel(
     LinearBatch b, LinearPass p) {
-  using Cfg = ScanCfg<IN, KD, W, PZ>;
+  using Cfg = ScanCfg<IN, KD, W, PZ, DOT>;
   constexpr int C = Cfg::C, NT = Cfg::NT, NB = Cfg::NB, KB = Cfg::KB, ES = Cfg::ES, PL = Cfg::PL;
   __shared__ __align__(1024) unsigned char lds[Cfg::BYTES];
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
@@ -432,18 +449,32 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
     if (chunks > 1) put_gates(1, 1, g1);
     __builtin_amdgcn_s_waitcnt(0);
     bare_barrier();
-    bare_barrier();
+    // the dot products of chunk s, one token a lane
+    auto store_dots = [&](int s) {
+      if (!DOT || cw != 1) return;
+      int tok;
+      const int len = chunk_at(s, tok);
+      const float* part = reinterpret_cast<const float*>(lds + Cfg::OFF_DOT) + (s & 1) * W * C;
+      float sum = 0.f;
+      if (lane < C) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) sum += part[i * C + lane];
+      }
+      if (lane < len)
+        p.dot[(static_cast<size_t>(slice) * b.H + h) * b.T_total + tok + lane] = sum;
+    };
     for (int s = 0, buf = 2; s < chunks; ++s, buf = next(buf)) {
       float gate = 0.f;
+      if (s > 0) store_dots(s - 1);
       if (s + 2 < chunks) gate = load_gate(s + 2);
       if (s + 1 < chunks) copy_w(s + 1);
-      if (s + 2 < chunks) {
-        copy_xy(s + 2, buf);
-        put_gates(s + 2, buf, gate);
-      }
+      if (s + 2 < chunks) copy_xy(s + 2, buf);
+      bare_barrier();
+      if (s + 2 < chunks) put_gates(s + 2, buf, gate);
       __builtin_amdgcn_s_waitcnt(0);
       bare_barrier();
     }
+    store_dots(chunks - 1);
     return;
   }
 
@@ -475,12 +506,12 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
     int kl[KB];
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) kl[kb] = row_lane<Cfg::CHK>(c, g, kb);
+    float v[PER][4], own[PER];
     auto scores = [&](int s, int buf) {
       int tok;
       const int len = chunk_at(s, tok);
       const unsigned char *X = x_tile(buf), *Y = X + Cfg::X_BYTES;
       const float* gate = gate_row(buf);
-      float* diag = reinterpret_cast<float*>(lds + Cfg::OFF_DIAG) + (s & 1) * C;
       floatx4 acc[PER];
 #pragma unroll
       for (int i = 0; i < PER; ++i) acc[i] = floatx4{0.f, 0.f, 0.f, 0.f};
@@ -499,37 +530,44 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
         const float gh = gate[t], gl = BACK ? gate[C + t] - ps2 : gate[C + t] + ps2;
         const floatx4 sh = *reinterpret_cast<const floatx4*>(gate + s4);
         const floatx4 sl = *reinterpret_cast<const floatx4*>(gate + C + s4);
-        float v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float d = (gh - sh[e]) + (gl - sl[e]);
           const float x = (ps < 0.f ? -acc[i][e] : acc[i][e]) * __builtin_amdgcn_exp2f(BACK ? -d : d);
           const int sc = s4 + e;
-          if (DOT && sc == t) diag[t] = x;
+          if (DOT && sc == t) own[i] = x;
           const bool in = BACK ? (DOT ? sc > t : sc >= t) && sc < len : (DOT ? sc < t : sc <= t);
-          v[e] = in ? x : 0.f;
+          v[i][e] = in ? x : 0.f;
         }
+      }
+    };
+    auto put_scores = [&]() {
+      float* diag = reinterpret_cast<float*>(lds + Cfg::OFF_DIAG);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        if (DOT && sts[i] == tts[i] && (c >> 2) == g) diag[16 * tts[i] + c] = own[i];
         const int half = sts[i] & 1;
-        unsigned char* to = lds + Cfg::OFF_P + (s & 1) * Cfg::P_BYTES +
-                            p_frag<NB, BACK>(tts[i], sts[i] >> 1) * PL * Cfg::FRAG;
+        unsigned char* to = lds + Cfg::OFF_P + p_frag<NB, BACK>(tts[i], sts[i] >> 1) * PL * Cfg::FRAG;
         if constexpr (IN == Dt::F32) {
-          *reinterpret_cast<floatx4*>(to + lane * 32 + 16 * half) = floatx4{v[0], v[1], v[2], v[3]};
+          *reinterpret_cast<floatx4*>(to + lane * 32 + 16 * half) =
+              floatx4{v[i][0], v[i][1], v[i][2], v[i][3]};
         } else {
           uint32_t lo[PL], hi[PL];
-          split2<PL>(v[0], v[1], lo);
-          split2<PL>(v[2], v[3], hi);
+          split2<PL>(v[i][0], v[i][1], lo);
+          split2<PL>(v[i][2], v[i][3], hi);
 #pragma unroll
           for (int q = 0; q < PL; ++q)
             *reinterpret_cast<uint2*>(to + q * Cfg::FRAG + lane * 16 + 8 * half) = make_uint2(lo[q], hi[q]);
         }
       }
     };
-    bare_barrier();
+    bare_barrier();  // the first chunks are there
     scores(0, 0);
-    lds_barrier();
     for (int s = 0, buf = 1; s < chunks; ++s, buf = next(buf)) {
+      put_scores();
+      lds_barrier();  // P of chunk s is there
       if (s + 1 < chunks) scores(s + 1, buf);
-      lds_barrier();
+      lds_barrier();  // chunk s is done
     }
     return;
   }
@@ -539,18 +577,15 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
   const size_t zbase = static_cast<size_t>(pair) * p.od * KD + (od + c) * p.row;
   floatx4 z[KD / 16];  // z[2 j + i][e] = Z[od + c][32 j + 8 g + 4 i + e]
 #pragma unroll
-  for (int j = 0; j < KD / 16; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int k = 32 * (j >> 1) + 8 * g + 4 * (j & 1) + e;
-      z[j][e] = p.start ? p.start[zbase + k * p.col] : 0.f;
-    }
+  for (int j = 0; j < KD / 16; ++j) {
+    const int k = 32 * (j >> 1) + 8 * g + 4 * (j & 1);
+    z[j] = p.start ? load_state4(p.start + zbase + k * p.col, p.col) : floatx4{0.f, 0.f, 0.f, 0.f};
+  }
   if (chunks > 0) {
     // the halves of P^T fragments beyond the diagonal stay zero
-    for (int i = threadIdx.x; i < 2 * Cfg::P_BYTES / 16; i += 64 * W)
+    for (int i = threadIdx.x; i < Cfg::P_BYTES / 16; i += 64 * W)
       *reinterpret_cast<uint4*>(lds + Cfg::OFF_P + 16 * i) = make_uint4(0, 0, 0, 0);
     lds_barrier();
-    bare_barrier();
   }
   const size_t out_es = p.out_dtype == 0 ? 2 : 4;
   const uint32_t out_row = static_cast<uint32_t>(b.H * p.od * out_es);
@@ -567,9 +602,9 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
     const int len = chunk_at(s, tok);
     const unsigned char *X = x_tile(buf), *Y = X + Cfg::X_BYTES;
     const unsigned char* Wt = lds + Cfg::OFF_W + (s & 1) * Cfg::W_BYTES;
-    const unsigned char* P = lds + Cfg::OFF_P + (s & 1) * Cfg::P_BYTES;
+    const unsigned char* P = lds + Cfg::OFF_P;
     const float* gate = gate_row(buf);
-    const float* diag = reinterpret_cast<const float*>(lds + Cfg::OFF_DIAG) + (s & 1) * C;
+    const float* diag = reinterpret_cast<const float*>(lds + Cfg::OFF_DIAG);
 
     // the rows to dot with the outputs: loaded first, used last
     float ev[DOT ? NT : 1][4];
@@ -589,31 +624,12 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
     Frag<IN> xf[2][NT];
 #pragma unroll
     for (int tt = 0; tt < NT; ++tt) xf[0][tt] = row_frag<IN, Cfg::CHK>(X, 16 * tt, 0, c, g, kl[0]);
-    Frag<IN> wf[NB];
-    Planes<IN, PZ> pf[Cfg::FRAGS];
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
       if (kb + 1 < KB) {
 #pragma unroll
         for (int tt = 0; tt < NT; ++tt)
           xf[(kb + 1) & 1][tt] = row_frag<IN, Cfg::CHK>(X, 16 * tt, kb + 1, c, g, kl[kb + 1]);
-      } else {
-#pragma unroll
-        for (int sb = 0; sb < NB; ++sb)
-          wf[sb] = col_frag_narrow<IN, Cfg::CHV>(Wt, 32 * sb, 16 * wave, c, g);
-#pragma unroll
-        for (int i = 0; i < Cfg::FRAGS; ++i) {
-          const unsigned char* from = P + i * PL * Cfg::FRAG;
-          if constexpr (IN == Dt::F32) {
-            const floatx4 a = *reinterpret_cast<const floatx4*>(from + lane * 32);
-            const floatx4 d = *reinterpret_cast<const floatx4*>(from + lane * 32 + 16);
-            pf[i].p[0] = {{a[0], a[1], a[2], a[3], d[0], d[1], d[2], d[3]}};
-          } else {
-#pragma unroll
-            for (int q = 0; q < PL; ++q)
-              pf[i].p[q] = *reinterpret_cast<const bf16x8*>(from + q * Cfg::FRAG + lane * 16);
-          }
-        }
       }
       const float zz[8] = {z[2 * kb][0], z[2 * kb][1], z[2 * kb][2], z[2 * kb][3],
                            z[2 * kb + 1][0], z[2 * kb + 1][1], z[2 * kb + 1][2], z[2 * kb + 1][3]};
@@ -623,54 +639,71 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
 #pragma unroll
         for (int tt = 0; tt < NT; ++tt) o[tt] = mma(zp.p[q], xf[kb & 1][tt], o[tt]);
     }
+    Frag<IN> wf[NB];
+#pragma unroll
+    for (int sb = 0; sb < NB; ++sb)
+      wf[sb] = col_frag_narrow<IN, Cfg::CHV>(Wt, 32 * sb, 16 * wave, c, g);
 #pragma unroll
     for (int tt = 0; tt < NT; ++tt) o[tt] *= gate[2 * C + 16 * tt + c];
+    bare_barrier();  // P of chunk s is there
 
     // + w^T P^T
 #pragma unroll
-    for (int sb = 0; sb < NB; ++sb)
+    for (int sb = 0; sb < NB; ++sb) {
+      Planes<IN, PZ> pf[NT];
+#pragma unroll
+      for (int tt = 0; tt < NT; ++tt) {
+        if (BACK ? sb < (tt >> 1) : sb > (tt >> 1)) continue;
+        const unsigned char* from = P + p_frag<NB, BACK>(tt, sb) * PL * Cfg::FRAG;
+        if constexpr (IN == Dt::F32) {
+          const floatx4 a = *reinterpret_cast<const floatx4*>(from + lane * 32);
+          const floatx4 d = *reinterpret_cast<const floatx4*>(from + lane * 32 + 16);
+          pf[tt].p[0] = {{a[0], a[1], a[2], a[3], d[0], d[1], d[2], d[3]}};
+        } else {
+#pragma unroll
+          for (int q = 0; q < PL; ++q)
+            pf[tt].p[q] = *reinterpret_cast<const bf16x8*>(from + q * Cfg::FRAG + lane * 16);
+        }
+      }
 #pragma unroll
       for (int q = PL - 1; q >= 0; --q)
 #pragma unroll
         for (int tt = 0; tt < NT; ++tt) {
           if (BACK ? sb < (tt >> 1) : sb > (tt >> 1)) continue;
-          o[tt] = mma(wf[sb], pf[p_frag<NB, BACK>(tt, sb)].p[q], o[tt]);
+          o[tt] = mma(wf[sb], pf[tt].p[q], o[tt]);
         }
+    }
 
-    // Z <- e^{G_C} Z + (update factors . w)^T y, four tiles' y fragments at a time
+    // Z <- e^{G_C} Z + (update factors . w)^T y, two tiles' y fragments at a time
     const float gc = gate[4 * C];
 #pragma unroll
     for (int j = 0; j < KD / 16; ++j) z[j] *= gc;
-    constexpr int JG = 4, GROUPS = KD / 16 / JG * NB;
-    Frag<IN> yf[2][JG];
-    auto read_y = [&](int i, Frag<IN> (&f)[JG]) {
-      const int sb = i / (KD / 16 / JG), j0 = i % (KD / 16 / JG) * JG;
-#pragma unroll
-      for (int j = 0; j < JG; ++j)
-        f[j] = col_frag_wide<IN, Cfg::CHK>(Y, 32 * sb, (j0 + j) >> 1, j & 1, c, g, jl[(j0 + j) >> 1]);
-    };
-    read_y(0, yf[0]);
-    Planes<IN, 3> up[NB];
 #pragma unroll
     for (int sb = 0; sb < NB; ++sb) {
       const floatx4 f0 = *reinterpret_cast<const floatx4*>(gate + 3 * C + 32 * sb + 4 * g);
       const floatx4 f1 = *reinterpret_cast<const floatx4*>(gate + 3 * C + 32 * sb + 16 + 4 * g);
+      Frag<IN> yf[2][2];
+      auto read_y = [&](int jb, Frag<IN> (&f)[2]) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          f[i] = col_frag_wide<IN, Cfg::CHK>(Y, 32 * sb, jb, i, c, g, jl[jb]);
+      };
+      read_y(0, yf[0]);
       float u[8];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         u[e] = frag_value(wf[sb], e) * f0[e];
         u[4 + e] = frag_value(wf[sb], 4 + e) * f1[e];
       }
-      up[sb] = to_planes<IN, 3>(u);
-    }
+      const Planes<IN, 3> up = to_planes<IN, 3>(u);
 #pragma unroll
-    for (int i = 0; i < GROUPS; ++i) {
-      if (i + 1 < GROUPS) read_y(i + 1, yf[(i + 1) & 1]);
-      const int sb = i / (KD / 16 / JG), j0 = i % (KD / 16 / JG) * JG;
+      for (int jb = 0; jb < KD / 32; ++jb) {
+        if (jb + 1 < KD / 32) read_y(jb + 1, yf[(jb + 1) & 1]);
 #pragma unroll
-      for (int q = Planes<IN, 3>::N - 1; q >= 0; --q)
+        for (int q = Planes<IN, 3>::N - 1; q >= 0; --q)
 #pragma unroll
-        for (int j = 0; j < JG; ++j) z[j0 + j] = mma(yf[i & 1][j], up[sb].p[q], z[j0 + j]);
+          for (int i = 0; i < 2; ++i) z[2 * jb + i] = mma(yf[jb & 1][i], up.p[q], z[2 * jb + i]);
+      }
     }
 
     // outputs
@@ -683,8 +716,8 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
         for (int e = 0; e < 4; ++e) dot = fmaf(ev[tt][e], o[tt][e], dot);
         dot += __shfl_xor(dot, 16);
         dot += __shfl_xor(dot, 32);
-        if (t < len && g == 0)
-          p.dot[(static_cast<size_t>(od / 16) * b.H + h) * b.T_total + tok + t] = dot;
+        if (g == 0)
+          (reinterpret_cast<float*>(lds + Cfg::OFF_DOT) + ((s & 1) * W + wave) * C)[t] = dot;
         o[tt] += diag[t] * row4<IN, Cfg::CHV>(Wt, t, 16 * wave + 4 * g);
       }
     }
@@ -709,20 +742,22 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
       for (int tt = 0; tt < NT; ++tt)
         if (16 * tt + c < len) store(tt);
     }
-    lds_barrier();  // the chunk is done
+    lds_barrier();  // chunk s is done
   }
 
   float ed = 0.f;
   const bool ends = p.end && (BACK ? unit.first : unit.last);
   const size_t ebase = (static_cast<size_t>(unit.n) * b.H + h) * p.od * KD + (od + c) * p.row;
 #pragma unroll
-  for (int j = 0; j < KD / 16; ++j)
+  for (int j = 0; j < KD / 16; ++j) {
+    const size_t at = (32 * (j >> 1) + 8 * g + 4 * (j & 1)) * p.col;
+    if (p.end_with) {
+      const floatx4 r = load_state4(p.end_with + zbase + at, p.col);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const size_t at = (32 * (j >> 1) + 8 * g + 4 * (j & 1) + e) * p.col;
-      if (p.end_with) ed = fmaf(z[j][e], p.end_with[zbase + at], ed);
-      if (ends) p.end[ebase + at] = z[j][e];
+      for (int e = 0; e < 4; ++e) ed = fmaf(z[j][e], r[e], ed);
     }
+    if (ends) store_state4(p.end + ebase + at, p.col, z[j]);
+  }
   if (p.end_with) {
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) ed += __shfl_xor(ed, d);
@@ -732,8 +767,10 @@ __global__ __launch_bounds__(64 * (W + kScoreWaves + kCopyWaves)) void linear_sc
 
 // ---- states at the starts of segments
 //
-// A segment's own state, from zero: the update of the scan alone, so the copy
-// waves bring y and w rows only.
+// A segment's own state, from zero: the update of the scan alone.  It is a
+// stream of y and w rows, so the copy waves keep three chunks in flight ahead
+// of the one in use (four buffers, one barrier a chunk); one wave forms the gate
+// factors.
 template <Dt IN, int KD, int W>
 struct LocalCfg {
   static constexpr int ES = IN == Dt::BF16 ? 2 : 4;
@@ -741,20 +778,30 @@ struct LocalCfg {
   static constexpr int NB = C / 32;
   static constexpr int VS = 16 * W;
   static constexpr int CHK = KD * ES / 16, CHV = VS * ES / 16;
-  static constexpr int THREADS = 64 * (W + kCopyWaves);
+  static constexpr int THREADS = 64 * (W + kCopyWaves + 1);
+  static constexpr int STAGES = 4;
   static constexpr int Y_BYTES = C * KD * ES, W_BYTES = C * VS * ES;
   static constexpr int BUF = Y_BYTES + W_BYTES;
   static constexpr int GATE_BYTES = (C + 4) * 4;  // update factors, e^{G_C}
-  static constexpr int OFF_G = 2 * BUF;
+  static constexpr int OFF_G = STAGES * BUF;
   static constexpr int BYTES = OFF_G + 2 * GATE_BYTES;
+  // copies of a chunk by one copy wave
+  static constexpr int NY = C * CHK / 64 / kCopyWaves, NW = C * CHV / 64 / kCopyWaves;
   static_assert(BYTES <= 160 * 1024, "LDS");
+  static_assert(2 * (NY + NW) < 64, "copies in flight");
 };
 
+// Waits until at most n of this wave's loads and stores are in flight.
+template <int N>
+__device__ __forceinline__ void wait_vmem() {
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+}
+
 template <Dt IN, int KD, int W, bool BACK>
-__global__ __launch_bounds__(64 * (W + kCopyWaves)) void linear_local_kernel(
+__global__ __launch_bounds__((LocalCfg<IN, KD, W>::THREADS)) void linear_local_kernel(
     LinearBatch b, LinearRows y, LinearRows w, float us, int od_all, float* states, float* decays) {
   using Cfg = LocalCfg<IN, KD, W>;
-  constexpr int C = Cfg::C, NB = Cfg::NB, ES = Cfg::ES;
+  constexpr int C = Cfg::C, NB = Cfg::NB, ES = Cfg::ES, NY = Cfg::NY, NW = Cfg::NW;
   __shared__ __align__(1024) unsigned char lds[Cfg::BYTES];
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -770,13 +817,38 @@ __global__ __launch_bounds__(64 * (W + kCopyWaves)) void linear_local_kernel(
     tok = tb + (BACK ? chunks - 1 - s : s) * C;
     return te - tok < C ? te - tok : C;
   };
+  if (wave == W + kCopyWaves) {  // ---- gate wave
+    auto load = [&](int s) {
+      int tok;
+      const int len = chunk_at(s, tok);
+      if (!b.gates.per_token) return b.gates.g[h];
+      return lane < len ? b.gates.g[static_cast<size_t>(tok + lane) * b.H + h] : 0.f;
+    };
+    auto put = [&](int s, float gate) {
+      int tok;
+      const int len = chunk_at(s, tok);
+      const Gates v = chunk_gates<C>(gate, b.gates.per_token, lane, len);
+      float* f = reinterpret_cast<float*>(lds + Cfg::OFF_G + (s & 1) * Cfg::GATE_BYTES);
+      if (lane < C) f[lane] = lane < len ? us * (BACK ? v.from_start : v.to_end) : 0.f;
+      if (lane == 0) f[C] = v.all;
+    };
+    float ahead = chunks > 1 ? load(1) : 0.f;
+    put(0, load(0));
+    lds_barrier();
+    for (int s = 0; s < chunks; ++s) {
+      const float gate = ahead;
+      if (s + 2 < chunks) ahead = load(s + 2);
+      if (s + 1 < chunks) put(s + 1, gate);
+      lds_barrier();
+    }
+    return;
+  }
   if (wave >= W) {  // ---- copy waves
     const int cw = wave - W;
     const char* ys = static_cast<const char*>(y.p) + static_cast<size_t>(h / y.group) * KD * ES;
     const char* ws = static_cast<const char*>(w.p) +
                      (static_cast<size_t>(h / w.group) * od_all + slice * Cfg::VS) * ES;
     const size_t yst = y.stride * ES, wst = w.stride * ES;
-    constexpr int NY = C * Cfg::CHK / 64 / kCopyWaves, NW = C * Cfg::CHV / 64 / kCopyWaves;
     auto piece = [&](int i, auto ch, int len, size_t stride) {
       constexpr int CH = decltype(ch)::value;
       const int q = 64 * (cw + kCopyWaves * i) + lane, r = q / CH, pc = q % CH;
@@ -789,17 +861,12 @@ __global__ __launch_bounds__(64 * (W + kCopyWaves)) void linear_local_kernel(
     for (int i = 0; i < NY; ++i) yo[i] = piece(i, chk, C, yst);
 #pragma unroll
     for (int i = 0; i < NW; ++i) wo[i] = piece(i, chv, C, wst);
-    auto bring = [&](int s) {
+    auto bring = [&](int s) {  // NY + NW copies
       int tok;
       const int len = chunk_at(s, tok);
-      float gate = 0.f;
-      if (cw == 0) {
-        if (!b.gates.per_token) gate = b.gates.g[h];
-        else if (lane < len) gate = b.gates.g[static_cast<size_t>(tok + lane) * b.H + h];
-      }
       const char* yb = ys + static_cast<size_t>(tok) * yst;
       const char* wb = ws + static_cast<size_t>(tok) * wst;
-      unsigned char* to = lds + (s & 1) * Cfg::BUF + 1024 * cw;
+      unsigned char* to = lds + (s % Cfg::STAGES) * Cfg::BUF + 1024 * cw;
       if (len == C) {
 #pragma unroll
         for (int i = 0; i < NY; ++i) copy16(yb + yo[i], to + 1024 * kCopyWaves * i);
@@ -812,18 +879,22 @@ __global__ __launch_bounds__(64 * (W + kCopyWaves)) void linear_local_kernel(
         for (int i = 0; i < NW; ++i)
           copy16(wb + piece(i, chv, len, wst), to + Cfg::Y_BYTES + 1024 * kCopyWaves * i);
       }
-      if (cw == 0) {
-        const Gates v = chunk_gates<C>(gate, b.gates.per_token, lane, len);
-        float* f = reinterpret_cast<float*>(lds + Cfg::OFF_G + (s & 1) * Cfg::GATE_BYTES);
-        if (lane < C) f[lane] = lane < len ? us * (BACK ? v.from_start : v.to_end) : 0.f;
-        if (lane == 0) f[C] = v.all;
-      }
-      __builtin_amdgcn_s_waitcnt(0);
     };
-    bring(0);
+    // chunk s + 1 is there when the copies of the (at most two) chunks behind it
+    // are all that is in flight
+    auto wait_for = [&](int behind) {
+      if (behind >= 2) wait_vmem<2 * (NY + NW)>();
+      else if (behind == 1) wait_vmem<NY + NW>();
+      else wait_vmem<0>();
+    };
+    const int lead = chunks < 3 ? chunks : 3;
+    for (int s = 0; s < lead; ++s) bring(s);
+    wait_for(lead - 1);
     bare_barrier();
     for (int s = 0; s < chunks; ++s) {
-      if (s + 1 < chunks) bring(s + 1);
+      if (s + 3 < chunks) bring(s + 3);
+      const int left = chunks - 2 - s;  // chunks behind s + 1
+      wait_for(left < 2 ? left : 2);
       bare_barrier();
     }
     return;
@@ -839,7 +910,7 @@ __global__ __launch_bounds__(64 * (W + kCopyWaves)) void linear_local_kernel(
   for (int j = 0; j < KD / 32; ++j) jl[j] = col_lane<Cfg::CHK>(c, g, j);
   bare_barrier();
   for (int s = 0; s < chunks; ++s) {
-    const unsigned char* Y = lds + (s & 1) * Cfg::BUF;
+    const unsigned char* Y = lds + (s % Cfg::STAGES) * Cfg::BUF;
     const float* f = reinterpret_cast<const float*>(lds + Cfg::OFF_G + (s & 1) * Cfg::GATE_BYTES);
     const float gc = f[C];
     decay *= gc;
@@ -922,38 +993,50 @@ __global__ __launch_bounds__(256) void linear_starts_kernel(LinearBatch b, int p
 
 // ---- gate gradient
 //
-// One wave a (unit, head): suffix sums of row - col, 64 tokens at a time from the
-// unit's end, in fp64.
-__global__ __launch_bounds__(64) void linear_dg_kernel(LinearBatch b, const float* row,
-                                                       int row_parts, const float* col,
-                                                       int col_parts, const float* end_dot,
-                                                       int end_parts, float* dg, double* unit_sum) {
-  const int pair = blockIdx.x, lane = threadIdx.x, h = pair % b.H;
+// One workgroup a (unit, head): suffix sums of row - col, 256 tokens at a time
+// from the unit's end, in fp64.
+__global__ __launch_bounds__(256) void linear_dg_kernel(LinearBatch b, const float* row,
+                                                        int row_parts, const float* col,
+                                                        int col_parts, const float* end_dot,
+                                                        int end_parts, float* dg, double* unit_sum) {
+  __shared__ double wave_sum[2][4];
+  const int pair = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = pair % b.H;
   Unit unit;
-  const bool real = unit_at(b, pair / b.H, unit);
   double total = 0.0;
-  if (real) {
+  if (unit_at(b, pair / b.H, unit)) {
     const size_t th = static_cast<size_t>(b.T_total) * b.H, units = static_cast<size_t>(b.units) * b.H;
     double acc = 0.0;
     if (end_dot)
       for (int i = 0; i < end_parts; ++i) acc += end_dot[i * units + pair];
-    for (int hi = unit.te; hi > unit.tb; hi -= 64) {
-      const int t = hi - 1 - lane;  // lane 0 has the latest token
-      const bool in = t >= unit.tb;
+    auto load = [&](int hi) {
+      const int t = hi - 1 - tid;  // thread 0 has the latest token
       double v = 0.0;
-      if (in) {
+      if (t >= unit.tb) {
         const size_t at = static_cast<size_t>(h) * b.T_total + t;
         for (int i = 0; i < row_parts; ++i) v += row[i * th + at];
         for (int i = 0; i < col_parts; ++i) v -= col[i * th + at];
       }
+      return v;
+    };
+    double ahead = load(unit.te);
+    for (int hi = unit.te, slot = 0; hi > unit.tb; hi -= 256, slot ^= 1) {
+      double v = ahead;
+      if (hi - 256 > unit.tb) ahead = load(hi - 256);
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) {
         const double up = __shfl_up(v, d);
         if (lane >= d) v += up;
       }
+      if (lane == 63) wave_sum[slot][wave] = v;
+      __syncthreads();
       v += acc;
-      acc = __shfl(v, 63);
-      if (in) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i < wave) v += wave_sum[slot][i];
+        acc += wave_sum[slot][i];
+      }
+      const int t = hi - 1 - tid;
+      if (t >= unit.tb) {
         total += v;
         if (dg) dg[static_cast<size_t>(t) * b.H + h] = static_cast<float>(v);
       }
@@ -962,7 +1045,10 @@ __global__ __launch_bounds__(64) void linear_dg_kernel(LinearBatch b, const floa
   if (unit_sum) {
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
-    if (lane == 0) unit_sum[pair] = total;
+    __syncthreads();
+    if (lane == 0) wave_sum[0][wave] = total;
+    __syncthreads();
+    if (tid == 0) unit_sum[pair] = wave_sum[0][0] + wave_sum[0][1] + wave_sum[0][2] + wave_sum[0][3];
   }
 }
 
@@ -1061,18 +1147,26 @@ unsigned scan_grid(const LinearBatch& b, int slices) {
 hipError_t launch_linear_pass(const LinearBatch& b, const LinearPass& p, hipStream_t stream) {
   return by_type(b.in_dtype, p.kd, [&](auto in, auto kd) {
     constexpr Dt IN = decltype(in)::value;
-    constexpr int KD = decltype(kd)::value, W = 4;
-    auto go = [&](auto dot, auto back) {
+    constexpr int KD = decltype(kd)::value;
+    auto go = [&](auto w, auto dot, auto back) {
+      constexpr int W = decltype(w)::value;
       constexpr bool DOT = decltype(dot)::value, BACK = decltype(back)::value;
-      hipLaunchKernelGGL((linear_scan_kernel<IN, KD, W, DOT ? 3 : 2, DOT, BACK>),
-                         dim3(scan_grid(b, p.od / (16 * W))),
-                         dim3(64 * (W + kScoreWaves + kCopyWaves)), 0, stream, b, p);
+      constexpr int PZ = DOT ? 3 : 2;
+      hipLaunchKernelGGL((linear_scan_kernel<IN, KD, W, PZ, DOT, BACK>),
+                         dim3(scan_grid(b, p.od / (16 * W))), dim3(ScanCfg<IN, KD, W, PZ, DOT>::THREADS), 0,
+                         stream, b, p);
       return hipGetLastError();
     };
+    const std::integral_constant<int, 4> w4;
+    const std::integral_constant<int, 8> w8;
     const std::true_type yes;
     const std::false_type no;
-    if (p.dot) return p.backward ? go(yes, yes) : go(yes, no);
-    return p.backward ? go(no, yes) : go(no, no);
+    if (p.od == 128) {
+      if (p.dot) return p.backward ? go(w8, yes, yes) : go(w8, yes, no);
+      return p.backward ? go(w8, no, yes) : go(w8, no, no);
+    }
+    if (p.dot) return p.backward ? go(w4, yes, yes) : go(w4, yes, no);
+    return p.backward ? go(w4, no, yes) : go(w4, no, no);
   });
 }
 
@@ -1081,14 +1175,20 @@ hipError_t launch_linear_starts(const LinearBatch& b, const LinearRows& y, const
                                 float* states, float* decays, float* last, hipStream_t stream) {
   hipError_t e = by_type(b.in_dtype, kd, [&](auto in, auto kdim) {
     constexpr Dt IN = decltype(in)::value;
-    constexpr int KD = decltype(kdim)::value, W = 4;
-    auto go = [&](auto back) {
+    constexpr int KD = decltype(kdim)::value;
+    auto go = [&](auto w_, auto back) {
+      constexpr int W = decltype(w_)::value;
       hipLaunchKernelGGL((linear_local_kernel<IN, KD, W, decltype(back)::value>),
-                         dim3(scan_grid(b, od / (16 * W))), dim3(64 * (W + kCopyWaves)), 0, stream,
-                         b, y, w, us, od, states, decays);
+                         dim3(scan_grid(b, od / (16 * W))), dim3(LocalCfg<IN, KD, W>::THREADS), 0,
+                         stream, b, y, w, us, od, states, decays);
       return hipGetLastError();
     };
-    return backward ? go(std::true_type()) : go(std::false_type());
+    const std::integral_constant<int, 4> w4;
+    const std::integral_constant<int, 8> w8;
+    const std::true_type yes;
+    const std::false_type no;
+    if (od == 128) return backward ? go(w8, yes) : go(w8, no);
+    return backward ? go(w4, yes) : go(w4, no);
   });
   if (e != hipSuccess) return e;
   const int per = od * kd;
@@ -1105,7 +1205,7 @@ hipError_t launch_linear_starts(const LinearBatch& b, const LinearRows& y, const
 hipError_t launch_linear_dg(const LinearBatch& b, const float* row, int row_parts,
                             const float* col, int col_parts, const float* end_dot, int end_parts,
                             float* dg, double* unit_sum, hipStream_t stream) {
-  hipLaunchKernelGGL(linear_dg_kernel, dim3(b.units * b.H), dim3(64), 0, stream, b, row, row_parts,
+  hipLaunchKernelGGL(linear_dg_kernel, dim3(b.units * b.H), dim3(256), 0, stream, b, row, row_parts,
                      col, col_parts, end_dot, end_parts, dg, unit_sum);
   return hipGetLastError();
 }

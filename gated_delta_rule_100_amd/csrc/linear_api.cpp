@@ -70,15 +70,21 @@ gdr_status hip_fail(hipError_t e, const char* who, const char* what) {
   return fail(GDR_ERR_HIP, "%s: %s: %s", who, what, hipGetErrorString(e));
 }
 
-// Tokens of a segment, or 0 to walk whole sequences.  Segments cost a second
-// read of y and w and their states' traffic, and make the walks short and even.
+// Tokens of a segment, or 0 to walk whole sequences.  A scan workgroup takes a
+// compute unit for one (unit, head), about 3.7 us a chunk of 64 tokens with all
+// of them at work, so segments are as long as 256 workgroups allow: fewer
+// states to form and pass on (4 x 4096 tokens, 16 heads: 115 us of scan, segment
+// states and chain at 1024 tokens, 137 at 512 and 168 at 2048; 131072 tokens, 4
+// heads: 220 at 2048, 246 at 1024; 8 sequences of 32768 tokens, 32 heads: 468 at
+// 4096, 505 at 2048).  The states cost three launches, so a sequence has to be
+// some chunks longer than a segment before that pays; the host knows only the
+// average length, and takes four times it for the longest one.
 int segment_tokens(int T_total, int N, int H, bool gradient) {
-  (void)N;
   const int64_t th = static_cast<int64_t>(T_total) * H;
-  int seg = 512;
-  while (seg < 4096 && th / seg > 512) seg *= 2;
-  if (!gradient && static_cast<int64_t>(N) * H >= 512) return 0;
-  return T_total > seg ? seg : 0;
+  const int64_t seg = (th + 256 * 64 - 1) / (256 * 64) * 64;
+  const int64_t longest = 4 * ((static_cast<int64_t>(T_total) + N - 1) / N);
+  const int64_t most = longest < T_total ? longest : T_total;
+  return most >= seg + (gradient ? 256 : 512) ? static_cast<int>(seg) : 0;
 }
 
 // Segment tables and states of `kinds` directions.
@@ -118,8 +124,8 @@ BackwardSizes backward_sizes(int T_total, int N, int H, int Hk, int dk, int dv) 
   const size_t th = static_cast<size_t>(T_total) * H * sizeof(float);
   const size_t pairs = static_cast<size_t>(z.seg.units) * H;
   if (H != Hk) z.part_q = z.part_k = align_up(th * dk);
-  z.row = align_up(th * (dk / 16));
-  z.col = align_up(th * (dv / 16));
+  z.row = align_up(th * gdr::linear_parts(dk));
+  z.col = align_up(th * gdr::linear_parts(dv));
   z.end = align_up(pairs * (dk / 16) * sizeof(float));
   z.sums = align_up(pairs * sizeof(double));
   return z;
@@ -326,7 +332,7 @@ gdr_status gdr_linear_backward(const void* q, const void* k, const void* v, cons
   }
   if (dg) {
     const bool heads = decay == GDR_DECAY_HEAD;
-    e = gdr::launch_linear_dg(b, row, dk / 16, col, dv / 16, behind ? end : nullptr, dk / 16,
+    e = gdr::launch_linear_dg(b, row, gdr::linear_parts(dk), col, gdr::linear_parts(dv), behind ? end : nullptr, dk / 16,
                               heads ? nullptr : dg, heads ? sums : nullptr, st);
     if (e == hipSuccess && heads) e = gdr::launch_linear_dg_heads(b, sums, dg, st);
     if (e != hipSuccess) return hip_fail(e, who, "gate gradient");
