@@ -1084,26 +1084,56 @@ __global__ __launch_bounds__(256) void linear_group_sum_kernel(LinearBatch b, co
 }
 
 // One token: row i of a state becomes alpha s_i + v_i k, its output scale s_i . q.
-template <Dt IN, Dt OUT>
-__global__ __launch_bounds__(256) void linear_decode_kernel(
-    const void* q, const void* k, const void* v, LinearGates g, float* state, void* o, int H,
-    int group, int dk, int dv, int64_t qs, int64_t ks, int64_t vs, float scale) {
-  const int blocks = dv / 16;
-  const int rb = blockIdx.x % blocks, nh = blockIdx.x / blocks;
-  const int n = nh / H, h = nh % H;
-  const int lane16 = threadIdx.x & 15, row = 16 * rb + (threadIdx.x >> 4);
-  const float alpha = expf(clamp_gate(g.per_token ? g.g[nh] : g.g[h]));
-  const float vv = load_scalar<IN>(v, n * vs + static_cast<size_t>(h) * dv + row);
-  float* s = state + (static_cast<size_t>(nh) * dv + row) * dk + lane16;
-  float acc = 0.f;
-  for (int i = 0; i < dk / 16; ++i) {
-    const size_t at = static_cast<size_t>(h / group) * dk + lane16 + 16 * i;
-    const float x = fmaf(vv, load_scalar<IN>(k, n * ks + at), alpha * s[16 * i]);
-    s[16 * i] = x;
-    acc = fmaf(x, load_scalar<IN>(q, n * qs + at), acc);
+// The state is read once and written once, and that stream is the whole cost:
+// 16 lanes to a row with 16-byte non-temporal accesses, ROWS rows of one head a
+// workgroup, every load issued before any arithmetic, no LDS.
+constexpr int kDecodeThreads = 256;
+
+template <int DK, int DV, Dt IN, Dt OUT, int ROWS>
+__global__ __launch_bounds__(kDecodeThreads) void linear_decode_kernel(
+    const void* __restrict__ q, const void* __restrict__ k, const void* __restrict__ v,
+    LinearGates gates, float* __restrict__ state, void* __restrict__ o, int H, int group,
+    int64_t qs, int64_t ks, int64_t vs, float scale) {
+  constexpr int RG = kDecodeThreads / 16, RPT = ROWS / RG, VEC = DK / 64, WPP = DV / ROWS;
+  const int pair = blockIdx.x / WPP, r0 = (blockIdx.x % WPP) * ROWS;
+  const int n = pair / H, h = pair % H, hk = h / group;
+  const int lane16 = threadIdx.x & 15, rg = threadIdx.x >> 4;
+  floatx4* S = reinterpret_cast<floatx4*>(state + static_cast<size_t>(pair) * DV * DK);
+  floatx4 st[RPT][VEC];
+#pragma unroll
+  for (int i = 0; i < RPT; ++i)
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+      st[i][j] = __builtin_nontemporal_load(&S[((r0 + rg + RG * i) * DK + 4 * lane16 + 64 * j) / 4]);
+  float kk[VEC][4], qq[VEC][4], vv[RPT];
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) {
+    const size_t at = static_cast<size_t>(hk) * DK + 4 * lane16 + 64 * j;
+    load_vec<IN, 4>(k, n * ks + at, kk[j]);
+    load_vec<IN, 4>(q, n * qs + at, qq[j]);
   }
-  acc = row16_sum(acc);
-  if (lane16 == 0) store_scalar<OUT>(o, static_cast<size_t>(nh) * dv + row, scale * acc);
+#pragma unroll
+  for (int i = 0; i < RPT; ++i)
+    vv[i] = load_scalar<IN>(v, n * vs + static_cast<size_t>(h) * DV + r0 + rg + RG * i);
+  const float alpha = expf(clamp_gate(gates.per_token ? gates.g[pair] : gates.g[h]));
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    float acc = 0.f;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = fmaf(vv[i], kk[j][e], alpha * st[i][j][e]);
+        st[i][j][e] = x;
+        acc = fmaf(x, qq[j][e], acc);
+      }
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+      __builtin_nontemporal_store(st[i][j], &S[((r0 + rg + RG * i) * DK + 4 * lane16 + 64 * j) / 4]);
+    acc = row16_sum(acc);
+    if (lane16 == i)
+      store_scalar<OUT>(o, static_cast<size_t>(pair) * DV + r0 + rg + RG * i, scale * acc);
+  }
 }
 
 }  // namespace
@@ -1112,17 +1142,28 @@ hipError_t launch_linear_decode(const void* q, const void* k, const void* v,
                                 const LinearGates& g, float* state, void* o, int N, int H, int Hk,
                                 int dk, int dv, int64_t qs, int64_t ks, int64_t vs, float scale,
                                 int in_dtype, int out_dtype, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(N) * H * (dv / 16));
-  auto go = [&](auto kern) {
-    hipLaunchKernelGGL(kern, grid, dim3(256), 0, stream, q, k, v, g, state, o, H, H / Hk, dk, dv,
-                       qs, ks, vs, scale);
+  constexpr int ROWS = 32;
+  const dim3 grid(static_cast<unsigned>(N) * H * (dv / ROWS));
+  const LinearGates gates = g;
+  auto by_out = [&](auto dkc, auto dvc, auto in) {
+    constexpr int DK = decltype(dkc)::value, DV = decltype(dvc)::value;
+    constexpr Dt IN = decltype(in)::value;
+    if (out_dtype == 0)
+      hipLaunchKernelGGL((linear_decode_kernel<DK, DV, IN, Dt::BF16, ROWS>), grid, dim3(kDecodeThreads),
+                         0, stream, q, k, v, gates, state, o, H, H / Hk, qs, ks, vs, scale);
+    else
+      hipLaunchKernelGGL((linear_decode_kernel<DK, DV, IN, Dt::F32, ROWS>), grid, dim3(kDecodeThreads),
+                         0, stream, q, k, v, gates, state, o, H, H / Hk, qs, ks, vs, scale);
     return hipGetLastError();
   };
-  if (in_dtype == 0)
-    return out_dtype == 0 ? go(linear_decode_kernel<Dt::BF16, Dt::BF16>)
-                          : go(linear_decode_kernel<Dt::BF16, Dt::F32>);
-  return out_dtype == 0 ? go(linear_decode_kernel<Dt::F32, Dt::BF16>)
-                        : go(linear_decode_kernel<Dt::F32, Dt::F32>);
+  const std::integral_constant<int, 64> d64;
+  const std::integral_constant<int, 128> d128;
+  auto by_dims = [&](auto in) {
+    if (dk == 64) return dv == 64 ? by_out(d64, d64, in) : by_out(d64, d128, in);
+    return dv == 64 ? by_out(d128, d64, in) : by_out(d128, d128, in);
+  };
+  return in_dtype == 0 ? by_dims(std::integral_constant<Dt, Dt::BF16>())
+                       : by_dims(std::integral_constant<Dt, Dt::F32>());
 }
 
 namespace {
