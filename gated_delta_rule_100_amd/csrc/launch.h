@@ -208,13 +208,14 @@ hipError_t launch_linear_starts(const LinearBatch& b, const LinearRows& y, const
                                 float us, int od, int kd, int backward, const float* from,
                                 float* states, float* decays, float* last, hipStream_t stream);
 
-// dg_t = dg_{t+1} + row_t - col_t over every unit, from its end's dot product;
-// row and col are [parts][H][T] partial sums, end_dot [parts][units * H].
-// dg_t goes to dg ([T, H]), or its sum over the unit's tokens to unit_sum
-// ([units * H]).
+// dg_t = dg_{t+1} + row_t - col_t over every unit, from its end's dot product and
+// back to its start's (NULL: zero); row and col are [parts][H][T] partial sums,
+// start_dot and end_dot [parts][units * H].  dg_t goes to dg ([T, H]), or its sum
+// over the unit's tokens to unit_sum ([units * H]).
 hipError_t launch_linear_dg(const LinearBatch& b, const float* row, int row_parts,
-                            const float* col, int col_parts, const float* end_dot, int end_parts,
-                            float* dg, double* unit_sum, hipStream_t stream);
+                            const float* col, int col_parts, const float* start_dot,
+                            int start_parts, const float* end_dot, int end_parts, float* dg,
+                            double* unit_sum, hipStream_t stream);
 
 // dg[h] = sum over units of unit_sum.
 hipError_t launch_linear_dg_heads(const LinearBatch& b, const double* unit_sum, float* dg,

@@ -993,23 +993,29 @@ __global__ __launch_bounds__(256) void linear_starts_kernel(LinearBatch b, int p
 
 // ---- gate gradient
 //
-// One workgroup a (unit, head): suffix sums of row - col, 256 tokens at a time
-// from the unit's end, in fp64.
+// One workgroup a (unit, head): suffix sums of row - col from the unit's end, 256
+// tokens at a time, in fp64.  The roundings of row and col add up like a random
+// walk over the unit, but its value at both ends is known as a product of two
+// states (start_dot, end_dot), so what the sums miss at the start is spread evenly
+// over the unit's tokens: 1024 tokens, 16 heads: relative error of dg 1.1e-6
+// without this.
 __global__ __launch_bounds__(256) void linear_dg_kernel(LinearBatch b, const float* row,
                                                         int row_parts, const float* col,
-                                                        int col_parts, const float* end_dot,
+                                                        int col_parts, const float* start_dot,
+                                                        int start_parts, const float* end_dot,
                                                         int end_parts, float* dg, double* unit_sum) {
   __shared__ double wave_sum[2][4];
   const int pair = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = pair % b.H;
   Unit unit;
   double total = 0.0;
-  if (unit_at(b, pair / b.H, unit)) {
+  if (unit_at(b, pair / b.H, unit) && unit.te > unit.tb) {
     const size_t th = static_cast<size_t>(b.T_total) * b.H, units = static_cast<size_t>(b.units) * b.H;
-    double acc = 0.0;
+    double acc = 0.0, start = 0.0;
     if (end_dot)
       for (int i = 0; i < end_parts; ++i) acc += end_dot[i * units + pair];
-    auto load = [&](int hi) {
-      const int t = hi - 1 - tid;  // thread 0 has the latest token
+    if (start_dot)
+      for (int i = 0; i < start_parts; ++i) start += start_dot[i * units + pair];
+    auto load = [&](int t) {
       double v = 0.0;
       if (t >= unit.tb) {
         const size_t at = static_cast<size_t>(h) * b.T_total + t;
@@ -1018,10 +1024,19 @@ __global__ __launch_bounds__(256) void linear_dg_kernel(LinearBatch b, const flo
       }
       return v;
     };
-    double ahead = load(unit.te);
+    double all = 0.0;
+    for (int t = unit.te - 1 - tid; t >= unit.tb; t -= 256) all += load(t);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) all += __shfl_xor(all, d);
+    if (lane == 0) wave_sum[1][wave] = all;
+    __syncthreads();
+    all = wave_sum[1][0] + wave_sum[1][1] + wave_sum[1][2] + wave_sum[1][3];
+    const double miss = (start - acc - all) / (unit.te - unit.tb);  // a token
+    double ahead = load(unit.te - 1 - tid);
     for (int hi = unit.te, slot = 0; hi > unit.tb; hi -= 256, slot ^= 1) {
+      const int t = hi - 1 - tid;  // thread 0 has the latest token
       double v = ahead;
-      if (hi - 256 > unit.tb) ahead = load(hi - 256);
+      ahead = load(t - 256);
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) {
         const double up = __shfl_up(v, d);
@@ -1035,8 +1050,8 @@ __global__ __launch_bounds__(256) void linear_dg_kernel(LinearBatch b, const flo
         if (i < wave) v += wave_sum[slot][i];
         acc += wave_sum[slot][i];
       }
-      const int t = hi - 1 - tid;
       if (t >= unit.tb) {
+        v += miss * (unit.te - t);
         total += v;
         if (dg) dg[static_cast<size_t>(t) * b.H + h] = static_cast<float>(v);
       }
@@ -1244,10 +1259,11 @@ hipError_t launch_linear_starts(const LinearBatch& b, const LinearRows& y, const
 }
 
 hipError_t launch_linear_dg(const LinearBatch& b, const float* row, int row_parts,
-                            const float* col, int col_parts, const float* end_dot, int end_parts,
-                            float* dg, double* unit_sum, hipStream_t stream) {
+                            const float* col, int col_parts, const float* start_dot,
+                            int start_parts, const float* end_dot, int end_parts, float* dg,
+                            double* unit_sum, hipStream_t stream) {
   hipLaunchKernelGGL(linear_dg_kernel, dim3(b.units * b.H), dim3(256), 0, stream, b, row, row_parts,
-                     col, col_parts, end_dot, end_parts, dg, unit_sum);
+                     col, col_parts, start_dot, start_parts, end_dot, end_parts, dg, unit_sum);
   return hipGetLastError();
 }
 

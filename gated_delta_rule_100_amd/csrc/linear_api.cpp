@@ -114,8 +114,8 @@ SegmentSizes segment_sizes(int T_total, int N, int H, int dk, int dv, int kinds)
 // decay a head.
 struct BackwardSizes {
   SegmentSizes seg;
-  size_t part_q = 0, part_k = 0, row = 0, col = 0, end = 0, sums = 0;
-  size_t total() const { return seg.total() + part_q + part_k + row + col + end + sums; }
+  size_t part_q = 0, part_k = 0, row = 0, col = 0, start = 0, end = 0, sums = 0;
+  size_t total() const { return seg.total() + part_q + part_k + row + col + start + end + sums; }
 };
 
 BackwardSizes backward_sizes(int T_total, int N, int H, int Hk, int dk, int dv) {
@@ -126,6 +126,7 @@ BackwardSizes backward_sizes(int T_total, int N, int H, int Hk, int dk, int dv) 
   if (H != Hk) z.part_q = z.part_k = align_up(th * dk);
   z.row = align_up(th * gdr::linear_parts(dk));
   z.col = align_up(th * gdr::linear_parts(dv));
+  z.start = align_up(pairs * (dv / 16) * sizeof(float));
   z.end = align_up(pairs * (dk / 16) * sizeof(float));
   z.sums = align_up(pairs * sizeof(double));
   return z;
@@ -281,6 +282,7 @@ gdr_status gdr_linear_backward(const void* q, const void* k, const void* v, cons
   float* part_k = ws.take<float>(z.part_k);
   float* row = ws.take<float>(z.row);
   float* col = ws.take<float>(z.col);
+  float* start = ws.take<float>(z.start);
   float* end = ws.take<float>(z.end);
   double* sums = ws.take<double>(z.sums);
   const LinearRows rq{q, q_stride, group}, rk{k, k_stride, group}, rv{v, v_stride, 1},
@@ -310,7 +312,11 @@ gdr_status gdr_linear_backward(const void* q, const void* k, const void* v, cons
   }
   pv.x = rk; pv.y = rq; pv.w = rd; pv.e = rv;
   pv.out = dv_out; pv.out_dtype = grad_dtype;
-  pv.dot = dg ? col : nullptr;
+  if (dg) {
+    pv.dot = col;
+    pv.end_with = from;
+    pv.end_dot = start;
+  }
   pv.start = behind;
   pv.end = dstate_in;
   pv.row = dk; pv.col = 1; pv.od = dv; pv.kd = dk;
@@ -332,8 +338,8 @@ gdr_status gdr_linear_backward(const void* q, const void* k, const void* v, cons
   }
   if (dg) {
     const bool heads = decay == GDR_DECAY_HEAD;
-    e = gdr::launch_linear_dg(b, row, gdr::linear_parts(dk), col, gdr::linear_parts(dv), behind ? end : nullptr, dk / 16,
-                              heads ? nullptr : dg, heads ? sums : nullptr, st);
+    e = gdr::launch_linear_dg(b, row, gdr::linear_parts(dk), col, gdr::linear_parts(dv),
+                              from ? start : nullptr, dv / 16, behind ? end : nullptr, dk / 16, heads ? nullptr : dg, heads ? sums : nullptr, st);
     if (e == hipSuccess && heads) e = gdr::launch_linear_dg_heads(b, sums, dg, st);
     if (e != hipSuccess) return hip_fail(e, who, "gate gradient");
   }
