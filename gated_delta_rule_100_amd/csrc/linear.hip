@@ -1052,6 +1052,8 @@ __global__ __launch_bounds__(256) void linear_dg_kernel(LinearBatch b, const flo
       }
       if (t >= unit.tb) {
         v += miss * (unit.te - t);
+        if ((b.gates.per_token ? b.gates.g[static_cast<size_t>(t) * b.H + h] : b.gates.g[h]) < kMinGate)
+          v = 0.0;  // a decay of zero
         total += v;
         if (dg) dg[static_cast<size_t>(t) * b.H + h] = static_cast<float>(v);
       }

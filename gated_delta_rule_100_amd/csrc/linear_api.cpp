@@ -339,7 +339,8 @@ gdr_status gdr_linear_backward(const void* q, const void* k, const void* v, cons
   if (dg) {
     const bool heads = decay == GDR_DECAY_HEAD;
     e = gdr::launch_linear_dg(b, row, gdr::linear_parts(dk), col, gdr::linear_parts(dv),
-                              from ? start : nullptr, dv / 16, behind ? end : nullptr, dk / 16, heads ? nullptr : dg, heads ? sums : nullptr, st);
+                              from ? start : nullptr, dv / 16, behind ? end : nullptr, dk / 16,
+                              heads ? nullptr : dg, heads ? sums : nullptr, st);
     if (e == hipSuccess && heads) e = gdr::launch_linear_dg_heads(b, sums, dg, st);
     if (e != hipSuccess) return hip_fail(e, who, "gate gradient");
   }

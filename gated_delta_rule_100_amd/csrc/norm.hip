@@ -110,9 +110,50 @@ __device__ __forceinline__ float row_sum(float x, float (*lds)[16], int& slot) {
   return x;
 }
 
-__device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
+// 1 / (1 + e^-z) by the hardware's base-2 exponential and reciprocal (one unit in
+// the last place each; e^-z may overflow to infinity: 0).
+__device__ __forceinline__ float sigmoid(float z) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));
+}
 
+// A row's operands as loaded, for 16-byte accesses: the next row's are read while
+// one is computed.
+template <Dt IN, int E>
+struct RawRow {
+  static constexpr int N = E / 8 * (IN == Dt::BF16 ? 1 : 2);
+  uint4 v[N];
+};
 template <Dt IN, int TPR, int E>
+__device__ __forceinline__ void load_raw(const void* base, size_t row, int D, int t, RawRow<IN, E>& r) {
+  constexpr int PER = IN == Dt::BF16 ? 1 : 2;
+  const char* p = static_cast<const char*>(base) + row * D * (IN == Dt::BF16 ? 2 : 4);
+#pragma unroll
+  for (int j = 0; j < E / 8; ++j) {
+    const int c = (j * TPR + t) * 8;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      r.v[PER * j + i] = c < D ? reinterpret_cast<const uint4*>(p + c * (PER == 1 ? 2 : 4))[i]
+                               : make_uint4(0, 0, 0, 0);
+  }
+}
+template <Dt IN, int E>
+__device__ __forceinline__ void widen(const RawRow<IN, E>& r, float (&x)[E]) {
+#pragma unroll
+  for (int j = 0; j < RawRow<IN, E>::N; ++j) {
+    const uint32_t w[4] = {r.v[j].x, r.v[j].y, r.v[j].z, r.v[j].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (IN == Dt::BF16) {
+        x[8 * j + 2 * i] = __uint_as_float(w[i] << 16);
+        x[8 * j + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      } else {
+        x[4 * j + i] = __uint_as_float(w[i]);
+      }
+    }
+  }
+}
+
+template <Dt IN, int TPR, int E, int NR>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_kernel(BlockNorm p) {
   constexpr int THREADS = TPR > 256 ? TPR : 256, RPB = THREADS / TPR;
   __shared__ float lds[2][16];
@@ -120,41 +161,52 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_kernel(Block
   const int t = threadIdx.x % TPR;
   const bool vec = p.D % 8 == 0;
   const float inv_d = 1.f / static_cast<float>(p.D);
-  const size_t row = static_cast<size_t>(blockIdx.x) * RPB + threadIdx.x / TPR;
-  if (row >= static_cast<size_t>(p.rows)) return;  // whole rows: no barrier is missed (RPB > 1
-                                                   // only where a row is inside one wave)
-  float x[E], z[E], r[E];
-  load_row<IN, TPR, E>(p.x, row, p.D, t, vec, x);
-  if (p.gate) load_row<IN, TPR, E>(p.gate, row, p.D, t, vec, z);
-  if (p.residual) load_row<IN, TPR, E>(p.residual, row, p.D, t, vec, r);
-  if (p.w_after) {
-    float w[E];
-    load_weight<TPR, E>(p.w_after, p.w_dtype, p.D, t, vec, w);
-    float ss = 0.f;
+  const size_t row0 = static_cast<size_t>(blockIdx.x) * RPB * NR + threadIdx.x / TPR;
+  // NR rows a thread, all of them loaded first (NR > 1 only where a row is inside
+  // one wave, so that no barrier is missed)
+  float x[NR][E], z[NR][E], r[NR][E];
 #pragma unroll
-    for (int i = 0; i < E; ++i) ss = fmaf(x[i], x[i], ss);
-    const float inv = rsqrtf(row_sum<TPR>(ss, lds, slot) * inv_d + p.eps);
-#pragma unroll
-    for (int i = 0; i < E; ++i) x[i] = x[i] * inv * w[i];
+  for (int n = 0; n < NR; ++n) {
+    const size_t row = row0 + n * RPB;
+    if (row >= static_cast<size_t>(p.rows)) continue;
+    load_row<IN, TPR, E>(p.x, row, p.D, t, vec, x[n]);
+    if (p.gate) load_row<IN, TPR, E>(p.gate, row, p.D, t, vec, z[n]);
+    if (p.residual) load_row<IN, TPR, E>(p.residual, row, p.D, t, vec, r[n]);
   }
-  if (p.gate) {
+  float wa[E], wb[E];
+  if (p.w_after) load_weight<TPR, E>(p.w_after, p.w_dtype, p.D, t, vec, wa);
+  if (p.w_before) load_weight<TPR, E>(p.w_before, p.w_dtype, p.D, t, vec, wb);
 #pragma unroll
-    for (int i = 0; i < E; ++i) x[i] *= sigmoid(z[i]) * (p.act == 0 ? z[i] : 1.f);
+  for (int n = 0; n < NR; ++n) {
+    const size_t row = row0 + n * RPB;
+    if (row >= static_cast<size_t>(p.rows)) continue;
+    if (p.w_after) {
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < E; ++i) ss = fmaf(x[n][i], x[n][i], ss);
+      const float inv = rsqrtf(row_sum<TPR>(ss, lds, slot) * inv_d + p.eps);
+#pragma unroll
+      for (int i = 0; i < E; ++i) x[n][i] = x[n][i] * inv * wa[i];
+    }
+    if (p.gate) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) x[n][i] *= sigmoid(z[n][i]) * (p.act == 0 ? z[n][i] : 1.f);
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      x[n][i] = p.residual ? fmaf(p.scale, x[n][i], r[n][i]) : p.scale * x[n][i];
+    if (p.w_before) {
+      float y[E];
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < E; ++i) ss = fmaf(x[n][i], x[n][i], ss);
+      const float inv = rsqrtf(row_sum<TPR>(ss, lds, slot) * inv_d + p.eps);
+#pragma unroll
+      for (int i = 0; i < E; ++i) y[i] = x[n][i] * inv * wb[i];
+      store_row<TPR, E>(p.y, p.out_dtype, row, p.D, t, vec, y);
+    }
+    if (p.h) store_row<TPR, E>(p.h, p.out_dtype, row, p.D, t, vec, x[n]);
   }
-#pragma unroll
-  for (int i = 0; i < E; ++i) x[i] = p.residual ? fmaf(p.scale, x[i], r[i]) : p.scale * x[i];
-  if (p.w_before) {
-    float w[E], y[E];
-    load_weight<TPR, E>(p.w_before, p.w_dtype, p.D, t, vec, w);
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < E; ++i) ss = fmaf(x[i], x[i], ss);
-    const float inv = rsqrtf(row_sum<TPR>(ss, lds, slot) * inv_d + p.eps);
-#pragma unroll
-    for (int i = 0; i < E; ++i) y[i] = x[i] * inv * w[i];
-    store_row<TPR, E>(p.y, p.out_dtype, row, p.D, t, vec, y);
-  }
-  if (p.h) store_row<TPR, E>(p.h, p.out_dtype, row, p.D, t, vec, x);
 }
 
 template <Dt IN, int TPR, int E>
@@ -170,16 +222,35 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_backward_ker
   for (int i = 0; i < E; ++i) wa[i] = wb[i] = ga[i] = gb[i] = 0.f;
   if (p.w_after) load_weight<TPR, E>(p.w_after, p.w_dtype, p.D, t, vec, wa);
   if (p.w_before) load_weight<TPR, E>(p.w_before, p.w_dtype, p.D, t, vec, wb);
-  for (size_t row = static_cast<size_t>(blockIdx.x) * RPB + sub; row < static_cast<size_t>(p.rows);
-       row += static_cast<size_t>(gridDim.x) * RPB) {
-    float x[E], z[E], d[E];
-    load_row<IN, TPR, E>(p.x, row, p.D, t, vec, x);
-    if (p.gate) load_row<IN, TPR, E>(p.gate, row, p.D, t, vec, z);
-    if (p.dh) {
-      load_row<IN, TPR, E>(p.dh, row, p.D, t, vec, d);
-    } else {
+  const size_t rows = static_cast<size_t>(p.rows), step = static_cast<size_t>(gridDim.x) * RPB;
+  size_t row = static_cast<size_t>(blockIdx.x) * RPB + sub;
+  RawRow<IN, E> nx, nz, nd, nr, ny;
+  auto read = [&](size_t at) {
+    if (!vec || at >= rows) return;
+    load_raw<IN, TPR, E>(p.x, at, p.D, t, nx);
+    if (p.gate) load_raw<IN, TPR, E>(p.gate, at, p.D, t, nz);
+    if (p.dh) load_raw<IN, TPR, E>(p.dh, at, p.D, t, nd);
+    if (p.w_before) load_raw<IN, TPR, E>(p.dy, at, p.D, t, ny);
+    if (p.w_before && p.residual) load_raw<IN, TPR, E>(p.residual, at, p.D, t, nr);
+  };
+  read(row);
+  for (; row < rows; row += step) {
+    float x[E], z[E], d[E], h[E], dy[E];
 #pragma unroll
-      for (int i = 0; i < E; ++i) d[i] = 0.f;
+    for (int i = 0; i < E; ++i) d[i] = h[i] = 0.f;
+    if (vec) {
+      widen<IN, E>(nx, x);
+      if (p.gate) widen<IN, E>(nz, z);
+      if (p.dh) widen<IN, E>(nd, d);
+      if (p.w_before) widen<IN, E>(ny, dy);
+      if (p.w_before && p.residual) widen<IN, E>(nr, h);
+      read(row + step);
+    } else {
+      load_row<IN, TPR, E>(p.x, row, p.D, t, vec, x);
+      if (p.gate) load_row<IN, TPR, E>(p.gate, row, p.D, t, vec, z);
+      if (p.dh) load_row<IN, TPR, E>(p.dh, row, p.D, t, vec, d);
+      if (p.w_before) load_row<IN, TPR, E>(p.dy, row, p.D, t, vec, dy);
+      if (p.w_before && p.residual) load_row<IN, TPR, E>(p.residual, row, p.D, t, vec, h);
     }
     float ix = 1.f;
     if (p.w_after) {
@@ -189,14 +260,6 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_backward_ker
       ix = rsqrtf(row_sum<TPR>(ss, lds, slot) * inv_d + p.eps);
     }
     if (p.w_before) {
-      float h[E], dy[E];
-      load_row<IN, TPR, E>(p.dy, row, p.D, t, vec, dy);
-      if (p.residual) {
-        load_row<IN, TPR, E>(p.residual, row, p.D, t, vec, h);
-      } else {
-#pragma unroll
-        for (int i = 0; i < E; ++i) h[i] = 0.f;
-      }
       float ss = 0.f;
 #pragma unroll
       for (int i = 0; i < E; ++i) {
@@ -275,24 +338,28 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_backward_ker
 }
 
 // dw[c] = sum over the workgroups' rows of part[., c]: 32 columns a workgroup,
-// 8 threads to a column.
-__global__ __launch_bounds__(256) void block_norm_weights_kernel(const float* pa, const float* pb,
-                                                                 float* dwa, float* dwb, int parts,
-                                                                 int D) {
+// 32 threads to a column.
+__global__ __launch_bounds__(1024) void block_norm_weights_kernel(const float* pa, const float* pb,
+                                                                  float* dwa, float* dwb, int parts,
+                                                                  int D) {
   const float* part = blockIdx.y == 0 ? pa : pb;
   float* dw = blockIdx.y == 0 ? dwa : dwb;
   if (!dw) return;
-  __shared__ float lds[8][33];
+  __shared__ float lds[32][33];
   const int cc = threadIdx.x & 31, rr = threadIdx.x >> 5, c = blockIdx.x * 32 + cc;
-  float sum = 0.f;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
   if (c < D)
-    for (int i = rr; i < parts; i += 8) sum += part[static_cast<size_t>(i) * D + c];
-  lds[rr][cc] = sum;
+    for (int i = rr; i < parts; i += 128)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i + 32 * j < parts) sum[j] += part[static_cast<size_t>(i + 32 * j) * D + c];
+  lds[rr][cc] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
   __syncthreads();
   if (rr == 0 && c < D) {
-    sum = 0.f;
-    for (int i = 0; i < 8; ++i) sum += lds[i][cc];
-    dw[c] = sum;
+    float all = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) all += lds[i][cc];
+    dw[c] = all;
   }
 }
 
@@ -321,20 +388,30 @@ int rows_per_block(int D) { return D <= 64 ? 32 : D <= 128 ? 16 : D <= 256 ? 8 :
 
 int block_norm_backward_blocks(int64_t rows, int D) {
   const int64_t rpb = rows_per_block(D), n = (rows + rpb - 1) / rpb;
-  return static_cast<int>(n < 512 ? n : 512);
+  return static_cast<int>(n < 1024 ? n : 1024);
 }
 
 hipError_t launch_block_norm(const BlockNorm& p, hipStream_t stream) {
   const int64_t rpb = rows_per_block(p.D);
-  const dim3 grid(static_cast<unsigned>((p.rows + rpb - 1) / rpb));
-  return by_width(p.D, [&](auto tpr, auto e) {
-    constexpr int T = decltype(tpr)::value, E = decltype(e)::value;
-    const dim3 block(T > 256 ? T : 256);
-    if (p.in_dtype == 0)
-      hipLaunchKernelGGL((block_norm_kernel<Dt::BF16, T, E>), grid, block, 0, stream, p);
-    else
-      hipLaunchKernelGGL((block_norm_kernel<Dt::F32, T, E>), grid, block, 0, stream, p);
-    return hipGetLastError();
+  return by_width(p.D, [&](auto tpr, auto el) {
+    constexpr int T = decltype(tpr)::value, E = decltype(el)::value;
+    auto go = [&](auto in, auto nr) {
+      constexpr int NR = decltype(nr)::value;
+      const dim3 grid(static_cast<unsigned>((p.rows + rpb * NR - 1) / (rpb * NR)));
+      hipLaunchKernelGGL((block_norm_kernel<decltype(in)::value, T, E, NR>), grid,
+                         dim3(T > 256 ? T : 256), 0, stream, p);
+      return hipGetLastError();
+    };
+    const std::integral_constant<Dt, Dt::BF16> bf16;
+    const std::integral_constant<Dt, Dt::F32> f32;
+    const std::integral_constant<int, 1> one;
+    if constexpr (T <= 64 && E == 8) {
+      const std::integral_constant<int, 2> two;
+      // two rows a thread once one a thread would be more than 32 workgroups a
+      // compute unit
+      if (p.rows > 8192 * rpb) return p.in_dtype == 0 ? go(bf16, two) : go(f32, two);
+    }
+    return p.in_dtype == 0 ? go(bf16, one) : go(f32, one);
   });
 }
 
@@ -356,7 +433,7 @@ hipError_t launch_block_norm_backward(const BlockNorm& p, float* dw_after, float
     if (e != hipSuccess) return e;
   }
   if (!dw_after && !dw_before) return hipSuccess;
-  hipLaunchKernelGGL(block_norm_weights_kernel, dim3((p.D + 31) / 32, 2), dim3(256), 0, stream,
+  hipLaunchKernelGGL(block_norm_weights_kernel, dim3((p.D + 31) / 32, 2), dim3(1024), 0, stream,
                      p.part_after, p.part_before, dw_after, dw_before, blocks, p.D);
   return hipGetLastError();
 }
