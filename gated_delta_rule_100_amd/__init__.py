@@ -324,15 +324,49 @@ def gdr_state_fixup(L, M, state_in, chunk_offsets, fixed, stream=None) -> None:
     _check(st, "gdr_state_fixup")
 
 
-def _rows_ptr(t, name, dtypes):
-    """Pointer and token stride of a [tokens, heads, d] tensor whose tokens may
-    be rows of a wider tensor (stride 0: dense)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+# The binding below is on the path of single tokens, where a call costs about as
+# much on the host as on the GPU: the current stream is read as a raw handle and
+# the device is switched only when it has to be.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _device(t, name):
+    """Index of the GPU that holds t."""
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if dev < 0 or not t.is_cuda:
         raise GdrError(f"{name} must be a torch tensor on the GPU")
+    return dev
+
+
+def _ptr(t, name, dtypes, dev):
+    """Pointer of a contiguous tensor on GPU `dev` (None: NULL)."""
+    if t is None:
+        return None
+    if _device(t, name) != dev:
+        raise GdrError(f"{name} is on another device than the first tensor")
+    if not t.is_contiguous():
+        raise GdrError(f"{name} must be contiguous")
     if t.dtype not in dtypes:
         raise GdrError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    return t.data_ptr()
+
+
+def _need(t, name):
+    if t is None:
+        raise GdrError(f"{name} is required")
+    return t
+
+
+def _rows_ptr(t, name, dev):
+    """Pointer and token stride of a [tokens, heads, d] tensor whose tokens may
+    be rows of a wider tensor (stride 0: dense)."""
     if t.is_contiguous():
-        return t.data_ptr(), 0
+        return _ptr(t, name, _IO, dev), 0
+    if _device(t, name) != dev:
+        raise GdrError(f"{name} is on another device than the first tensor")
+    if t.dtype not in _IO:
+        raise GdrError(f"{name} has dtype {t.dtype}, expected one of {_IO}")
     n, h, d = t.shape
     st, sh, sd = t.stride()
     if sd != 1 or (h > 1 and sh != d) or (n > 1 and st < h * d):
@@ -340,22 +374,45 @@ def _rows_ptr(t, name, dtypes):
     return t.data_ptr(), st if n > 1 else 0
 
 
-def _gates(g, tokens, H, who):
+def _gates(g, tokens, H, dev, who):
     """Pointer and decay code of g, [tokens, H] or [H]."""
     if g.shape == (tokens, H):
-        return _dev_ptr(g, "g", _F32), GDR_DECAY_TOKEN
+        return _ptr(g, "g", _F32, dev), GDR_DECAY_TOKEN
     if g.shape == (H,):
-        return _dev_ptr(g, "g", _F32), GDR_DECAY_HEAD
+        return _ptr(g, "g", _F32, dev), GDR_DECAY_HEAD
     raise GdrError(f"{who}: g must have shape {(tokens, H)} or {(H,)}")
 
 
-def _same_device(who, *tensors):
-    """The one device of the tensors, as a context in which to launch."""
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise GdrError(f"{who}: tensors are on {dev} and {t.device}")
-    return torch.cuda.device(dev)
+def _workspace(workspace, need, dev, stream):
+    """Pointer, size and tensor of the caller's workspace, or of one allocated
+    here on the launch stream (none when none is needed)."""
+    if workspace is None:
+        if not need:
+            return None, 0, None
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        else:
+            with torch.cuda.stream(_stream_obj(stream)):
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    return _ptr(workspace, "workspace", (torch.uint8,), dev), workspace.numel(), workspace
+
+
+def _launch(who, fn, dev, stream, *args):
+    """fn(*args, stream) with GPU `dev` current; raises on a non-OK status."""
+    handle = _raw_stream(dev) if stream is None else _stream(stream)
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, handle)
+    if st != 0:
+        _check(st, who)
+
+
+def _same_dtype(who, names, first, *others):
+    for t in others:
+        if t.dtype != first.dtype:
+            raise GdrError(f"{who}: {names} must share a dtype")
 
 
 def gdr_linear_decode(q, k, v, g, state, o, *, scale=1.0, stream=None) -> None:
@@ -370,15 +427,15 @@ def gdr_linear_decode(q, k, v, g, state, o, *, scale=1.0, stream=None) -> None:
     if k.shape != q.shape or v.shape[0] != N or state.shape != (N, H, dv, dk) \
             or o.shape != (N, H, dv):
         raise GdrError(f"{who}: inconsistent shapes")
-    if k.dtype != q.dtype or v.dtype != q.dtype:
-        raise GdrError(f"{who}: q, k, v must share a dtype")
-    (qp, qs), (kp, ks), (vp, vs) = (_rows_ptr(t, n, _IO) for t, n in ((q, "q"), (k, "k"), (v, "v")))
-    gp, decay = _gates(g, N, H, who)
-    sp, op = _dev_ptr(state, "state", _F32), _dev_ptr(o, "o", _IO)
-    with _same_device(who, q, k, v, g, state, o):
-        st = _load().gdr_linear_decode(qp, kp, vp, gp, sp, op, N, H, Hk, dk, dv, qs, ks, vs, scale,
-                                       decay, _code(q.dtype), _code(o.dtype), _stream(stream))
-    _check(st, who)
+    _same_dtype(who, "q, k, v", q, k, v)
+    dev = _device(q, "q")
+    qp, qs = _rows_ptr(q, "q", dev)
+    kp, ks = _rows_ptr(k, "k", dev)
+    vp, vs = _rows_ptr(v, "v", dev)
+    gp, decay = _gates(g, N, H, dev, who)
+    _launch(who, _load().gdr_linear_decode, dev, stream, qp, kp, vp, gp,
+            _ptr(state, "state", _F32, dev), _ptr(o, "o", _IO, dev), N, H, Hk, dk, dv, qs, ks, vs,
+            scale, decay, _code(q.dtype), _code(o.dtype))
 
 
 def gdr_linear_prefill_workspace_bytes(T_total, N, H, dk, dv, in_dtype=GDR_BF16) -> int:
@@ -396,34 +453,25 @@ def gdr_linear_backward_workspace_bytes(T_total, N, H, Hk, dk, dv, in_dtype=GDR_
 
 
 def _linear_args(who, q, k, v, g, cu_seqlens, state_in, like_v):
-    """Checks shared by prefill and backward; pointers of q, k, v, g, cu and
-    state_in, their strides, and the sizes."""
+    """Checks shared by prefill and backward; the device, the pointers of q, k,
+    v, g, cu and state_in, the strides, the decay code and the sizes."""
     T, Hk, dk = q.shape
     H, dv = v.shape[1:]
     N = cu_seqlens.shape[0] - 1
     if k.shape != q.shape or v.shape[0] != T or cu_seqlens.dim() != 1 \
             or any(t.shape != (T, H, dv) for t in like_v):
         raise GdrError(f"{who}: inconsistent shapes")
-    if k.dtype != q.dtype or v.dtype != q.dtype:
-        raise GdrError(f"{who}: q, k, v must share a dtype")
+    _same_dtype(who, "q, k, v", q, k, v)
     if state_in is not None and state_in.shape != (N, H, dv, dk):
         raise GdrError(f"{who}: state_in must have shape {(N, H, dv, dk)}")
-    (qp, qs), (kp, ks), (vp, vs) = (_rows_ptr(t, n, _IO) for t, n in ((q, "q"), (k, "k"), (v, "v")))
-    gp, decay = _gates(g, T, H, who)
-    ptrs = [qp, kp, vp, gp, _dev_ptr(cu_seqlens, "cu_seqlens", _I32), N,
-            _dev_ptr(state_in, "state_in", _F32, optional=True)]
-    return ptrs, (qs, ks, vs), decay, (T, N, H, Hk, dk, dv)
-
-
-def _workspace(workspace, need, device, stream):
-    """Pointer and size of the caller's workspace, or of one allocated here on
-    the launch stream (none when none is needed), and its tensor."""
-    if workspace is None and need:
-        with torch.cuda.stream(_stream_obj(stream)):
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    if workspace is None:
-        return None, 0, None
-    return _dev_ptr(workspace, "workspace", (torch.uint8,)), workspace.numel(), workspace
+    dev = _device(q, "q")
+    qp, qs = _rows_ptr(q, "q", dev)
+    kp, ks = _rows_ptr(k, "k", dev)
+    vp, vs = _rows_ptr(v, "v", dev)
+    gp, decay = _gates(g, T, H, dev, who)
+    ptrs = (qp, kp, vp, gp, _ptr(_need(cu_seqlens, "cu_seqlens"), "cu_seqlens", _I32, dev), N,
+            _ptr(state_in, "state_in", _F32, dev))
+    return dev, ptrs, (qs, ks, vs), decay, (T, N, H, Hk, dk, dv)
 
 
 def gdr_linear_prefill(q, k, v, g, cu_seqlens, state_in, state_out, o, *, scale=1.0,
@@ -436,18 +484,16 @@ def gdr_linear_prefill(q, k, v, g, cu_seqlens, state_in, state_out, o, *, scale=
     fp32.  workspace: as gdr_chunk_prefill's, by
     gdr_linear_prefill_workspace_bytes."""
     who = "gdr_linear_prefill"
-    ptrs, strides, decay, (T, N, H, Hk, dk, dv) = _linear_args(who, q, k, v, g, cu_seqlens,
-                                                               state_in, (o,))
+    dev, ptrs, strides, decay, (T, N, H, Hk, dk, dv) = _linear_args(who, q, k, v, g, cu_seqlens,
+                                                                    state_in, (o,))
     if state_out is not None and state_out.shape != (N, H, dv, dk):
         raise GdrError(f"{who}: state_out must have shape {(N, H, dv, dk)}")
-    sp, op = _dev_ptr(state_out, "state_out", _F32, optional=True), _dev_ptr(o, "o", _IO)
-    code = _code(q.dtype)
-    with _same_device(who, q, k, v, g, cu_seqlens, state_in, state_out, o, workspace):
-        need = _load().gdr_linear_prefill_workspace_bytes(T, N, H, dk, dv, code)
-        wp, wb, workspace = _workspace(workspace, need, q.device, stream)
-        st = _load().gdr_linear_prefill(*ptrs, sp, op, T, H, Hk, dk, dv, *strides, scale, decay,
-                                        code, _code(o.dtype), wp, wb, _stream(stream))
-    _check(st, who)
+    code, lib = _code(q.dtype), _load()
+    wp, wb, workspace = _workspace(
+        workspace, lib.gdr_linear_prefill_workspace_bytes(T, N, H, dk, dv, code), dev, stream)
+    _launch(who, lib.gdr_linear_prefill, dev, stream, *ptrs,
+            _ptr(state_out, "state_out", _F32, dev), _ptr(o, "o", _IO, dev), T, H, Hk, dk, dv,
+            *strides, scale, decay, code, _code(o.dtype), wp, wb)
 
 
 def gdr_linear_backward(q, k, v, g, cu_seqlens, state_in, do, dstate_out, dq, dk, dv, *, dg=None,
@@ -462,43 +508,42 @@ def gdr_linear_backward(q, k, v, g, cu_seqlens, state_in, do, dstate_out, dq, dk
     if dq.shape != q.shape or dk.shape != q.shape or (dg is not None and dg.shape != g.shape) \
             or any(t is not None and t.shape != states for t in (dstate_out, dstate_in)):
         raise GdrError(f"{who}: inconsistent shapes")
-    ptrs, strides, decay, (T, N, H, Hk, kd, vd) = _linear_args(who, q, k, v, g, cu_seqlens,
-                                                               state_in, (do, dv))
-    if dk.dtype != dq.dtype or dv.dtype != dq.dtype:
-        raise GdrError(f"{who}: dq, dk, dv must share a dtype")
-    outs = [_dev_ptr(do, "do", (q.dtype,)), _dev_ptr(dstate_out, "dstate_out", _F32, optional=True),
-            _dev_ptr(dq, "dq", _IO), _dev_ptr(dk, "dk", _IO), _dev_ptr(dv, "dv", _IO),
-            _dev_ptr(dg, "dg", _F32, optional=True),
-            _dev_ptr(dstate_in, "dstate_in", _F32, optional=True)]
-    code = _code(q.dtype)
-    with _same_device(who, q, k, v, g, cu_seqlens, state_in, do, dstate_out, dq, dk, dv, dg,
-                      dstate_in, workspace):
-        need = _load().gdr_linear_backward_workspace_bytes(T, N, H, Hk, kd, vd, code)
-        wp, wb, workspace = _workspace(workspace, need, q.device, stream)
-        st = _load().gdr_linear_backward(*ptrs, *outs, T, H, Hk, kd, vd, *strides, scale, decay,
-                                         code, _code(dq.dtype), wp, wb, _stream(stream))
-    _check(st, who)
+    dev, ptrs, strides, decay, (T, N, H, Hk, kd, vd) = _linear_args(who, q, k, v, g, cu_seqlens,
+                                                                    state_in, (do, dv))
+    _same_dtype(who, "dq, dk, dv", dq, dk, dv)
+    code, lib = _code(q.dtype), _load()
+    wp, wb, workspace = _workspace(
+        workspace, lib.gdr_linear_backward_workspace_bytes(T, N, H, Hk, kd, vd, code), dev, stream)
+    _launch(who, lib.gdr_linear_backward, dev, stream, *ptrs, _ptr(do, "do", (q.dtype,), dev),
+            _ptr(dstate_out, "dstate_out", _F32, dev), _ptr(dq, "dq", _IO, dev),
+            _ptr(dk, "dk", _IO, dev), _ptr(dv, "dv", _IO, dev), _ptr(dg, "dg", _F32, dev),
+            _ptr(dstate_in, "dstate_in", _F32, dev), T, H, Hk, kd, vd, *strides, scale, decay,
+            code, _code(dq.dtype), wp, wb)
 
 
 def _norm_args(who, x, w_after, gate, act, residual, w_before, like_x, outs):
     """Checks shared by the norm and its gradient: row operands like x, outputs
-    of one dtype, weights [D] of one dtype.  Returns rows, D and the codes of
-    gate, input, weights and outputs."""
-    D = x.shape[-1] if x.dim() else 0
+    of one dtype, weights [D] of one dtype.  Returns the device, rows, D and the
+    codes of gate, input, weights and outputs."""
+    shape = x.shape
+    D = shape[-1] if shape else 0
     for t in (gate, residual, *like_x):
-        if t is not None and (t.shape != x.shape or t.dtype != x.dtype):
+        if t is not None and (t.shape != shape or t.dtype != x.dtype):
             raise GdrError(f"{who}: row operands must have the shape and dtype of x")
-    outs = [t for t in outs if t is not None]
-    if any(t.shape != x.shape or t.dtype != outs[0].dtype for t in outs):
-        raise GdrError(f"{who}: outputs must have the shape of x and one dtype")
-    weights = [w for w in (w_after, w_before) if w is not None]
-    if any(w.shape != (D,) or w.dtype != weights[0].dtype for w in weights):
-        raise GdrError(f"{who}: weights must have shape {(D,)} and one dtype")
+    out = None
+    for t in outs:
+        if t is not None:
+            out = t if out is None else out
+            if t.shape != shape or t.dtype != out.dtype:
+                raise GdrError(f"{who}: outputs must have the shape of x and one dtype")
+    w = w_after if w_after is not None else w_before
+    for t in (w_after, w_before):
+        if t is not None and (t.shape != (D,) or t.dtype != w.dtype):
+            raise GdrError(f"{who}: weights must have shape {(D,)} and one dtype")
     if gate is not None and act not in GDR_GATES:
         raise GdrError(f"{who}: act must be one of {sorted(GDR_GATES)}")
-    return (x.numel() // D if D else 0, D, GDR_GATES.get(act, 0), _code(x.dtype),
-            _code(weights[0].dtype) if weights else GDR_FP32,
-            _code(outs[0].dtype) if outs else GDR_FP32)
+    return (_device(x, "x"), x.numel() // D if D else 0, D, GDR_GATES.get(act, 0), _code(x.dtype),
+            GDR_FP32 if w is None else _code(w.dtype), GDR_FP32 if out is None else _code(out.dtype))
 
 
 def gdr_block_norm(x, h=None, y=None, *, w_after=None, gate=None, act="silu", residual=None,
@@ -509,13 +554,12 @@ def gdr_block_norm(x, h=None, y=None, *, w_after=None, gate=None, act="silu", re
     residual like x; weights [D]; h and y [..., D] (h may be left out where y is
     wanted; y exactly with w_before).  bf16 or fp32 each."""
     who = "gdr_block_norm"
-    rows, D, ac, ic, wc, oc = _norm_args(who, x, w_after, gate, act, residual, w_before, (), (h, y))
-    p = [_dev_ptr(x, "x", _IO)] + [_dev_ptr(t, n, _IO, optional=True) for t, n in (
-        (w_after, "w_after"), (gate, "gate"), (residual, "residual"), (w_before, "w_before"),
-        (h, "h"), (y, "y"))]
-    with _same_device(who, x, w_after, gate, residual, w_before, h, y):
-        st = _load().gdr_block_norm(*p, rows, D, scale, eps, ac, ic, wc, oc, _stream(stream))
-    _check(st, who)
+    dev, rows, D, ac, ic, wc, oc = _norm_args(who, x, w_after, gate, act, residual, w_before, (),
+                                              (h, y))
+    _launch(who, _load().gdr_block_norm, dev, stream, _ptr(x, "x", _IO, dev),
+            _ptr(w_after, "w_after", _IO, dev), _ptr(gate, "gate", _IO, dev),
+            _ptr(residual, "residual", _IO, dev), _ptr(w_before, "w_before", _IO, dev),
+            _ptr(h, "h", _IO, dev), _ptr(y, "y", _IO, dev), rows, D, scale, eps, ac, ic, wc, oc)
 
 
 def gdr_block_norm_backward_workspace_bytes(rows, D) -> int:
@@ -531,21 +575,18 @@ def gdr_block_norm_backward(x, dh, dy, dx, *, w_after=None, gate=None, act="silu
     gdr_block_norm_backward_workspace_bytes(rows, D) bytes, or None to allocate
     one here on the launch stream."""
     who = "gdr_block_norm_backward"
-    rows, D, ac, ic, wc, oc = _norm_args(who, x, w_after, gate, act, residual, w_before, (dh, dy),
-                                         (dx, dgate, dresidual))
-    if any(t is not None and t.shape != (D,) for t in (dw_after, dw_before)):
-        raise GdrError(f"{who}: weight gradients must have shape {(D,)}")
-    p = [_dev_ptr(x, "x", _IO)] + [_dev_ptr(t, n, _IO, optional=True) for t, n in (
-        (w_after, "w_after"), (gate, "gate"), (residual, "residual"), (w_before, "w_before"),
-        (dh, "dh"), (dy, "dy"), (dx, "dx"), (dgate, "dgate"), (dresidual, "dresidual"))]
-    p += [_dev_ptr(t, n, _F32, optional=True) for t, n in ((dw_after, "dw_after"),
-                                                          (dw_before, "dw_before"))]
-    with _same_device(who, x, w_after, gate, residual, w_before, dh, dy, dx, dgate, dresidual,
-                      dw_after, dw_before, workspace):
-        need = 0
-        if dw_after is not None or dw_before is not None:
-            need = _load().gdr_block_norm_backward_workspace_bytes(rows, D)
-        wp, wb, workspace = _workspace(workspace, need, x.device, stream)
-        st = _load().gdr_block_norm_backward(*p, rows, D, scale, eps, ac, ic, wc, oc, wp, wb,
-                                             _stream(stream))
-    _check(st, who)
+    if any(t is not None and t.shape != x.shape[-1:] for t in (dw_after, dw_before)):
+        raise GdrError(f"{who}: weight gradients must have shape {tuple(x.shape[-1:])}")
+    dev, rows, D, ac, ic, wc, oc = _norm_args(who, x, w_after, gate, act, residual, w_before,
+                                              (dh, dy), (dx, dgate, dresidual))
+    lib, need = _load(), 0
+    if dw_after is not None or dw_before is not None:
+        need = lib.gdr_block_norm_backward_workspace_bytes(rows, D)
+    wp, wb, workspace = _workspace(workspace, need, dev, stream)
+    _launch(who, lib.gdr_block_norm_backward, dev, stream, _ptr(x, "x", _IO, dev),
+            _ptr(w_after, "w_after", _IO, dev), _ptr(gate, "gate", _IO, dev),
+            _ptr(residual, "residual", _IO, dev), _ptr(w_before, "w_before", _IO, dev),
+            _ptr(dh, "dh", _IO, dev), _ptr(dy, "dy", _IO, dev), _ptr(dx, "dx", _IO, dev),
+            _ptr(dgate, "dgate", _IO, dev), _ptr(dresidual, "dresidual", _IO, dev),
+            _ptr(dw_after, "dw_after", _F32, dev), _ptr(dw_before, "dw_before", _F32, dev),
+            rows, D, scale, eps, ac, ic, wc, oc, wp, wb)

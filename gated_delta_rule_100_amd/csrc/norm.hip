@@ -153,13 +153,12 @@ __device__ __forceinline__ void widen(const RawRow<IN, E>& r, float (&x)[E]) {
   }
 }
 
-template <Dt IN, int TPR, int E, int NR>
+template <Dt IN, int TPR, int E, int NR, bool vec>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_kernel(BlockNorm p) {
   constexpr int THREADS = TPR > 256 ? TPR : 256, RPB = THREADS / TPR;
   __shared__ float lds[2][16];
   int slot = 0;
   const int t = threadIdx.x % TPR;
-  const bool vec = p.D % 8 == 0;
   const float inv_d = 1.f / static_cast<float>(p.D);
   const size_t row0 = static_cast<size_t>(blockIdx.x) * RPB * NR + threadIdx.x / TPR;
   // NR rows a thread, all of them loaded first (NR > 1 only where a row is inside
@@ -209,13 +208,12 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_kernel(Block
   }
 }
 
-template <Dt IN, int TPR, int E>
-__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_backward_kernel(BlockNorm p) {
+template <Dt IN, int TPR, int E, bool vec>
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256, IN == Dt::BF16 && TPR <= 256 && E == 8 ? 4 : 1) void block_norm_backward_kernel(BlockNorm p) {
   constexpr int THREADS = TPR > 256 ? TPR : 256, RPB = THREADS / TPR;
   __shared__ float lds[2][16];
   int slot = 0;
   const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
-  const bool vec = p.D % 8 == 0;
   const float inv_d = 1.f / static_cast<float>(p.D);
   float wa[E], wb[E], ga[E], gb[E];
 #pragma unroll
@@ -224,9 +222,11 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_backward_ker
   if (p.w_before) load_weight<TPR, E>(p.w_before, p.w_dtype, p.D, t, vec, wb);
   const size_t rows = static_cast<size_t>(p.rows), step = static_cast<size_t>(gridDim.x) * RPB;
   size_t row = static_cast<size_t>(blockIdx.x) * RPB + sub;
+  // (rows of 1024 threads have no registers left for it)
+  constexpr bool AHEAD = vec && TPR <= 256;
   RawRow<IN, E> nx, nz, nd, nr, ny;
   auto read = [&](size_t at) {
-    if (!vec || at >= rows) return;
+    if (!AHEAD || at >= rows) return;
     load_raw<IN, TPR, E>(p.x, at, p.D, t, nx);
     if (p.gate) load_raw<IN, TPR, E>(p.gate, at, p.D, t, nz);
     if (p.dh) load_raw<IN, TPR, E>(p.dh, at, p.D, t, nd);
@@ -238,7 +238,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_backward_ker
     float x[E], z[E], d[E], h[E], dy[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) d[i] = h[i] = 0.f;
-    if (vec) {
+    if constexpr (AHEAD) {
       widen<IN, E>(nx, x);
       if (p.gate) widen<IN, E>(nz, z);
       if (p.dh) widen<IN, E>(nd, d);
@@ -398,8 +398,13 @@ hipError_t launch_block_norm(const BlockNorm& p, hipStream_t stream) {
     auto go = [&](auto in, auto nr) {
       constexpr int NR = decltype(nr)::value;
       const dim3 grid(static_cast<unsigned>((p.rows + rpb * NR - 1) / (rpb * NR)));
-      hipLaunchKernelGGL((block_norm_kernel<decltype(in)::value, T, E, NR>), grid,
-                         dim3(T > 256 ? T : 256), 0, stream, p);
+      const dim3 block(T > 256 ? T : 256);
+      if (p.D % 8 == 0)
+        hipLaunchKernelGGL((block_norm_kernel<decltype(in)::value, T, E, NR, true>), grid, block, 0,
+                           stream, p);
+      else
+        hipLaunchKernelGGL((block_norm_kernel<decltype(in)::value, T, E, NR, false>), grid, block, 0,
+                           stream, p);
       return hipGetLastError();
     };
     const std::integral_constant<Dt, Dt::BF16> bf16;
@@ -421,14 +426,15 @@ hipError_t launch_block_norm_backward(const BlockNorm& p, float* dw_after, float
   if (blocks > 0) {
     const hipError_t e = by_width(p.D, [&](auto tpr, auto el) {
       constexpr int T = decltype(tpr)::value, E = decltype(el)::value;
-      const dim3 block(T > 256 ? T : 256);
-      if (p.in_dtype == 0)
-        hipLaunchKernelGGL((block_norm_backward_kernel<Dt::BF16, T, E>), dim3(blocks), block, 0,
-                           stream, p);
-      else
-        hipLaunchKernelGGL((block_norm_backward_kernel<Dt::F32, T, E>), dim3(blocks), block, 0,
-                           stream, p);
-      return hipGetLastError();
+      auto go = [&](auto in, auto vec) {
+        hipLaunchKernelGGL((block_norm_backward_kernel<decltype(in)::value, T, E, decltype(vec)::value>),
+                           dim3(blocks), dim3(T > 256 ? T : 256), 0, stream, p);
+        return hipGetLastError();
+      };
+      const std::integral_constant<Dt, Dt::BF16> bf16;
+      const std::integral_constant<Dt, Dt::F32> f32;
+      if (p.D % 8 == 0) return p.in_dtype == 0 ? go(bf16, std::true_type()) : go(f32, std::true_type());
+      return p.in_dtype == 0 ? go(bf16, std::false_type()) : go(f32, std::false_type());
     });
     if (e != hipSuccess) return e;
   }
