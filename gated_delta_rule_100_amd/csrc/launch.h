@@ -150,7 +150,9 @@ struct LinearGates {
 
 // A packed batch, and the units its passes walk: the sequences (seg == 0,
 // units = N), or segments of seg tokens of them (launch_layout with seg as its
-// chunk: seg_offs [N + 1], seg_idx [units][2], slots past the real count -1).
+// chunk: seg_offs [N + 1], seg_idx [units][2], slots past the real count -1;
+// NULL for at most kInlineSeqs sequences, where the kernels form the table).
+constexpr int kInlineSeqs = 64;
 struct LinearBatch {
   const int32_t* cu;
   int N, H, T_total, in_dtype;
@@ -203,10 +205,15 @@ hipError_t launch_linear_pass(const LinearBatch& b, const LinearPass& p, hipStre
 // columns: the segments' own states from zero (y, w, us as in a pass) and their
 // decays [units * H], then the chain over each sequence's segments from `from`
 // ([N * H], NULL for zero).  last ([N * H] or NULL) gets `from` where a sequence
-// has no tokens.
-hipError_t launch_linear_starts(const LinearBatch& b, const LinearRows& y, const LinearRows& w,
-                                float us, int od, int kd, int backward, const float* from,
-                                float* states, float* decays, float* last, hipStream_t stream);
+// has no tokens.  One job forwards and, when given, one backwards.
+struct LinearStates {
+  LinearRows y, w;
+  float us;
+  const float* from;
+  float *states, *decays, *last;
+};
+hipError_t launch_linear_starts(const LinearBatch& b, int od, int kd, const LinearStates& forward,
+                                const LinearStates* backward, hipStream_t stream);
 
 // dg_t = dg_{t+1} + row_t - col_t over every unit, from its end's dot product and
 // back to its start's (NULL: zero); row and col are [parts][H][T] partial sums,

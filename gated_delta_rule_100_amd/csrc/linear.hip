@@ -31,11 +31,66 @@ __device__ __forceinline__ void token_range(const LinearBatch& b, int n, int& tb
 }
 
 // Sequence and tokens [tb, te) of a unit, and whether it is the first and the
-// last of its sequence; false for a slot without a segment.
+// last of its sequence.
 struct Unit {
   int n, tb, te;
   bool first, last;
 };
+
+// The units of a sequence: its first `count - tail` segments are units from,
+// from + 1, ..; with tail, its last one (shorter than the others) is unit tail_at.
+struct SequenceUnits {
+  int from, count, tail, tail_at;
+  __device__ __forceinline__ int at(int j) const { return j < count - tail ? from + j : tail_at; }
+};
+
+// The segment table of at most kInlineSeqs sequences, formed by every wave for
+// itself with one sequence a lane (a launch and a dependent read less than a
+// table in memory).  All whole segments come before all shorter ones, so that the
+// long walks start first: 8 sequences of 32768 tokens, 32 heads, scan 345 us in
+// the order of the sequences.
+struct SegmentPrefix {
+  int whole, tails;  // inclusive prefix sums, lane n for sequence n
+  int all_whole;
+};
+__device__ __forceinline__ SegmentPrefix segment_prefix(const LinearBatch& b, int lane) {
+  int tb = 0, te = 0;
+  if (lane < b.N) token_range(b, lane, tb, te);
+  SegmentPrefix p;
+  p.whole = (te - tb) / b.seg;
+  p.tails = (te - tb) % b.seg != 0;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int w = __shfl_up(p.whole, d), t = __shfl_up(p.tails, d);
+    if (lane >= d) {
+      p.whole += w;
+      p.tails += t;
+    }
+  }
+  p.all_whole = __builtin_amdgcn_readlane(p.whole, 63);
+  return p;
+}
+
+__device__ __forceinline__ SequenceUnits sequence_units(const LinearBatch& b, int n) {
+  SequenceUnits r;
+  if (b.seg_offs) {
+    int u0 = b.seg_offs[n], u1 = b.seg_offs[n + 1];
+    u0 = u0 < 0 ? 0 : (u0 > b.units ? b.units : u0);
+    u1 = u1 < u0 ? u0 : (u1 > b.units ? b.units : u1);
+    r = {u0, u1 - u0, 0, 0};
+  } else {
+    const SegmentPrefix p = segment_prefix(b, threadIdx.x & 63);
+    const int w1 = __builtin_amdgcn_readlane(p.whole, n), t1 = __builtin_amdgcn_readlane(p.tails, n);
+    const int w0 = n > 0 ? __builtin_amdgcn_readlane(p.whole, n - 1) : 0;
+    const int t0 = n > 0 ? __builtin_amdgcn_readlane(p.tails, n - 1) : 0;
+    r = {w0, w1 - w0 + t1 - t0, t1 - t0, p.all_whole + t0};
+    // (offsets that go back or past the tokens could name more units than there are)
+    if (r.from + r.count - r.tail > b.units || (r.tail && r.tail_at >= b.units)) r.count = r.tail = 0;
+  }
+  return r;
+}
+
+// False for a slot without a segment.
 __device__ __forceinline__ bool unit_at(const LinearBatch& b, int u, Unit& r) {
   if (b.seg == 0) {
     r.n = u;
@@ -43,9 +98,22 @@ __device__ __forceinline__ bool unit_at(const LinearBatch& b, int u, Unit& r) {
     token_range(b, u, r.tb, r.te);
     return true;
   }
-  r.n = b.seg_idx[2 * u];
-  const int j = b.seg_idx[2 * u + 1];
-  if (r.n < 0 || r.n >= b.N || j < 0) return false;
+  int j;
+  if (b.seg_idx) {
+    r.n = b.seg_idx[2 * u];
+    j = b.seg_idx[2 * u + 1];
+    if (r.n < 0 || r.n >= b.N || j < 0) return false;
+  } else {
+    const int lane = threadIdx.x & 63;
+    const SegmentPrefix p = segment_prefix(b, lane);
+    const bool whole = u < p.all_whole;
+    const int sum = whole ? p.whole : p.all_whole + p.tails;
+    const uint64_t later = __ballot(lane < b.N && u < sum);
+    if (later == 0) return false;
+    r.n = __builtin_ctzll(later);
+    const int before = r.n > 0 ? __builtin_amdgcn_readlane(p.whole, r.n - 1) : 0;
+    j = whole ? u - before : __builtin_amdgcn_readlane(p.whole, r.n) - before;
+  }
   int tb, te;
   token_range(b, r.n, tb, te);
   const int64_t from = tb + static_cast<int64_t>(j) * b.seg;
@@ -263,20 +331,19 @@ __device__ __forceinline__ Gates chunk_gates(float gate, bool per_token, int lan
 //     tiles of the state update: lane (c, g) holds Z[c][32 j + 8 g + 0..7],
 //     which is also the fragment of Z in the product with x.  In step s they
 //     form out = Z x + P w and the update of Z for chunk s;
-//   - 4 score waves form the scores x.y of chunk s + 1, with their decays, in
+//   - SW score waves form the scores x.y of chunk s + 1, with their decays, in
 //     registers: they do not depend on the state, and their arithmetic fills
 //     the issue slots that the compute waves' chain leaves;
-//   - 4 copy waves copy the x and y rows of chunk s + 2 and the w rows of chunk
+//   - SW copy waves copy the x and y rows of chunk s + 2 and the w rows of chunk
 //     s + 1 to LDS (global-to-LDS loads) and form the gate factors of s + 2.
 //     They are waves of their own because a wave's LDS reads wait for all its
 //     global-to-LDS loads in flight.
 // Two barriers a chunk: one behind its last reads, and one behind the score
 // waves' writing P^T for the next chunk (right after the former, while the
 // compute waves form Z x).
-constexpr int kScoreWaves = 4;
-constexpr int kCopyWaves = 4;
+constexpr int kCopyWaves = 4;  // of the segment states' kernel
 
-template <Dt IN, int KD, int W, int PZ, bool DOT>
+template <Dt IN, int KD, int W, int PZ, bool DOT, int SW>
 struct ScanCfg {
   static constexpr int ES = IN == Dt::BF16 ? 2 : 4;
   static constexpr int C = IN == Dt::BF16 ? 64 : 32;  // tokens a chunk (fp32: half, for LDS)
@@ -284,7 +351,8 @@ struct ScanCfg {
   static constexpr int KB = KD / 32;          // 32-deep blocks over kd
   static constexpr int VS = 16 * W;           // columns of w a workgroup
   static constexpr int CHK = KD * ES / 16, CHV = VS * ES / 16;
-  static constexpr int THREADS = 64 * (W + kScoreWaves + kCopyWaves);
+  static constexpr int CW = SW;  // as many copy waves as score waves
+  static constexpr int THREADS = 64 * (W + SW + CW);
   // three buffers of x and y rows, two of w rows
   static constexpr int X_BYTES = C * KD * ES, W_BYTES = C * VS * ES;
   static constexpr int OFF_W = 3 * 2 * X_BYTES;
@@ -328,10 +396,11 @@ __device__ __forceinline__ void store_state4(float* p, int64_t col, const floatx
   }
 }
 
-template <Dt IN, int KD, int W, int PZ, bool DOT, bool BACK>
-__global__ __launch_bounds__((ScanCfg<IN, KD, W, PZ, DOT>::THREADS)) void linear_scan_kernel(
+template <Dt IN, int KD, int W, int PZ, bool DOT, bool BACK, int SW>
+__global__ __launch_bounds__((ScanCfg<IN, KD, W, PZ, DOT, SW>::THREADS)) void linear_scan_kernel(
     LinearBatch b, LinearPass p) {
-  using Cfg = ScanCfg<IN, KD, W, PZ, DOT>;
+  using Cfg = ScanCfg<IN, KD, W, PZ, DOT, SW>;
+  constexpr int CW = Cfg::CW;
   constexpr int C = Cfg::C, NT = Cfg::NT, NB = Cfg::NB, KB = Cfg::KB, ES = Cfg::ES, PL = Cfg::PL;
   __shared__ __align__(1024) unsigned char lds[Cfg::BYTES];
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
@@ -357,9 +426,9 @@ __global__ __launch_bounds__((ScanCfg<IN, KD, W, PZ, DOT>::THREADS)) void linear
   };
   auto next = [](int i) { return i == 2 ? 0 : i + 1; };
 
-  if (wave >= W + kScoreWaves) {  // ---- copy waves
+  if (wave >= W + SW) {  // ---- copy waves
     if (chunks == 0) return;
-    const int cw = wave - W - kScoreWaves;
+    const int cw = wave - W - SW;
     auto rows = [&](const LinearRows& r, int width, int skip) {
       return static_cast<const char*>(r.p) + (static_cast<size_t>(h / r.group) * width + skip) * ES;
     };
@@ -371,11 +440,11 @@ __global__ __launch_bounds__((ScanCfg<IN, KD, W, PZ, DOT>::THREADS)) void linear
     // they stay below 2^32 (strides are at most 2^24 elements).  In a chunk
     // shorter than C the rows past its end repeat its last token: nothing
     // outside the sequence is read, and their factors are zero.
-    constexpr int NX = C * Cfg::CHK / 64 / kCopyWaves, NW = C * Cfg::CHV / 64 / kCopyWaves;
+    constexpr int NX = C * Cfg::CHK / 64 / CW, NW = C * Cfg::CHV / 64 / CW;
     uint32_t xo[NX], yo[NX], wo[NW];
     auto piece = [&](int i, auto ch, int len, size_t stride) {
       constexpr int CH = decltype(ch)::value;
-      const int q = 64 * (cw + kCopyWaves * i) + lane, r = q / CH, pc = q % CH;
+      const int q = 64 * (cw + CW * i) + lane, r = q / CH, pc = q % CH;
       return static_cast<uint32_t>((r < len ? r : len - 1) * stride + 16 * (pc ^ perm<CH>(r)));
     };
     const std::integral_constant<int, Cfg::CHK> chk;
@@ -396,14 +465,14 @@ __global__ __launch_bounds__((ScanCfg<IN, KD, W, PZ, DOT>::THREADS)) void linear
       if (len == C) {
 #pragma unroll
         for (int i = 0; i < NX; ++i) {
-          copy16(xb + xo[i], to + 1024 * kCopyWaves * i);
-          copy16(yb + yo[i], to + Cfg::X_BYTES + 1024 * kCopyWaves * i);
+          copy16(xb + xo[i], to + 1024 * CW * i);
+          copy16(yb + yo[i], to + Cfg::X_BYTES + 1024 * CW * i);
         }
       } else {
 #pragma unroll
         for (int i = 0; i < NX; ++i) {
-          copy16(xb + piece(i, chk, len, xst), to + 1024 * kCopyWaves * i);
-          copy16(yb + piece(i, chk, len, yst), to + Cfg::X_BYTES + 1024 * kCopyWaves * i);
+          copy16(xb + piece(i, chk, len, xst), to + 1024 * CW * i);
+          copy16(yb + piece(i, chk, len, yst), to + Cfg::X_BYTES + 1024 * CW * i);
         }
       }
     };
@@ -414,10 +483,10 @@ __global__ __launch_bounds__((ScanCfg<IN, KD, W, PZ, DOT>::THREADS)) void linear
       unsigned char* to = lds + Cfg::OFF_W + (s & 1) * Cfg::W_BYTES + 1024 * cw;
       if (len == C) {
 #pragma unroll
-        for (int i = 0; i < NW; ++i) copy16(wb + wo[i], to + 1024 * kCopyWaves * i);
+        for (int i = 0; i < NW; ++i) copy16(wb + wo[i], to + 1024 * CW * i);
       } else {
 #pragma unroll
-        for (int i = 0; i < NW; ++i) copy16(wb + piece(i, chv, len, wst), to + 1024 * kCopyWaves * i);
+        for (int i = 0; i < NW; ++i) copy16(wb + piece(i, chv, len, wst), to + 1024 * CW * i);
       }
     };
     auto load_gate = [&](int s) {
@@ -481,20 +550,33 @@ __global__ __launch_bounds__((ScanCfg<IN, KD, W, PZ, DOT>::THREADS)) void linear
   if (wave >= W) {  // ---- score waves
     if (chunks == 0) return;
     const int sw = wave - W;
-    // Tiles (row tile, column tile) of this wave.  Of the ten on the walked side
-    // of the diagonal each wave has two of one row tile and a third one; the
-    // last wave forms tiles that another forms as well (the same values).
-    constexpr int PER = NB == 2 ? 3 : 1;
+    // Tiles (row tile, column tile) of this wave, of the ten (fp32: three) on the
+    // walked side of the diagonal; tiles 2 i and 2 i + 1 have one row tile.  Some
+    // are formed by two waves (the same values).
+    constexpr int PER = NB == 2 ? (SW == 4 ? 3 : 5) : (SW == 4 ? 1 : 2);
     int tts[PER], sts[PER];
-    if constexpr (NB == 2) {
+    if constexpr (NB == 2 && SW == 4) {
       tts[0] = tts[1] = 3 - sw;
       sts[0] = 0;
       sts[1] = sw < 3 ? 1 : 0;
       tts[2] = sw == 1 ? 2 : 3;
       sts[2] = sw < 2 ? 2 : 3;
-    } else {
+    } else if constexpr (NB == 2) {
+      tts[0] = tts[1] = sw == 0 ? 3 : 2;
+      sts[0] = sw == 0 ? 0 : 1;
+      sts[1] = sw == 0 ? 1 : 2;
+      tts[2] = tts[3] = sw == 0 ? 3 : 1;
+      sts[2] = sw == 0 ? 2 : 0;
+      sts[3] = sw == 0 ? 3 : 1;
+      tts[4] = sw == 0 ? 2 : 0;
+      sts[4] = 0;
+    } else if constexpr (SW == 4) {
       tts[0] = sw == 0 ? 0 : 1;
       sts[0] = sw < 2 ? 0 : 1;
+    } else {
+      tts[0] = tts[1] = sw == 0 ? 1 : 0;
+      sts[0] = 0;
+      sts[1] = sw == 0 ? 1 : 0;
     }
     if (BACK)
       for (int i = 0; i < PER; ++i) {
@@ -517,10 +599,10 @@ __global__ __launch_bounds__((ScanCfg<IN, KD, W, PZ, DOT>::THREADS)) void linear
       for (int i = 0; i < PER; ++i) acc[i] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
-        Frag<IN> xf = row_frag<IN, Cfg::CHK>(X, 16 * tts[0], kb, c, g, kl[kb]);
+        Frag<IN> xf;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-          if (i == 2) xf = row_frag<IN, Cfg::CHK>(X, 16 * tts[i], kb, c, g, kl[kb]);
+          if (i % 2 == 0) xf = row_frag<IN, Cfg::CHK>(X, 16 * tts[i], kb, c, g, kl[kb]);
           acc[i] = mma(row_frag<IN, Cfg::CHK>(Y, 16 * sts[i], kb, c, g, kl[kb]), xf, acc[i]);
         }
       }
@@ -768,9 +850,8 @@ __global__ __launch_bounds__((ScanCfg<IN, KD, W, PZ, DOT>::THREADS)) void linear
 // ---- states at the starts of segments
 //
 // A segment's own state, from zero: the update of the scan alone.  It is a
-// stream of y and w rows, so the copy waves keep three chunks in flight ahead
-// of the one in use (four buffers, one barrier a chunk); one wave forms the gate
-// factors.
+// stream of y and w rows, so the copy waves run three chunks ahead (four buffers,
+// one barrier a chunk); one wave forms the gate factors.
 template <Dt IN, int KD, int W>
 struct LocalCfg {
   static constexpr int ES = IN == Dt::BF16 ? 2 : 4;
@@ -798,11 +879,13 @@ __device__ __forceinline__ void wait_vmem() {
 }
 
 template <Dt IN, int KD, int W, bool BACK>
-__global__ __launch_bounds__((LocalCfg<IN, KD, W>::THREADS)) void linear_local_kernel(
-    LinearBatch b, LinearRows y, LinearRows w, float us, int od_all, float* states, float* decays) {
+__device__ __forceinline__ void local_states(const LinearBatch& b, const LinearStates& job,
+                                             int od_all, unsigned char* lds) {
   using Cfg = LocalCfg<IN, KD, W>;
   constexpr int C = Cfg::C, NB = Cfg::NB, ES = Cfg::ES, NY = Cfg::NY, NW = Cfg::NW;
-  __shared__ __align__(1024) unsigned char lds[Cfg::BYTES];
+  const LinearRows &y = job.y, &w = job.w;
+  const float us = job.us;
+  float *states = job.states, *decays = job.decays;
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int slices = od_all / Cfg::VS, xcd = blockIdx.x % kXcds, k0 = blockIdx.x / kXcds;
@@ -949,21 +1032,31 @@ __global__ __launch_bounds__((LocalCfg<IN, KD, W>::THREADS)) void linear_local_k
   if (od == 0 && lane == 0) decays[pair] = decay;
 }
 
+// One job forwards (blockIdx.y = 0), one backwards (1).
+template <Dt IN, int KD, int W>
+__global__ __launch_bounds__((LocalCfg<IN, KD, W>::THREADS)) void linear_local_kernel(
+    LinearBatch b, LinearStates forward, LinearStates backward, int od_all) {
+  __shared__ __align__(1024) unsigned char lds[LocalCfg<IN, KD, W>::BYTES];
+  if (blockIdx.y == 0) local_states<IN, KD, W, false>(b, forward, od_all, lds);
+  else local_states<IN, KD, W, true>(b, backward, od_all, lds);
+}
+
 // The chain over a sequence's segments, elementwise: states[u] becomes the state
 // in front of segment u's walk.  One thread has four elements; kAhead segments
 // are read before the first is needed.
 constexpr int kAhead = 8;
-template <bool BACK>
-__global__ __launch_bounds__(256) void linear_starts_kernel(LinearBatch b, int per, const float* from,
-                                                            float* states, const float* decays,
-                                                            float* last) {
+__global__ __launch_bounds__(256) void linear_starts_kernel(LinearBatch b, int per,
+                                                            LinearStates forward,
+                                                            LinearStates backward) {
+  const bool BACK = blockIdx.y == 1;
+  const LinearStates& job = BACK ? backward : forward;
+  const float *from = job.from, *decays = job.decays;
+  float *states = job.states, *last = job.last;
   const int blocks = per / 1024, nh = blockIdx.x / blocks;
   const int n = nh / b.H, h = nh % b.H;
   const size_t at = (blockIdx.x % blocks) * 1024 + 4 * threadIdx.x;
-  int u0 = b.seg_offs[n], u1 = b.seg_offs[n + 1];
-  u0 = u0 < 0 ? 0 : (u0 > b.units ? b.units : u0);
-  u1 = u1 < u0 ? u0 : (u1 > b.units ? b.units : u1);
-  const int count = u1 - u0;
+  const SequenceUnits units = sequence_units(b, n);
+  const int count = units.count;
   floatx4 z = {0.f, 0.f, 0.f, 0.f};
   if (from) z = *reinterpret_cast<const floatx4*>(from + static_cast<size_t>(nh) * per + at);
   if (count == 0) {
@@ -976,7 +1069,7 @@ __global__ __launch_bounds__(256) void linear_starts_kernel(LinearBatch b, int p
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       if (i0 + i >= count - 1) continue;  // the last walk's own state is not needed
-      const int u = BACK ? u1 - 1 - (i0 + i) : u0 + i0 + i;
+      const int u = units.at(BACK ? count - 1 - (i0 + i) : i0 + i);
       const size_t pair = static_cast<size_t>(u) * b.H + h;
       own[i] = *reinterpret_cast<const floatx4*>(states + pair * per + at);
       d[i] = decays[pair];
@@ -984,7 +1077,7 @@ __global__ __launch_bounds__(256) void linear_starts_kernel(LinearBatch b, int p
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       if (i0 + i >= count) continue;
-      const int u = BACK ? u1 - 1 - (i0 + i) : u0 + i0 + i;
+      const int u = units.at(BACK ? count - 1 - (i0 + i) : i0 + i);
       *reinterpret_cast<floatx4*>(states + (static_cast<size_t>(u) * b.H + h) * per + at) = z;
       if (i0 + i < count - 1) z = d[i] * z + own[i];
     }
@@ -1209,10 +1302,10 @@ hipError_t launch_linear_pass(const LinearBatch& b, const LinearPass& p, hipStre
     auto go = [&](auto w, auto dot, auto back) {
       constexpr int W = decltype(w)::value;
       constexpr bool DOT = decltype(dot)::value, BACK = decltype(back)::value;
-      constexpr int PZ = DOT ? 3 : 2;
-      hipLaunchKernelGGL((linear_scan_kernel<IN, KD, W, PZ, DOT, BACK>),
-                         dim3(scan_grid(b, p.od / (16 * W))), dim3(ScanCfg<IN, KD, W, PZ, DOT>::THREADS), 0,
-                         stream, b, p);
+      constexpr int PZ = DOT ? 3 : 2, SW = IN == Dt::BF16 && W == 8 ? 2 : 4;
+      hipLaunchKernelGGL((linear_scan_kernel<IN, KD, W, PZ, DOT, BACK, SW>),
+                         dim3(scan_grid(b, p.od / (16 * W))),
+                         dim3(ScanCfg<IN, KD, W, PZ, DOT, SW>::THREADS), 0, stream, b, p);
       return hipGetLastError();
     };
     const std::integral_constant<int, 4> w4;
@@ -1228,35 +1321,25 @@ hipError_t launch_linear_pass(const LinearBatch& b, const LinearPass& p, hipStre
   });
 }
 
-hipError_t launch_linear_starts(const LinearBatch& b, const LinearRows& y, const LinearRows& w,
-                                float us, int od, int kd, int backward, const float* from,
-                                float* states, float* decays, float* last, hipStream_t stream) {
-  hipError_t e = by_type(b.in_dtype, kd, [&](auto in, auto kdim) {
+hipError_t launch_linear_starts(const LinearBatch& b, int od, int kd, const LinearStates& forward,
+                                const LinearStates* backward, hipStream_t stream) {
+  const int ways = backward ? 2 : 1;
+  const LinearStates& back = backward ? *backward : forward;
+  const hipError_t e = by_type(b.in_dtype, kd, [&](auto in, auto kdim) {
     constexpr Dt IN = decltype(in)::value;
     constexpr int KD = decltype(kdim)::value;
-    auto go = [&](auto w_, auto back) {
+    auto go = [&](auto w_) {
       constexpr int W = decltype(w_)::value;
-      hipLaunchKernelGGL((linear_local_kernel<IN, KD, W, decltype(back)::value>),
-                         dim3(scan_grid(b, od / (16 * W))), dim3(LocalCfg<IN, KD, W>::THREADS), 0,
-                         stream, b, y, w, us, od, states, decays);
+      hipLaunchKernelGGL((linear_local_kernel<IN, KD, W>), dim3(scan_grid(b, od / (16 * W)), ways),
+                         dim3(LocalCfg<IN, KD, W>::THREADS), 0, stream, b, forward, back, od);
       return hipGetLastError();
     };
-    const std::integral_constant<int, 4> w4;
-    const std::integral_constant<int, 8> w8;
-    const std::true_type yes;
-    const std::false_type no;
-    if (od == 128) return backward ? go(w8, yes) : go(w8, no);
-    return backward ? go(w4, yes) : go(w4, no);
+    return od == 128 ? go(std::integral_constant<int, 8>()) : go(std::integral_constant<int, 4>());
   });
   if (e != hipSuccess) return e;
   const int per = od * kd;
-  const dim3 grid(static_cast<unsigned>(b.N) * b.H * (per / 1024));
-  if (backward)
-    hipLaunchKernelGGL(linear_starts_kernel<true>, grid, dim3(256), 0, stream, b, per, from, states,
-                       decays, last);
-  else
-    hipLaunchKernelGGL(linear_starts_kernel<false>, grid, dim3(256), 0, stream, b, per, from, states,
-                       decays, last);
+  hipLaunchKernelGGL(linear_starts_kernel, dim3(static_cast<unsigned>(b.N) * b.H * (per / 1024), ways),
+                     dim3(256), 0, stream, b, per, forward, back);
   return hipGetLastError();
 }
 

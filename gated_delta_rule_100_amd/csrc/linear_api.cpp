@@ -102,8 +102,10 @@ SegmentSizes segment_sizes(int T_total, int N, int H, int dk, int dv, int kinds)
   if (!z.seg) return z;
   z.kinds = kinds;
   const size_t pairs = static_cast<size_t>(z.units) * H;
-  z.offs = align_up(sizeof(int32_t) * (static_cast<size_t>(N) + 1));
-  z.idx = align_up(sizeof(int32_t) * 2 * static_cast<size_t>(z.units));
+  if (N > gdr::kInlineSeqs) {
+    z.offs = align_up(sizeof(int32_t) * (static_cast<size_t>(N) + 1));
+    z.idx = align_up(sizeof(int32_t) * 2 * static_cast<size_t>(z.units));
+  }
   z.states = align_up(sizeof(float) * pairs * dk * dv);
   z.decays = align_up(sizeof(float) * pairs);
   return z;
@@ -147,7 +149,7 @@ struct Carver {
 hipError_t make_segments(LinearBatch* b, const SegmentSizes& z, Carver* ws, hipStream_t st) {
   b->seg = z.seg;
   b->units = z.units;
-  if (!z.seg) return hipSuccess;
+  if (!z.seg || !z.offs) return hipSuccess;
   int32_t* offs = ws->take<int32_t>(z.offs);
   int32_t* idx = ws->take<int32_t>(z.idx);
   b->seg_offs = offs;
@@ -225,8 +227,8 @@ gdr_status gdr_linear_prefill(const void* q, const void* k, const void* v, const
   if (z.seg) {
     float* states = ws.take<float>(z.states);
     float* decays = ws.take<float>(z.decays);
-    e = gdr::launch_linear_starts(b, p.y, p.w, p.us, dv, dk, 0, state_in, states, decays, state_out,
-                                  st);
+    e = gdr::launch_linear_starts(b, dv, dk, {p.y, p.w, 1.f, state_in, states, decays, state_out},
+                                  nullptr, st);
     if (e != hipSuccess) return hip_fail(e, who, "segment states");
     p.start = states;
   }
@@ -290,10 +292,9 @@ gdr_status gdr_linear_backward(const void* q, const void* k, const void* v, cons
   // states in front of every unit's walk: S forwards, R backwards
   const float *from = state_in, *behind = dstate_out;
   if (z.seg.seg) {
-    e = gdr::launch_linear_starts(b, rk, rv, 1.f, dv, dk, 0, state_in, starts, decays, nullptr, st);
-    if (e == hipSuccess)
-      e = gdr::launch_linear_starts(b, rq, rd, scale, dv, dk, 1, dstate_out, ends, decays_back,
-                                    dstate_in, st);
+    const gdr::LinearStates back{rq, rd, scale, dstate_out, ends, decays_back, dstate_in};
+    e = gdr::launch_linear_starts(b, dv, dk, {rk, rv, 1.f, state_in, starts, decays, nullptr}, &back,
+                                  st);
     if (e != hipSuccess) return hip_fail(e, who, "segment states");
     from = starts;
     behind = ends;

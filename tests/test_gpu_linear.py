@@ -66,6 +66,15 @@ def test_prefill_in_segments(lens, dtype, dk, dv, decay, gate, state):
     assert torch.equal(o, prefill(d, state_out=False)[0])
 
 
+def test_many_sequences_in_segments():
+    """More sequences than the kernels form a segment table for by themselves."""
+    lens = [1, 0, 700] + [3, 70] * 35 + [650]
+    say(f"prefill and backward of {len(lens)} sequences, some in segments")
+    d = ref.make(lens, 2, 2, 64, 64, "bf16", "token", "slow", True, seed=20)
+    check_prefill(d, *prefill(d))
+    check_backward(d, backward(d))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("gate", ["unit", "std", "steep", "reset"])
 def test_prefill_gates(dtype, gate):
