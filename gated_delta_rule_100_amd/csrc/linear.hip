@@ -46,26 +46,31 @@ struct SequenceUnits {
 
 // The segment table of at most kInlineSeqs sequences, formed by every wave for
 // itself with one sequence a lane (a launch and a dependent read less than a
-// table in memory).  All whole segments come before all shorter ones, so that the
-// long walks start first: 8 sequences of 32768 tokens, 32 heads, scan 345 us in
-// the order of the sequences.
-struct SegmentPrefix {
-  int whole, tails;  // inclusive prefix sums, lane n for sequence n
+// table in memory).  All whole segments come first, then the sequences' shorter
+// last ones by falling length: the hardware starts workgroups in order, so the
+// long walks start first (8 sequences of 32768 tokens, 32 heads: scan 348 us with
+// the last ones in the order of the sequences, 315 us this way).
+struct SegmentTable {
+  int whole;      // inclusive prefix sum of whole segments, lane n for sequence n
+  int tail;       // tokens of the shorter last segment, 0 for none
+  int rank;       // its place among them
   int all_whole;
 };
-__device__ __forceinline__ SegmentPrefix segment_prefix(const LinearBatch& b, int lane) {
+__device__ __forceinline__ SegmentTable segment_table(const LinearBatch& b, int lane) {
   int tb = 0, te = 0;
   if (lane < b.N) token_range(b, lane, tb, te);
-  SegmentPrefix p;
+  SegmentTable p;
   p.whole = (te - tb) / b.seg;
-  p.tails = (te - tb) % b.seg != 0;
+  p.tail = (te - tb) % b.seg;
+  p.rank = 0;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int w = __shfl_up(p.whole, d), t = __shfl_up(p.tails, d);
-    if (lane >= d) {
-      p.whole += w;
-      p.tails += t;
-    }
+    const int w = __shfl_up(p.whole, d);
+    if (lane >= d) p.whole += w;
+  }
+  for (int m = 0; m < b.N; ++m) {
+    const int t = __builtin_amdgcn_readlane(p.tail, m);
+    p.rank += t > p.tail || (t == p.tail && m < lane);
   }
   p.all_whole = __builtin_amdgcn_readlane(p.whole, 63);
   return p;
@@ -79,11 +84,11 @@ __device__ __forceinline__ SequenceUnits sequence_units(const LinearBatch& b, in
     u1 = u1 < u0 ? u0 : (u1 > b.units ? b.units : u1);
     r = {u0, u1 - u0, 0, 0};
   } else {
-    const SegmentPrefix p = segment_prefix(b, threadIdx.x & 63);
-    const int w1 = __builtin_amdgcn_readlane(p.whole, n), t1 = __builtin_amdgcn_readlane(p.tails, n);
+    const SegmentTable p = segment_table(b, threadIdx.x & 63);
+    const int w1 = __builtin_amdgcn_readlane(p.whole, n);
     const int w0 = n > 0 ? __builtin_amdgcn_readlane(p.whole, n - 1) : 0;
-    const int t0 = n > 0 ? __builtin_amdgcn_readlane(p.tails, n - 1) : 0;
-    r = {w0, w1 - w0 + t1 - t0, t1 - t0, p.all_whole + t0};
+    const int tail = __builtin_amdgcn_readlane(p.tail, n) > 0;
+    r = {w0, w1 - w0 + tail, tail, p.all_whole + __builtin_amdgcn_readlane(p.rank, n)};
     // (offsets that go back or past the tokens could name more units than there are)
     if (r.from + r.count - r.tail > b.units || (r.tail && r.tail_at >= b.units)) r.count = r.tail = 0;
   }
@@ -105,12 +110,12 @@ __device__ __forceinline__ bool unit_at(const LinearBatch& b, int u, Unit& r) {
     if (r.n < 0 || r.n >= b.N || j < 0) return false;
   } else {
     const int lane = threadIdx.x & 63;
-    const SegmentPrefix p = segment_prefix(b, lane);
+    const SegmentTable p = segment_table(b, lane);
     const bool whole = u < p.all_whole;
-    const int sum = whole ? p.whole : p.all_whole + p.tails;
-    const uint64_t later = __ballot(lane < b.N && u < sum);
-    if (later == 0) return false;
-    r.n = __builtin_ctzll(later);
+    const uint64_t found = __ballot(lane < b.N && (whole ? u < p.whole
+                                                         : p.tail > 0 && p.rank == u - p.all_whole));
+    if (found == 0) return false;
+    r.n = __builtin_ctzll(found);
     const int before = r.n > 0 ? __builtin_amdgcn_readlane(p.whole, r.n - 1) : 0;
     j = whole ? u - before : __builtin_amdgcn_readlane(p.whole, r.n) - before;
   }
