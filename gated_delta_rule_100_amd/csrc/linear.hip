@@ -356,7 +356,7 @@ struct ScanCfg {
   static constexpr int KB = KD / 32;          // 32-deep blocks over kd
   static constexpr int VS = 16 * W;           // columns of w a workgroup
   static constexpr int CHK = KD * ES / 16, CHV = VS * ES / 16;
-  static constexpr int CW = SW;  // as many copy waves as score waves
+  static constexpr int CW = SW == 3 ? 1 : 4;  // copy waves
   static constexpr int THREADS = 64 * (W + SW + CW);
   // three buffers of x and y rows, two of w rows
   static constexpr int X_BYTES = C * KD * ES, W_BYTES = C * VS * ES;
@@ -461,26 +461,21 @@ __global__ __launch_bounds__((ScanCfg<IN, KD, W, PZ, DOT, SW>::THREADS)) void li
     }
 #pragma unroll
     for (int i = 0; i < NW; ++i) wo[i] = piece(i, chv, C, wst);
-    auto copy_xy = [&](int s, int buf) {
+    auto copy_rows = [&](int s, const char* src, size_t stride, const uint32_t (&full)[NX],
+                         unsigned char* to) {
       int tok;
       const int len = chunk_at(s, tok);
-      const char* xb = xs + static_cast<size_t>(tok) * xst;
-      const char* yb = ys + static_cast<size_t>(tok) * yst;
-      unsigned char* to = x_tile(buf) + 1024 * cw;
+      const char* base = src + static_cast<size_t>(tok) * stride;
       if (len == C) {
 #pragma unroll
-        for (int i = 0; i < NX; ++i) {
-          copy16(xb + xo[i], to + 1024 * CW * i);
-          copy16(yb + yo[i], to + Cfg::X_BYTES + 1024 * CW * i);
-        }
+        for (int i = 0; i < NX; ++i) copy16(base + full[i], to + 1024 * (cw + CW * i));
       } else {
 #pragma unroll
-        for (int i = 0; i < NX; ++i) {
-          copy16(xb + piece(i, chk, len, xst), to + 1024 * CW * i);
-          copy16(yb + piece(i, chk, len, yst), to + Cfg::X_BYTES + 1024 * CW * i);
-        }
+        for (int i = 0; i < NX; ++i) copy16(base + piece(i, chk, len, stride), to + 1024 * (cw + CW * i));
       }
     };
+    auto copy_x = [&](int s, int buf) { copy_rows(s, xs, xst, xo, x_tile(buf)); };
+    auto copy_y = [&](int s, int buf) { copy_rows(s, ys, yst, yo, x_tile(buf) + Cfg::X_BYTES); };
     auto copy_w = [&](int s) {
       int tok;
       const int len = chunk_at(s, tok);
@@ -516,16 +511,20 @@ __global__ __launch_bounds__((ScanCfg<IN, KD, W, PZ, DOT, SW>::THREADS)) void li
       }
     };
     const float g0 = load_gate(0), g1 = chunks > 1 ? load_gate(1) : 0.f;
-    copy_xy(0, 0);
+    copy_x(0, 0);
+    copy_y(0, 0);
     copy_w(0);
-    if (chunks > 1) copy_xy(1, 1);
+    if (chunks > 1) {
+      copy_x(1, 1);
+      copy_y(1, 1);
+    }
     put_gates(0, 0, g0);
     if (chunks > 1) put_gates(1, 1, g1);
     __builtin_amdgcn_s_waitcnt(0);
     bare_barrier();
     // the dot products of chunk s, one token a lane
     auto store_dots = [&](int s) {
-      if (!DOT || cw != 1) return;
+      if (!DOT || cw != CW - 1) return;
       int tok;
       const int len = chunk_at(s, tok);
       const float* part = reinterpret_cast<const float*>(lds + Cfg::OFF_DOT) + (s & 1) * W * C;
@@ -542,9 +541,12 @@ __global__ __launch_bounds__((ScanCfg<IN, KD, W, PZ, DOT, SW>::THREADS)) void li
       if (s > 0) store_dots(s - 1);
       if (s + 2 < chunks) gate = load_gate(s + 2);
       if (s + 1 < chunks) copy_w(s + 1);
-      if (s + 2 < chunks) copy_xy(s + 2, buf);
+      if (s + 2 < chunks) copy_x(s + 2, buf);
       bare_barrier();
-      if (s + 2 < chunks) put_gates(s + 2, buf, gate);
+      if (s + 2 < chunks) {
+        copy_y(s + 2, buf);
+        put_gates(s + 2, buf, gate);
+      }
       __builtin_amdgcn_s_waitcnt(0);
       bare_barrier();
     }
@@ -557,31 +559,25 @@ __global__ __launch_bounds__((ScanCfg<IN, KD, W, PZ, DOT, SW>::THREADS)) void li
     const int sw = wave - W;
     // Tiles (row tile, column tile) of this wave, of the ten (fp32: three) on the
     // walked side of the diagonal; tiles 2 i and 2 i + 1 have one row tile.  Some
-    // are formed by two waves (the same values).
-    constexpr int PER = NB == 2 ? (SW == 4 ? 3 : 5) : (SW == 4 ? 1 : 2);
+    // are formed twice (the same values).
+    constexpr int PER = NB == 1 ? 1 : SW == 4 ? 3 : 4;
     int tts[PER], sts[PER];
-    if constexpr (NB == 2 && SW == 4) {
+    if constexpr (NB == 1) {
+      tts[0] = sw == 0 ? 0 : 1;
+      sts[0] = sw < 2 ? 0 : 1;
+    } else if constexpr (SW == 4) {
       tts[0] = tts[1] = 3 - sw;
       sts[0] = 0;
       sts[1] = sw < 3 ? 1 : 0;
       tts[2] = sw == 1 ? 2 : 3;
       sts[2] = sw < 2 ? 2 : 3;
-    } else if constexpr (NB == 2) {
-      tts[0] = tts[1] = sw == 0 ? 3 : 2;
-      sts[0] = sw == 0 ? 0 : 1;
-      sts[1] = sw == 0 ? 1 : 2;
-      tts[2] = tts[3] = sw == 0 ? 3 : 1;
-      sts[2] = sw == 0 ? 2 : 0;
-      sts[3] = sw == 0 ? 3 : 1;
-      tts[4] = sw == 0 ? 2 : 0;
-      sts[4] = 0;
-    } else if constexpr (SW == 4) {
-      tts[0] = sw == 0 ? 0 : 1;
-      sts[0] = sw < 2 ? 0 : 1;
-    } else {
-      tts[0] = tts[1] = sw == 0 ? 1 : 0;
+    } else {  // a row tile each, the last wave the two shortest
+      tts[0] = tts[1] = 3 - sw;
+      tts[2] = tts[3] = sw == 2 ? 0 : 3 - sw;
       sts[0] = 0;
-      sts[1] = sw == 0 ? 1 : 0;
+      sts[1] = 1;
+      sts[2] = sw == 2 ? 0 : 2;
+      sts[3] = sw == 2 ? 0 : 3 - sw;
     }
     if (BACK)
       for (int i = 0; i < PER; ++i) {
@@ -1307,7 +1303,7 @@ hipError_t launch_linear_pass(const LinearBatch& b, const LinearPass& p, hipStre
     auto go = [&](auto w, auto dot, auto back) {
       constexpr int W = decltype(w)::value;
       constexpr bool DOT = decltype(dot)::value, BACK = decltype(back)::value;
-      constexpr int PZ = DOT ? 3 : 2, SW = IN == Dt::BF16 && W == 8 ? 2 : 4;
+      constexpr int PZ = DOT ? 3 : 2, SW = IN == Dt::BF16 && W == 8 ? 3 : 4;
       hipLaunchKernelGGL((linear_scan_kernel<IN, KD, W, PZ, DOT, BACK, SW>),
                          dim3(scan_grid(b, p.od / (16 * W))),
                          dim3(ScanCfg<IN, KD, W, PZ, DOT, SW>::THREADS), 0, stream, b, p);
