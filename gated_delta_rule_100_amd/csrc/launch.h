@@ -201,6 +201,10 @@ hipError_t launch_linear_decode(const void* q, const void* k, const void* v,
 
 hipError_t launch_linear_pass(const LinearBatch& b, const LinearPass& p, hipStream_t stream);
 
+// The passes of a gradient: dq forwards, dv and dk backwards.
+hipError_t launch_linear_grads(const LinearBatch& b, const LinearPass& pq, const LinearPass& pv,
+                               const LinearPass& pk, hipStream_t stream);
+
 // States at the start of every segment's walk, [units * H] of od rows and kd
 // columns: the segments' own states from zero (y, w, us as in a pass) and their
 // decays [units * H], then the chain over each sequence's segments from `from`

@@ -401,13 +401,13 @@ __device__ __forceinline__ void store_state4(float* p, int64_t col, const floatx
   }
 }
 
-template <Dt IN, int KD, int W, int PZ, bool DOT, bool BACK, int SW>
-__global__ __launch_bounds__((ScanCfg<IN, KD, W, PZ, DOT, SW>::THREADS)) void linear_scan_kernel(
-    LinearBatch b, LinearPass p) {
+template <Dt IN, int KD, int W, bool DOT, bool BACK, int SW>
+__device__ __forceinline__ void scan_pass(const LinearBatch& b, const LinearPass& p,
+                                          unsigned char* lds) {
+  constexpr int PZ = DOT ? 3 : 2;
   using Cfg = ScanCfg<IN, KD, W, PZ, DOT, SW>;
   constexpr int CW = Cfg::CW;
   constexpr int C = Cfg::C, NT = Cfg::NT, NB = Cfg::NB, KB = Cfg::KB, ES = Cfg::ES, PL = Cfg::PL;
-  __shared__ __align__(1024) unsigned char lds[Cfg::BYTES];
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // the workgroups of one (unit, head) read the same x and y rows: one XCD
@@ -846,6 +846,31 @@ __global__ __launch_bounds__((ScanCfg<IN, KD, W, PZ, DOT, SW>::THREADS)) void li
     for (int d = 1; d < 64; d <<= 1) ed += __shfl_xor(ed, d);
     if (lane == 0) p.end_dot[static_cast<size_t>(od / 16) * b.units * b.H + pair] = ed;
   }
+}
+
+// Score waves of a workgroup: with eight compute waves and bf16 inputs three and
+// one copy wave (168 registers a wave), else four and four copy waves.
+template <Dt IN, int W>
+constexpr int score_waves() { return IN == Dt::BF16 && W == 8 ? 3 : 4; }
+
+template <Dt IN, int KD, int W, bool DOT, bool BACK>
+__global__ __launch_bounds__((ScanCfg<IN, KD, W, DOT ? 3 : 2, DOT, score_waves<IN, W>()>::THREADS))
+void linear_scan_kernel(LinearBatch b, LinearPass p) {
+  constexpr int SW = score_waves<IN, W>();
+  __shared__ __align__(1024) unsigned char lds[ScanCfg<IN, KD, W, DOT ? 3 : 2, DOT, SW>::BYTES];
+  scan_pass<IN, KD, W, DOT, BACK, SW>(b, p, lds);
+}
+
+// The three passes of a gradient (dq, dv, dk) in one launch, where dk = dv: their
+// workgroups follow each other without the gaps of launches.
+template <Dt IN, int KD, int W>
+__global__ __launch_bounds__((ScanCfg<IN, KD, W, 3, true, score_waves<IN, W>()>::THREADS))
+void linear_grad_kernel(LinearBatch b, LinearPass pq, LinearPass pv, LinearPass pk) {
+  constexpr int SW = score_waves<IN, W>();
+  __shared__ __align__(1024) unsigned char lds[ScanCfg<IN, KD, W, 3, true, SW>::BYTES];
+  if (blockIdx.y == 0) scan_pass<IN, KD, W, true, false, SW>(b, pq, lds);
+  else if (blockIdx.y == 1) scan_pass<IN, KD, W, true, true, SW>(b, pv, lds);
+  else scan_pass<IN, KD, W, false, true, SW>(b, pk, lds);
 }
 
 // ---- states at the starts of segments
@@ -1303,10 +1328,9 @@ hipError_t launch_linear_pass(const LinearBatch& b, const LinearPass& p, hipStre
     auto go = [&](auto w, auto dot, auto back) {
       constexpr int W = decltype(w)::value;
       constexpr bool DOT = decltype(dot)::value, BACK = decltype(back)::value;
-      constexpr int PZ = DOT ? 3 : 2, SW = IN == Dt::BF16 && W == 8 ? 3 : 4;
-      hipLaunchKernelGGL((linear_scan_kernel<IN, KD, W, PZ, DOT, BACK, SW>),
-                         dim3(scan_grid(b, p.od / (16 * W))),
-                         dim3(ScanCfg<IN, KD, W, PZ, DOT, SW>::THREADS), 0, stream, b, p);
+      constexpr int THREADS = ScanCfg<IN, KD, W, DOT ? 3 : 2, DOT, score_waves<IN, W>()>::THREADS;
+      hipLaunchKernelGGL((linear_scan_kernel<IN, KD, W, DOT, BACK>),
+                         dim3(scan_grid(b, p.od / (16 * W))), dim3(THREADS), 0, stream, b, p);
       return hipGetLastError();
     };
     const std::integral_constant<int, 4> w4;
@@ -1319,6 +1343,24 @@ hipError_t launch_linear_pass(const LinearBatch& b, const LinearPass& p, hipStre
     }
     if (p.dot) return p.backward ? go(w4, yes, yes) : go(w4, yes, no);
     return p.backward ? go(w4, no, yes) : go(w4, no, no);
+  });
+}
+
+hipError_t launch_linear_grads(const LinearBatch& b, const LinearPass& pq, const LinearPass& pv,
+                               const LinearPass& pk, hipStream_t stream) {
+  if (pq.kd != pv.kd || !pq.dot || !pv.dot) {
+    hipError_t e = launch_linear_pass(b, pq, stream);
+    if (e == hipSuccess) e = launch_linear_pass(b, pv, stream);
+    if (e == hipSuccess) e = launch_linear_pass(b, pk, stream);
+    return e;
+  }
+  return by_type(b.in_dtype, pq.kd, [&](auto in, auto kd) {
+    constexpr Dt IN = decltype(in)::value;
+    constexpr int KD = decltype(kd)::value, W = KD / 16;
+    constexpr int THREADS = ScanCfg<IN, KD, W, 3, true, score_waves<IN, W>()>::THREADS;
+    hipLaunchKernelGGL((linear_grad_kernel<IN, KD, W>), dim3(scan_grid(b, 1), 3), dim3(THREADS), 0,
+                       stream, b, pq, pv, pk);
+    return hipGetLastError();
   });
 }
 

@@ -328,9 +328,7 @@ gdr_status gdr_linear_backward(const void* q, const void* k, const void* v, cons
   pk.start = behind;
   pk.row = 1; pk.col = dk; pk.od = dk; pk.kd = dv;
   pk.us = scale; pk.os = 1.f; pk.backward = 1;
-  e = gdr::launch_linear_pass(b, pq, st);
-  if (e == hipSuccess) e = gdr::launch_linear_pass(b, pv, st);
-  if (e == hipSuccess) e = gdr::launch_linear_pass(b, pk, st);
+  e = gdr::launch_linear_grads(b, pq, pv, pk, st);
   if (e != hipSuccess) return hip_fail(e, who, "scan");
   if (group > 1 && T_total > 0) {
     e = gdr::launch_linear_group_sum(b, part_q, group, dk, dq, grad_dtype, st);
