@@ -12,7 +12,7 @@
 // All exponents are <= 0 for g <= 0.
 #include <type_traits>
 
-#include "launch.h"
+#include "linear.h"
 #include "mfma_planes.h"
 
 namespace gdr {

@@ -9,6 +9,7 @@
 #include "../../include/gdr.h"
 #include "api_internal.h"
 #include "launch.h"
+#include "linear.h"
 
 namespace {
 
@@ -44,8 +45,8 @@ gdr_status check_common(const char* who, int tokens, int N, int H, int Hk, int d
     return fail(GDR_ERR_UNSUPPORTED, "%s: dtype codes must be GDR_BF16 or GDR_FP32", who);
   if (decay != GDR_DECAY_TOKEN && decay != GDR_DECAY_HEAD)
     return fail(GDR_ERR_INVALID_ARG, "%s: decay must be GDR_DECAY_TOKEN or GDR_DECAY_HEAD", who);
-  // grids count one workgroup for every 16 state rows
-  if (static_cast<int64_t>(tokens) * H > INT32_MAX || static_cast<int64_t>(N) * H > INT32_MAX / 8)
+  // a launch has fewer than 2^32 threads, 1024 at most for a (sequence, head)
+  if (static_cast<int64_t>(tokens) * H > INT32_MAX || static_cast<int64_t>(N) * H > 4000000)
     return fail(GDR_ERR_INVALID_ARG, "%s: tokens*H or N*H too large", who);
   const int64_t per16 = 16 / static_cast<int64_t>(elem_size(in_dtype));
   struct { int64_t* s; int64_t width; const char* name; } rows[] = {
@@ -56,7 +57,8 @@ gdr_status check_common(const char* who, int tokens, int N, int H, int Hk, int d
     if (*r.s == 0) *r.s = r.width;
     if (*r.s < r.width || *r.s % per16 != 0 || *r.s > (int64_t{1} << 24))
       return fail(GDR_ERR_INVALID_ARG,
-                  "%s: %s=%lld must be 0 or from %lld to 2^24 and a multiple of %lld", who, r.name, static_cast<long long>(*r.s), static_cast<long long>(r.width),
+                  "%s: %s=%lld must be 0 or from %lld to 2^24 and a multiple of %lld", who, r.name,
+                  static_cast<long long>(*r.s), static_cast<long long>(r.width),
                   static_cast<long long>(per16));
   }
   for (const void* p : ptrs)

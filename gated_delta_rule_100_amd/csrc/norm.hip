@@ -11,7 +11,7 @@
 #include <type_traits>
 
 #include "gdr_device.h"
-#include "launch.h"
+#include "norm.h"
 
 namespace gdr {
 namespace {

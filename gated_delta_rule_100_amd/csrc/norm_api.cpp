@@ -6,7 +6,7 @@
 
 #include "../../include/gdr.h"
 #include "api_internal.h"
-#include "launch.h"
+#include "norm.h"
 
 namespace {
 
@@ -17,8 +17,12 @@ using gdr::hip_status;
 using gdr::ok;
 
 constexpr int kMaxWidth = 16384;
+// A launch has fewer than 2^32 threads, at most max(8, D / 4) a row.
+constexpr int64_t kMaxRows = int64_t{1} << 28, kMaxElements = int64_t{1} << 33;
 
 bool valid_dtype(int d) { return d == GDR_BF16 || d == GDR_FP32; }
+
+bool valid_rows(int64_t rows, int D) { return rows >= 0 && rows <= kMaxRows && rows * D < kMaxElements; }
 
 size_t align_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
@@ -27,10 +31,10 @@ size_t partial_bytes(int64_t rows, int D) {
 }
 
 gdr_status check_common(const char* who, const BlockNorm& p) {
-  if (p.rows < 0 || p.rows > INT32_MAX) return fail(GDR_ERR_INVALID_ARG, "%s: rows=%lld", who,
-                                                    static_cast<long long>(p.rows));
   if (p.D < 1 || p.D > kMaxWidth)
     return fail(GDR_ERR_UNSUPPORTED, "%s: D=%d not in [1, %d]", who, p.D, kMaxWidth);
+  if (!valid_rows(p.rows, p.D))
+    return fail(GDR_ERR_INVALID_ARG, "%s: rows=%lld", who, static_cast<long long>(p.rows));
   if (!valid_dtype(p.in_dtype) || !valid_dtype(p.w_dtype) || !valid_dtype(p.out_dtype))
     return fail(GDR_ERR_UNSUPPORTED, "%s: dtype codes must be GDR_BF16 or GDR_FP32", who);
   if (p.gate && p.act != GDR_GATE_SILU && p.act != GDR_GATE_SIGMOID)
@@ -78,7 +82,7 @@ gdr_status gdr_block_norm(const void* x, const void* w_after, const void* gate,
 }
 
 size_t gdr_block_norm_backward_workspace_bytes(int64_t rows, int D) {
-  if (rows < 0 || rows > INT32_MAX || D < 1 || D > kMaxWidth) return 0;
+  if (D < 1 || D > kMaxWidth || !valid_rows(rows, D)) return 0;
   return 2 * partial_bytes(rows, D);
 }
 

@@ -307,6 +307,7 @@ gdr_status gdr_state_fixup(const float* L, const float* M, const float* state_in
  *     width and at most 2^24 elements.
  *   - cu_seqlens[N] may be below T_total: rows behind the last sequence are
  *     neither read nor written.
+ *   - N <= 65536, H <= 65535, N * H <= 4000000 and T_total * H < 2^31.
  *   - An infinity or NaN in a token's q, k or v may make the outputs of its
  *     own chunk of 64 tokens non-finite as well as those after it; other
  *     sequences are not affected.
@@ -414,7 +415,7 @@ size_t gdr_linear_backward_workspace_bytes(int T_total, int N, int H, int Hk, in
  *                                  may be the buffer of x, gate or residual when
  *                                  the dtypes agree (not both the same one)
  *   act                GDR_GATE_SILU: z sigmoid(z), GDR_GATE_SIGMOID: sigmoid(z)
- *   rows >= 0, 1 <= D <= 16384; rows * D may pass 2^31
+ *   1 <= D <= 16384, 0 <= rows <= 2^28, rows * D < 2^33
  * For D a multiple of 8 every row is read with 16-byte loads; other D take
  * single-element accesses.
  */

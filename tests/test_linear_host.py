@@ -104,7 +104,8 @@ SHARED = [
     (dict(H=5), 1, "multiple"), (dict(dk=96), 2, "(96, 64)"), (dict(dv=256), 2, "(128, 256)"),
     (dict(ind=2), 2, "dtype"), (dict(outd=-1), 2, "dtype"), (dict(decay=2), 1, "decay"),
     (dict(qs=255), 1, "q_stride"), (dict(qs=260), 1, "q_stride"), (dict(ks=-256), 1, "k_stride"),
-    (dict(vs=128), 1, "v_stride"), (dict(N=70000), 1, "large"), (dict(k=FAKE + 8), 1, "aligned"),
+    (dict(vs=128), 1, "v_stride"), (dict(ks=(1 << 24) + 8), 1, "2^24"),
+    (dict(N=1 << 15, H=128), 1, "large"), (dict(N=70000), 1, "large"), (dict(k=FAKE + 8), 1, "aligned"),
 ]
 
 

@@ -65,6 +65,7 @@ def _backward(lib, **over):
 @pytest.mark.parametrize("call", [_forward, _backward])
 @pytest.mark.parametrize("over, status, word", [
     (dict(x=None), 1, "NULL"), (dict(rows=-1), 1, "rows"), (dict(rows=1 << 31), 1, "rows"),
+    (dict(rows=(1 << 28) + 1, D=1), 1, "rows"), (dict(rows=1 << 20, D=8192), 1, "rows"),
     (dict(D=0), 2, "D=0"), (dict(D=16385), 2, "D=16385"), (dict(act=2), 1, "act"),
     (dict(eps=-1.0), 1, "eps"), (dict(eps=float("nan")), 1, "eps"), (dict(ind=2), 2, "dtype"),
     (dict(wd=3), 2, "dtype"), (dict(outd=-1), 2, "dtype"), (dict(r=FAKE + 4), 1, "aligned"),
