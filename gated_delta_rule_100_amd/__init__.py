@@ -172,10 +172,13 @@ _F32 = (torch.float32,)
 _I32 = (torch.int32,)
 
 
-def gdr_decode_step(q, k, v, g, beta, state, o, stream=None) -> None:
+def gdr_decode_step(q, k, v, g, beta, state, o, stream=None, *, norm=None) -> None:
     """One decode token, state updated in place.  q, k [N, H, dk], v [N, H, dv]
     (bf16 or fp32, one dtype); g, beta [N, H] fp32; state [N, H, dv, dk] fp32;
-    o [N, H, dv] bf16 or fp32."""
+    o [N, H, dv] bf16 or fp32.  norm: a dict of gdr_block_norm's arguments after
+    x (h, y, w_after, gate, ...): the norm and gate behind the heads, of every
+    row of o, on the same stream; what it would refuse is refused before
+    anything runs."""
     N, H, dk = q.shape
     dv = v.shape[2]
     if k.shape != q.shape or v.shape[:2] != (N, H) or g.shape != (N, H) or beta.shape != (N, H) \
@@ -183,19 +186,22 @@ def gdr_decode_step(q, k, v, g, beta, state, o, stream=None) -> None:
         raise GdrError("gdr_decode_step: inconsistent shapes")
     if k.dtype != q.dtype or v.dtype != q.dtype:
         raise GdrError("gdr_decode_step: q, k, v must share a dtype")
+    after = _norm_after(o, norm, stream)
     st = _load().gdr_decode_step(
         _dev_ptr(q, "q", _IO), _dev_ptr(k, "k", _IO), _dev_ptr(v, "v", _IO),
         _dev_ptr(g, "g", _F32), _dev_ptr(beta, "beta", _F32), _dev_ptr(state, "state", _F32),
         _dev_ptr(o, "o", _IO), N, H, dk, dv, _code(q.dtype), _code(o.dtype), _stream(stream))
     _check(st, "gdr_decode_step")
+    after()
 
 
-def gdr_decode_mtp(q, k, v, g, beta, state_in, state_out, o, inter=None, stream=None) -> None:
+def gdr_decode_mtp(q, k, v, g, beta, state_in, state_out, o, inter=None, stream=None, *,
+                   norm=None) -> None:
     """T decode tokens per (sequence, head).  q, k [N, T, H, dk], v [N, T, H, dv]
     (bf16 or fp32, one dtype); g, beta [N, T, H] fp32; state_in [N, H, dv, dk]
     fp32; state_out like state_in, the same tensor (in place) or None (no final
     state written); o [N, T, H, dv] bf16 or fp32; inter [N, T, H, dv, dk] fp32
-    or None (the state after every token)."""
+    or None (the state after every token).  norm: as gdr_decode_step's."""
     N, T, H, dk = q.shape
     dv = v.shape[3]
     if k.shape != q.shape or v.shape[:3] != (N, T, H) or g.shape != (N, T, H) \
@@ -206,6 +212,7 @@ def gdr_decode_mtp(q, k, v, g, beta, state_in, state_out, o, inter=None, stream=
         raise GdrError("gdr_decode_mtp: inconsistent shapes")
     if k.dtype != q.dtype or v.dtype != q.dtype:
         raise GdrError("gdr_decode_mtp: q, k, v must share a dtype")
+    after = _norm_after(o, norm, stream)
     st = _load().gdr_decode_mtp(
         _dev_ptr(q, "q", _IO), _dev_ptr(k, "k", _IO), _dev_ptr(v, "v", _IO),
         _dev_ptr(g, "g", _F32), _dev_ptr(beta, "beta", _F32),
@@ -213,6 +220,7 @@ def gdr_decode_mtp(q, k, v, g, beta, state_in, state_out, o, inter=None, stream=
         _dev_ptr(o, "o", _IO), _dev_ptr(inter, "inter", _F32, optional=True), N, T, H, dk, dv,
         _code(q.dtype), _code(o.dtype), _stream(stream))
     _check(st, "gdr_decode_mtp")
+    after()
 
 
 def gdr_max_chunks(T_total: int, N: int, chunk: int) -> int:
@@ -272,7 +280,7 @@ def _prefill_args(q, k, v, g, beta, cu_seqlens, state_in, state_out, o, chunk, L
 
 def gdr_chunk_prefill(q, k, v, g, beta, cu_seqlens, state_in, state_out, o, *, chunk=64,
                       L_out=None, M_out=None, fixed_out=None, workspace=None,
-                      stream=None) -> None:
+                      stream=None, norm=None) -> None:
     """Chunked prefill over packed sequences.  q, k [T, H, dk], v [T, H, dv];
     g, beta [T, H] fp32; cu_seqlens [N+1] int32 (device); state_in
     [N, H, dv, dk] fp32 or None; state_out [N, H, dv, dk] fp32; o [T, H, dv];
@@ -281,9 +289,11 @@ def gdr_chunk_prefill(q, k, v, g, beta, cu_seqlens, state_in, state_out, o, *, c
     with S_end = S_start @ M_c + L_c.  workspace: a uint8 device tensor of
     gdr_chunk_prefill_workspace_bytes(...) bytes, or None to allocate one here
     (on the launch stream, so that the caching allocator does not hand its
-    memory to work on another stream while the kernels still use it)."""
+    memory to work on another stream while the kernels still use it).  norm: as
+    gdr_decode_step's."""
     args, (T, N, H, dk, dv) = _prefill_args(q, k, v, g, beta, cu_seqlens, state_in, state_out, o,
                                             chunk, L_out, M_out, fixed_out, "gdr_chunk_prefill")
+    after = _norm_after(o, norm, stream)
     if workspace is None:
         need = gdr_chunk_prefill_workspace_bytes(T, N, H, dk, dv, chunk, q.dtype)
         with torch.cuda.stream(_stream_obj(stream)):
@@ -292,10 +302,12 @@ def gdr_chunk_prefill(q, k, v, g, beta, cu_seqlens, state_in, state_out, o, *, c
         *args, _dev_ptr(workspace, "workspace", (torch.uint8,)), workspace.numel(),
         _stream(stream))
     _check(st, "gdr_chunk_prefill")
+    after()
 
 
 def gdr_chunk_prefill_noalloc(q, k, v, g, beta, cu_seqlens, state_in, state_out, o, *, chunk=64,
-                              L_out=None, M_out=None, fixed_out=None, stream=None) -> None:
+                              L_out=None, M_out=None, fixed_out=None, stream=None,
+                              norm=None) -> None:
     """gdr_chunk_prefill on the library's static device scratch: no workspace
     argument and no allocation, for callers that cannot allocate (e.g. under
     HIP graph capture).  Same arguments and results as gdr_chunk_prefill; a
@@ -303,8 +315,10 @@ def gdr_chunk_prefill_noalloc(q, k, v, g, beta, cu_seqlens, state_in, state_out,
     overlap on one device share the scratch and race."""
     args, _ = _prefill_args(q, k, v, g, beta, cu_seqlens, state_in, state_out, o, chunk, L_out,
                             M_out, fixed_out, "gdr_chunk_prefill_noalloc")
+    after = _norm_after(o, norm, stream)
     st = _load().gdr_chunk_prefill_noalloc(*args, _stream(stream))
     _check(st, "gdr_chunk_prefill_noalloc")
+    after()
 
 
 def gdr_state_fixup(L, M, state_in, chunk_offsets, fixed, stream=None) -> None:
@@ -415,12 +429,12 @@ def _same_dtype(who, names, first, *others):
             raise GdrError(f"{who}: {names} must share a dtype")
 
 
-def gdr_linear_decode(q, k, v, g, state, o, *, scale=1.0, stream=None) -> None:
+def gdr_linear_decode(q, k, v, g, state, o, *, scale=1.0, stream=None, norm=None) -> None:
     """One token of linear attention with a decay for each head, S <- e^g S +
     v k^T, o = scale S q, state updated in place.  q, k [N, Hk, dk], v [N, H,
     dv] (bf16 or fp32, one dtype; tokens may be rows of wider tensors); g [N, H]
     or [H] fp32; state [N, H, dv, dk] fp32; o [N, H, dv] bf16 or fp32.  Value
-    head h reads query and key head h // (H // Hk)."""
+    head h reads query and key head h // (H // Hk).  norm: as gdr_decode_step's."""
     who = "gdr_linear_decode"
     N, Hk, dk = q.shape
     H, dv = v.shape[1:]
@@ -433,9 +447,11 @@ def gdr_linear_decode(q, k, v, g, state, o, *, scale=1.0, stream=None) -> None:
     kp, ks = _rows_ptr(k, "k", dev)
     vp, vs = _rows_ptr(v, "v", dev)
     gp, decay = _gates(g, N, H, dev, who)
+    after = _norm_after(o, norm, stream)
     _launch(who, _load().gdr_linear_decode, dev, stream, qp, kp, vp, gp,
             _ptr(state, "state", _F32, dev), _ptr(o, "o", _IO, dev), N, H, Hk, dk, dv, qs, ks, vs,
             scale, decay, _code(q.dtype), _code(o.dtype))
+    after()
 
 
 def gdr_linear_prefill_workspace_bytes(T_total, N, H, dk, dv, in_dtype=GDR_BF16) -> int:
@@ -475,25 +491,28 @@ def _linear_args(who, q, k, v, g, cu_seqlens, state_in, like_v):
 
 
 def gdr_linear_prefill(q, k, v, g, cu_seqlens, state_in, state_out, o, *, scale=1.0,
-                       workspace=None, stream=None) -> None:
+                       workspace=None, stream=None, norm=None) -> None:
     """Linear attention with a decay for each head over packed sequences: S_t =
     e^g S_{t-1} + v_t k_t^T, o_t = scale S_t q_t.  q, k [T, Hk, dk], v [T, H, dv]
     (bf16 or fp32, one dtype; tokens may be rows of wider tensors); g [T, H] or
     [H] fp32; cu_seqlens [N+1] int32 (device); state_in [N, H, dv, dk] fp32 or
     None; state_out like it (may be state_in) or None; o [T, H, dv] bf16 or
     fp32.  workspace: as gdr_chunk_prefill's, by
-    gdr_linear_prefill_workspace_bytes."""
+    gdr_linear_prefill_workspace_bytes.  norm: as gdr_decode_step's (of rows
+    behind the last sequence too, whose o is as the caller left it)."""
     who = "gdr_linear_prefill"
     dev, ptrs, strides, decay, (T, N, H, Hk, dk, dv) = _linear_args(who, q, k, v, g, cu_seqlens,
                                                                     state_in, (o,))
     if state_out is not None and state_out.shape != (N, H, dv, dk):
         raise GdrError(f"{who}: state_out must have shape {(N, H, dv, dk)}")
+    after = _norm_after(o, norm, stream)
     code, lib = _code(q.dtype), _load()
     wp, wb, workspace = _workspace(
         workspace, lib.gdr_linear_prefill_workspace_bytes(T, N, H, dk, dv, code), dev, stream)
     _launch(who, lib.gdr_linear_prefill, dev, stream, *ptrs,
             _ptr(state_out, "state_out", _F32, dev), _ptr(o, "o", _IO, dev), T, H, Hk, dk, dv,
             *strides, scale, decay, code, _code(o.dtype), wp, wb)
+    after()
 
 
 def gdr_linear_backward(q, k, v, g, cu_seqlens, state_in, do, dstate_out, dq, dk, dv, *, dg=None,
@@ -553,13 +572,39 @@ def gdr_block_norm(x, h=None, y=None, *, w_after=None, gate=None, act="silu", re
     y = h / rms(h) * w_before, each part where its operand is given.  gate and
     residual like x; weights [D]; h and y [..., D] (h may be left out where y is
     wanted; y exactly with w_before).  bf16 or fp32 each."""
+    dev, ptrs, rows, tail = _norm_call(x, h, y, w_after, gate, act, residual, scale, w_before, eps)
+    _launch("gdr_block_norm", _load().gdr_block_norm, dev, stream, *ptrs, rows, *tail)
+
+
+def _norm_call(x, h=None, y=None, w_after=None, gate=None, act="silu", residual=None, scale=1.0,
+               w_before=None, eps=1e-6):
+    """Device and arguments of a gdr_block_norm call: pointers, rows and the rest."""
     who = "gdr_block_norm"
     dev, rows, D, ac, ic, wc, oc = _norm_args(who, x, w_after, gate, act, residual, w_before, (),
                                               (h, y))
-    _launch(who, _load().gdr_block_norm, dev, stream, _ptr(x, "x", _IO, dev),
-            _ptr(w_after, "w_after", _IO, dev), _ptr(gate, "gate", _IO, dev),
-            _ptr(residual, "residual", _IO, dev), _ptr(w_before, "w_before", _IO, dev),
-            _ptr(h, "h", _IO, dev), _ptr(y, "y", _IO, dev), rows, D, scale, eps, ac, ic, wc, oc)
+    return dev, (_ptr(x, "x", _IO, dev), _ptr(w_after, "w_after", _IO, dev),
+                 _ptr(gate, "gate", _IO, dev), _ptr(residual, "residual", _IO, dev),
+                 _ptr(w_before, "w_before", _IO, dev), _ptr(h, "h", _IO, dev),
+                 _ptr(y, "y", _IO, dev)), rows, (D, scale, eps, ac, ic, wc, oc)
+
+
+def _nothing():
+    pass
+
+
+def _norm_after(o, norm, stream):
+    """The call of gdr_block_norm on o that `norm` asks for, its arguments checked
+    now: by the library too, in a call for no rows, which launches nothing."""
+    if norm is None:
+        return _nothing
+    who, fn = "gdr_block_norm", _load().gdr_block_norm
+    dev, ptrs, rows, tail = _norm_call(o, **norm)
+    if norm.get("h") is None and norm.get("y") is None:
+        raise GdrError(f"{who}: h or y is required")
+    if (norm.get("y") is None) != (norm.get("w_before") is None):
+        raise GdrError(f"{who}: y is given exactly when w_before is")
+    _launch(who, fn, dev, stream, *ptrs, 0, *tail)
+    return lambda: _launch(who, fn, dev, stream, *ptrs, rows, *tail)
 
 
 def gdr_block_norm_backward_workspace_bytes(rows, D) -> int:
