@@ -98,9 +98,10 @@ hipError_t launch_linear_dg(const LinearBatch& b, const float* row, int row_part
 hipError_t launch_linear_dg_heads(const LinearBatch& b, const double* unit_sum, float* dg,
                                   hipStream_t stream);
 
-// Sum of [T, H, d] fp32 over groups of heads to [T, H / group, d] of out_dtype,
-// for the tokens of the batch's sequences.
-hipError_t launch_linear_group_sum(const LinearBatch& b, const float* part, int group, int d,
-                                   void* out, int out_dtype, hipStream_t stream);
+// Sums of two [T, H, d] fp32 tensors over groups of heads to [T, H / group, d] of
+// out_dtype, for the tokens of the batch's sequences.
+hipError_t launch_linear_group_sum(const LinearBatch& b, const float* part_q, const float* part_k,
+                                   int group, int d, void* dq, void* dk, int out_dtype,
+                                   hipStream_t stream);
 
 }  // namespace gdr

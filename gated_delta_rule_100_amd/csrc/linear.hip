@@ -346,8 +346,6 @@ __device__ __forceinline__ Gates chunk_gates(float gate, bool per_token, int lan
 // Two barriers a chunk: one behind its last reads, and one behind the score
 // waves' writing P^T for the next chunk (right after the former, while the
 // compute waves form Z x).
-constexpr int kCopyWaves = 4;  // of the segment states' kernel
-
 template <Dt IN, int KD, int W, int PZ, bool DOT, int SW>
 struct ScanCfg {
   static constexpr int ES = IN == Dt::BF16 ? 2 : 4;
@@ -848,15 +846,16 @@ __device__ __forceinline__ void scan_pass(const LinearBatch& b, const LinearPass
   }
 }
 
-// Score waves of a workgroup: with eight compute waves and bf16 inputs three and
-// one copy wave (168 registers a wave), else four and four copy waves.
-template <Dt IN, int W>
-constexpr int score_waves() { return IN == Dt::BF16 && W == 8 ? 3 : 4; }
+// Score waves of a workgroup: with eight compute waves three and one copy wave
+// (168 registers a wave; with 128 the fp32 and the dot passes spill), with four
+// compute waves four and four copy waves.
+template <int W>
+constexpr int score_waves() { return W == 8 ? 3 : 4; }
 
 template <Dt IN, int KD, int W, bool DOT, bool BACK>
-__global__ __launch_bounds__((ScanCfg<IN, KD, W, DOT ? 3 : 2, DOT, score_waves<IN, W>()>::THREADS))
+__global__ __launch_bounds__((ScanCfg<IN, KD, W, DOT ? 3 : 2, DOT, score_waves<W>()>::THREADS))
 void linear_scan_kernel(LinearBatch b, LinearPass p) {
-  constexpr int SW = score_waves<IN, W>();
+  constexpr int SW = score_waves<W>();
   __shared__ __align__(1024) unsigned char lds[ScanCfg<IN, KD, W, DOT ? 3 : 2, DOT, SW>::BYTES];
   scan_pass<IN, KD, W, DOT, BACK, SW>(b, p, lds);
 }
@@ -864,9 +863,9 @@ void linear_scan_kernel(LinearBatch b, LinearPass p) {
 // The three passes of a gradient (dq, dv, dk) in one launch, where dk = dv: their
 // workgroups follow each other without the gaps of launches.
 template <Dt IN, int KD, int W>
-__global__ __launch_bounds__((ScanCfg<IN, KD, W, 3, true, score_waves<IN, W>()>::THREADS))
+__global__ __launch_bounds__((ScanCfg<IN, KD, W, 3, true, score_waves<W>()>::THREADS))
 void linear_grad_kernel(LinearBatch b, LinearPass pq, LinearPass pv, LinearPass pk) {
-  constexpr int SW = score_waves<IN, W>();
+  constexpr int SW = score_waves<W>();
   __shared__ __align__(1024) unsigned char lds[ScanCfg<IN, KD, W, 3, true, SW>::BYTES];
   if (blockIdx.y == 0) scan_pass<IN, KD, W, true, false, SW>(b, pq, lds);
   else if (blockIdx.y == 1) scan_pass<IN, KD, W, true, true, SW>(b, pv, lds);
@@ -885,7 +884,10 @@ struct LocalCfg {
   static constexpr int NB = C / 32;
   static constexpr int VS = 16 * W;
   static constexpr int CHK = KD * ES / 16, CHV = VS * ES / 16;
-  static constexpr int THREADS = 64 * (W + kCopyWaves + 1);
+  // copy waves: with four the fp32 form has 128 registers a wave and spills (4 x 2048
+  // tokens, 16 heads: prompt 174 us, with two 157); bf16 prompts take 115 us with both
+  static constexpr int CW = 2;
+  static constexpr int THREADS = 64 * (W + CW + 1);
   static constexpr int STAGES = 4;
   static constexpr int Y_BYTES = C * KD * ES, W_BYTES = C * VS * ES;
   static constexpr int BUF = Y_BYTES + W_BYTES;
@@ -893,7 +895,7 @@ struct LocalCfg {
   static constexpr int OFF_G = STAGES * BUF;
   static constexpr int BYTES = OFF_G + 2 * GATE_BYTES;
   // copies of a chunk by one copy wave
-  static constexpr int NY = C * CHK / 64 / kCopyWaves, NW = C * CHV / 64 / kCopyWaves;
+  static constexpr int NY = C * CHK / 64 / CW, NW = C * CHV / 64 / CW;
   static_assert(BYTES <= 160 * 1024, "LDS");
   static_assert(2 * (NY + NW) < 64, "copies in flight");
 };
@@ -908,7 +910,7 @@ template <Dt IN, int KD, int W, bool BACK>
 __device__ __forceinline__ void local_states(const LinearBatch& b, const LinearStates& job,
                                              int od_all, unsigned char* lds) {
   using Cfg = LocalCfg<IN, KD, W>;
-  constexpr int C = Cfg::C, NB = Cfg::NB, ES = Cfg::ES, NY = Cfg::NY, NW = Cfg::NW;
+  constexpr int C = Cfg::C, NB = Cfg::NB, ES = Cfg::ES, NY = Cfg::NY, NW = Cfg::NW, CW = Cfg::CW;
   const LinearRows &y = job.y, &w = job.w;
   const float us = job.us;
   float *states = job.states, *decays = job.decays;
@@ -926,7 +928,7 @@ __device__ __forceinline__ void local_states(const LinearBatch& b, const LinearS
     tok = tb + (BACK ? chunks - 1 - s : s) * C;
     return te - tok < C ? te - tok : C;
   };
-  if (wave == W + kCopyWaves) {  // ---- gate wave
+  if (wave == W + CW) {  // ---- gate wave
     auto load = [&](int s) {
       int tok;
       const int len = chunk_at(s, tok);
@@ -960,7 +962,7 @@ __device__ __forceinline__ void local_states(const LinearBatch& b, const LinearS
     const size_t yst = y.stride * ES, wst = w.stride * ES;
     auto piece = [&](int i, auto ch, int len, size_t stride) {
       constexpr int CH = decltype(ch)::value;
-      const int q = 64 * (cw + kCopyWaves * i) + lane, r = q / CH, pc = q % CH;
+      const int q = 64 * (cw + CW * i) + lane, r = q / CH, pc = q % CH;
       return static_cast<uint32_t>((r < len ? r : len - 1) * stride + 16 * (pc ^ perm<CH>(r)));
     };
     const std::integral_constant<int, Cfg::CHK> chk;
@@ -978,15 +980,15 @@ __device__ __forceinline__ void local_states(const LinearBatch& b, const LinearS
       unsigned char* to = lds + (s % Cfg::STAGES) * Cfg::BUF + 1024 * cw;
       if (len == C) {
 #pragma unroll
-        for (int i = 0; i < NY; ++i) copy16(yb + yo[i], to + 1024 * kCopyWaves * i);
+        for (int i = 0; i < NY; ++i) copy16(yb + yo[i], to + 1024 * CW * i);
 #pragma unroll
-        for (int i = 0; i < NW; ++i) copy16(wb + wo[i], to + Cfg::Y_BYTES + 1024 * kCopyWaves * i);
+        for (int i = 0; i < NW; ++i) copy16(wb + wo[i], to + Cfg::Y_BYTES + 1024 * CW * i);
       } else {
 #pragma unroll
-        for (int i = 0; i < NY; ++i) copy16(yb + piece(i, chk, len, yst), to + 1024 * kCopyWaves * i);
+        for (int i = 0; i < NY; ++i) copy16(yb + piece(i, chk, len, yst), to + 1024 * CW * i);
 #pragma unroll
         for (int i = 0; i < NW; ++i)
-          copy16(wb + piece(i, chv, len, wst), to + Cfg::Y_BYTES + 1024 * kCopyWaves * i);
+          copy16(wb + piece(i, chv, len, wst), to + Cfg::Y_BYTES + 1024 * CW * i);
       }
     };
     // chunk s + 1 is there when the copies of the (at most two) chunks behind it
@@ -1112,18 +1114,19 @@ __global__ __launch_bounds__(256) void linear_starts_kernel(LinearBatch b, int p
 
 // ---- gate gradient
 //
-// One workgroup a (unit, head): suffix sums of row - col from the unit's end, 256
-// tokens at a time, in fp64.  The roundings of row and col add up like a random
-// walk over the unit, but its value at both ends is known as a product of two
-// states (start_dot, end_dot), so what the sums miss at the start is spread evenly
-// over the unit's tokens: 1024 tokens, 16 heads: relative error of dg 1.1e-6
-// without this.
+// One workgroup a (unit, head): suffix sums of row - col from the unit's end, 1024
+// tokens at a time (four a thread, 256 apart, whose scans run side by side), in
+// fp64.  The roundings of row and col add up like a random walk over the unit, but
+// its value at both ends is known as a product of two states (start_dot, end_dot),
+// so what the sums miss at the start is spread evenly over the unit's tokens (1024
+// tokens, 16 heads: relative error of dg 1.1e-6 without this, 6.7e-7 with it).
 __global__ __launch_bounds__(256) void linear_dg_kernel(LinearBatch b, const float* row,
                                                         int row_parts, const float* col,
                                                         int col_parts, const float* start_dot,
                                                         int start_parts, const float* end_dot,
                                                         int end_parts, float* dg, double* unit_sum) {
-  __shared__ double wave_sum[2][4];
+  constexpr int B = 4, SPAN = 256 * B;
+  __shared__ double wave_sum[2][B][4], whole[4];
   const int pair = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = pair % b.H;
   Unit unit;
   double total = 0.0;
@@ -1143,38 +1146,52 @@ __global__ __launch_bounds__(256) void linear_dg_kernel(LinearBatch b, const flo
       }
       return v;
     };
-    double all = 0.0;
-    for (int t = unit.te - 1 - tid; t >= unit.tb; t -= 256) all += load(t);
+    const double to_start = start - acc;
+    const int len = unit.te - unit.tb;
+    double all = 0.0;  // the sum over the unit (of one span: from its scan)
+    if (len > SPAN) {
+      for (int t = unit.te - 1 - tid; t >= unit.tb; t -= 256) all += load(t);
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) all += __shfl_xor(all, d);
-    if (lane == 0) wave_sum[1][wave] = all;
-    __syncthreads();
-    all = wave_sum[1][0] + wave_sum[1][1] + wave_sum[1][2] + wave_sum[1][3];
-    const double miss = (start - acc - all) / (unit.te - unit.tb);  // a token
-    double ahead = load(unit.te - 1 - tid);
-    for (int hi = unit.te, slot = 0; hi > unit.tb; hi -= 256, slot ^= 1) {
-      const int t = hi - 1 - tid;  // thread 0 has the latest token
-      double v = ahead;
-      ahead = load(t - 256);
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const double up = __shfl_up(v, d);
-        if (lane >= d) v += up;
-      }
-      if (lane == 63) wave_sum[slot][wave] = v;
+      for (int d = 1; d < 64; d <<= 1) all += __shfl_xor(all, d);
+      if (lane == 0) whole[wave] = all;
       __syncthreads();
-      v += acc;
+      all = whole[0] + whole[1] + whole[2] + whole[3];
+    }
+    for (int hi = unit.te, slot = 0; hi > unit.tb; hi -= SPAN, slot ^= 1) {
+      double v[B];  // thread 0 has the latest token of each block
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (i < wave) v += wave_sum[slot][i];
-        acc += wave_sum[slot][i];
-      }
-      if (t >= unit.tb) {
-        v += miss * (unit.te - t);
+      for (int e = 0; e < B; ++e) v[e] = load(hi - 1 - tid - 256 * e);
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1)
+#pragma unroll
+        for (int e = 0; e < B; ++e) {
+          const double up = __shfl_up(v[e], d);
+          if (lane >= d) v[e] += up;
+        }
+#pragma unroll
+      for (int e = 0; e < B; ++e)
+        if (lane == 63) wave_sum[slot][e][wave] = v[e];
+      __syncthreads();
+      double sum = 0.0;
+#pragma unroll
+      for (int e = 0; e < B; ++e)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (i == wave) v[e] += acc + sum;
+          sum += wave_sum[slot][e][i];
+        }
+      acc += sum;
+      if (len <= SPAN) all = sum;
+      const double miss = (to_start - all) / len;  // a token
+#pragma unroll
+      for (int e = 0; e < B; ++e) {
+        const int t = hi - 1 - tid - 256 * e;
+        if (t < unit.tb) continue;
+        double r = v[e] + miss * (unit.te - t);
         if ((b.gates.per_token ? b.gates.g[static_cast<size_t>(t) * b.H + h] : b.gates.g[h]) < kMinGate)
-          v = 0.0;  // a decay of zero
-        total += v;
-        if (dg) dg[static_cast<size_t>(t) * b.H + h] = static_cast<float>(v);
+          r = 0.0;  // a decay of zero
+        total += r;
+        if (dg) dg[static_cast<size_t>(t) * b.H + h] = static_cast<float>(r);
       }
     }
   }
@@ -1182,9 +1199,9 @@ __global__ __launch_bounds__(256) void linear_dg_kernel(LinearBatch b, const flo
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
     __syncthreads();
-    if (lane == 0) wave_sum[0][wave] = total;
+    if (lane == 0) whole[wave] = total;
     __syncthreads();
-    if (tid == 0) unit_sum[pair] = wave_sum[0][0] + wave_sum[0][1] + wave_sum[0][2] + wave_sum[0][3];
+    if (tid == 0) unit_sum[pair] = whole[0] + whole[1] + whole[2] + whole[3];
   }
 }
 
@@ -1198,24 +1215,28 @@ __global__ __launch_bounds__(64) void linear_dg_heads_kernel(LinearBatch b, cons
   if (lane == 0) dg[h] = static_cast<float>(acc);
 }
 
-__global__ __launch_bounds__(256) void linear_group_sum_kernel(LinearBatch b, const float* part,
-                                                               int group, int d, void* out,
-                                                               int out_dtype) {
+// Sums over the value heads that share a head: dq (blockIdx.y = 0) and dk (1).
+__global__ __launch_bounds__(256) void linear_group_sum_kernel(LinearBatch b, const float* part_q,
+                                                               const float* part_k, int group, int d,
+                                                               void* dq, void* dk, int out_dtype) {
+  const float* part = blockIdx.y == 0 ? part_q : part_k;
+  void* out = blockIdx.y == 0 ? dq : dk;
   int te = b.cu[b.N];
   te = te < 0 ? 0 : (te > b.T_total ? b.T_total : te);
   const int hk = b.H / group;
   const size_t i = (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
   if (i >= static_cast<size_t>(te) * hk * d) return;
-  const size_t th = i / d;
-  const int col = i % d;
-  const size_t t = th / hk;
-  const int hh = th % hk;
+  // rows of a token's shared head are `group` rows of its value heads
+  const float* from = part + i / d * group * d + i % d;
   floatx4 acc = {0.f, 0.f, 0.f, 0.f};
-  for (int j = 0; j < group; ++j)
-    acc += *reinterpret_cast<const floatx4*>(part + (t * b.H + hh * group + j) * d + col);
-  for (int e = 0; e < 4; ++e) {
-    if (out_dtype == 0) store_scalar<Dt::BF16>(out, i + e, acc[e]);
-    else store_scalar<Dt::F32>(out, i + e, acc[e]);
+  for (int j = 0; j < group; ++j) acc += *reinterpret_cast<const floatx4*>(from + static_cast<size_t>(j) * d);
+  if (out_dtype == 0) {
+    uint32_t lo[1], hi[1];
+    split2<1>(acc[0], acc[1], lo);
+    split2<1>(acc[2], acc[3], hi);
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + i) = make_uint2(lo[0], hi[0]);
+  } else {
+    *reinterpret_cast<floatx4*>(static_cast<float*>(out) + i) = acc;
   }
 }
 
@@ -1328,7 +1349,7 @@ hipError_t launch_linear_pass(const LinearBatch& b, const LinearPass& p, hipStre
     auto go = [&](auto w, auto dot, auto back) {
       constexpr int W = decltype(w)::value;
       constexpr bool DOT = decltype(dot)::value, BACK = decltype(back)::value;
-      constexpr int THREADS = ScanCfg<IN, KD, W, DOT ? 3 : 2, DOT, score_waves<IN, W>()>::THREADS;
+      constexpr int THREADS = ScanCfg<IN, KD, W, DOT ? 3 : 2, DOT, score_waves<W>()>::THREADS;
       hipLaunchKernelGGL((linear_scan_kernel<IN, KD, W, DOT, BACK>),
                          dim3(scan_grid(b, p.od / (16 * W))), dim3(THREADS), 0, stream, b, p);
       return hipGetLastError();
@@ -1357,7 +1378,7 @@ hipError_t launch_linear_grads(const LinearBatch& b, const LinearPass& pq, const
   return by_type(b.in_dtype, pq.kd, [&](auto in, auto kd) {
     constexpr Dt IN = decltype(in)::value;
     constexpr int KD = decltype(kd)::value, W = KD / 16;
-    constexpr int THREADS = ScanCfg<IN, KD, W, 3, true, score_waves<IN, W>()>::THREADS;
+    constexpr int THREADS = ScanCfg<IN, KD, W, 3, true, score_waves<W>()>::THREADS;
     hipLaunchKernelGGL((linear_grad_kernel<IN, KD, W>), dim3(scan_grid(b, 1), 3), dim3(THREADS), 0,
                        stream, b, pq, pv, pk);
     return hipGetLastError();
@@ -1401,11 +1422,12 @@ hipError_t launch_linear_dg_heads(const LinearBatch& b, const double* unit_sum, 
   return hipGetLastError();
 }
 
-hipError_t launch_linear_group_sum(const LinearBatch& b, const float* part, int group, int d,
-                                   void* out, int out_dtype, hipStream_t stream) {
+hipError_t launch_linear_group_sum(const LinearBatch& b, const float* part_q, const float* part_k,
+                                   int group, int d, void* dq, void* dk, int out_dtype,
+                                   hipStream_t stream) {
   const size_t n = static_cast<size_t>(b.T_total) * (b.H / group) * d / 4;
-  hipLaunchKernelGGL(linear_group_sum_kernel, dim3((n + 255) / 256), dim3(256), 0, stream, b, part,
-                     group, d, out, out_dtype);
+  hipLaunchKernelGGL(linear_group_sum_kernel, dim3((n + 255) / 256, 2), dim3(256), 0, stream, b,
+                     part_q, part_k, group, d, dq, dk, out_dtype);
   return hipGetLastError();
 }
 

@@ -333,8 +333,7 @@ gdr_status gdr_linear_backward(const void* q, const void* k, const void* v, cons
   e = gdr::launch_linear_grads(b, pq, pv, pk, st);
   if (e != hipSuccess) return hip_fail(e, who, "scan");
   if (group > 1 && T_total > 0) {
-    e = gdr::launch_linear_group_sum(b, part_q, group, dk, dq, grad_dtype, st);
-    if (e == hipSuccess) e = gdr::launch_linear_group_sum(b, part_k, group, dk, dk_out, grad_dtype, st);
+    e = gdr::launch_linear_group_sum(b, part_q, part_k, group, dk, dq, dk_out, grad_dtype, st);
     if (e != hipSuccess) return hip_fail(e, who, "shared heads");
   }
   if (dg) {

@@ -57,7 +57,14 @@ __device__ __forceinline__ void load_weight(const void* w, int dtype, int D, int
   else load_row<Dt::F32, TPR, E>(w, 0, D, t, vec, out);
 }
 
-template <int TPR, int E>
+template <bool STREAM, class V>
+__device__ __forceinline__ void put(V* p, V v) {
+  if constexpr (STREAM) __builtin_nontemporal_store(v, p);
+  else *p = v;
+}
+
+// STREAM: past the caches (vectors only).
+template <int TPR, int E, bool STREAM = false>
 __device__ __forceinline__ void store_row(void* base, int dtype, size_t row, int D, int t, bool vec,
                                           const float (&x)[E]) {
   typedef float f32x8 __attribute__((ext_vector_type(8)));
@@ -72,12 +79,12 @@ __device__ __forceinline__ void store_row(void* base, int dtype, size_t row, int
         f32x8 v;
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = x[8 * j + e];
-        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(base) + at + c) =
-            __builtin_bit_cast(u32x4, __builtin_convertvector(v, bf16x8));
+        put<STREAM>(reinterpret_cast<u32x4*>(static_cast<uint16_t*>(base) + at + c),
+                    __builtin_bit_cast(u32x4, __builtin_convertvector(v, bf16x8)));
       } else {
         floatx4* p = reinterpret_cast<floatx4*>(static_cast<float*>(base) + at + c);
-        p[0] = floatx4{x[8 * j], x[8 * j + 1], x[8 * j + 2], x[8 * j + 3]};
-        p[1] = floatx4{x[8 * j + 4], x[8 * j + 5], x[8 * j + 6], x[8 * j + 7]};
+        put<STREAM>(p, floatx4{x[8 * j], x[8 * j + 1], x[8 * j + 2], x[8 * j + 3]});
+        put<STREAM>(p + 1, floatx4{x[8 * j + 4], x[8 * j + 5], x[8 * j + 6], x[8 * j + 7]});
       }
     }
   } else {
@@ -281,7 +288,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256, IN == Dt::BF16 && TPR <= 256
 #pragma unroll
       for (int i = 0; i < E; ++i) d[i] = fmaf(ih, fmaf(-h[i], dot, dy[i]), d[i]);
     }
-    if (p.dresidual) store_row<TPR, E>(p.dresidual, p.out_dtype, row, p.D, t, vec, d);
+    if (p.dresidual) store_row<TPR, E, true>(p.dresidual, p.out_dtype, row, p.D, t, vec, d);
 #pragma unroll
     for (int i = 0; i < E; ++i) d[i] *= p.scale;
     if (p.gate) {
@@ -294,7 +301,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256, IN == Dt::BF16 && TPR <= 256
         z[i] = d[i] * n * slope;
         d[i] *= a;
       }
-      if (p.dgate) store_row<TPR, E>(p.dgate, p.out_dtype, row, p.D, t, vec, z);
+      if (p.dgate) store_row<TPR, E, true>(p.dgate, p.out_dtype, row, p.D, t, vec, z);
     }
     if (p.w_after) {
       float dot = 0.f;
@@ -309,7 +316,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256, IN == Dt::BF16 && TPR <= 256
 #pragma unroll
       for (int i = 0; i < E; ++i) d[i] = ix * fmaf(-x[i], dot, d[i]);
     }
-    store_row<TPR, E>(p.dx, p.out_dtype, row, p.D, t, vec, d);
+    store_row<TPR, E, true>(p.dx, p.out_dtype, row, p.D, t, vec, d);
   }
   // this workgroup's weight gradients: rows of one column added in order
   __shared__ float cols[RPB > 1 ? THREADS * E : 1];
