@@ -40,15 +40,12 @@ struct LinearRows {
   int64_t stride;
   int group;
 };
-// Partial sums of a dot product over od columns: one a workgroup.
-inline int linear_parts(int od) { return od == 128 ? 1 : od / 64; }
 
 struct LinearPass {
   LinearRows x, y, w;
   LinearRows e;        // rows of od values to dot with the outputs (dot != NULL)
   void* out;           // [T, H, od]
-  float* dot;          // [linear_parts(od)][H][T] partial sums of e_t . out_t
-                       // without the token's own term, or NULL
+  float* dot;          // [H][T] e_t . out_t without the token's own term, or NULL
   const float* start;  // [units * H] states the walks start from, NULL for zero
   float* end;          // [N * H] states where the last walk of a sequence ends,
                        // NULL: not written; not written for sequences without units
@@ -65,9 +62,11 @@ hipError_t launch_linear_decode(const void* q, const void* k, const void* v,
                                 int dk, int dv, int64_t qs, int64_t ks, int64_t vs, float scale,
                                 int in_dtype, int out_dtype, hipStream_t stream);
 
-hipError_t launch_linear_pass(const LinearBatch& b, const LinearPass& p, hipStream_t stream);
+// A forward pass without dot products.
+hipError_t launch_linear_prompt(const LinearBatch& b, const LinearPass& p, hipStream_t stream);
 
-// The passes of a gradient: dq forwards, dv and dk backwards.
+// The passes of a gradient: dq forwards, dv and dk backwards; dot products in both
+// of the first two or in none.
 hipError_t launch_linear_grads(const LinearBatch& b, const LinearPass& pq, const LinearPass& pv,
                                const LinearPass& pk, hipStream_t stream);
 
@@ -86,13 +85,12 @@ hipError_t launch_linear_starts(const LinearBatch& b, int od, int kd, const Line
                                 const LinearStates* backward, hipStream_t stream);
 
 // dg_t = dg_{t+1} + row_t - col_t over every unit, from its end's dot product and
-// back to its start's (NULL: zero); row and col are [parts][H][T] partial sums,
-// start_dot and end_dot [parts][units * H].  dg_t goes to dg ([T, H]), or its sum
+// back to its start's (NULL: zero); row and col are [H][T], start_dot and end_dot
+// partial sums [parts][units * H].  dg_t goes to dg ([T, H]), or its sum
 // over the unit's tokens to unit_sum ([units * H]).
-hipError_t launch_linear_dg(const LinearBatch& b, const float* row, int row_parts,
-                            const float* col, int col_parts, const float* start_dot,
-                            int start_parts, const float* end_dot, int end_parts, float* dg,
-                            double* unit_sum, hipStream_t stream);
+hipError_t launch_linear_dg(const LinearBatch& b, const float* row, const float* col,
+                            const float* start_dot, int start_parts, const float* end_dot,
+                            int end_parts, float* dg, double* unit_sum, hipStream_t stream);
 
 // dg[h] = sum over units of unit_sum.
 hipError_t launch_linear_dg_heads(const LinearBatch& b, const double* unit_sum, float* dg,

@@ -19,7 +19,6 @@ namespace gdr {
 namespace {
 
 constexpr float kMinGate = -110.f;  // e^-110 is zero in fp32: stands for every smaller g
-constexpr int kXcds = 8;
 
 __device__ __forceinline__ float clamp_gate(float g) { return g < kMinGate ? kMinGate : g; }
 
@@ -330,8 +329,9 @@ __device__ __forceinline__ Gates chunk_gates(float gate, bool per_token, int lan
 
 // ---- the chunk scan
 //
-// One workgroup per (unit, head, 16 W columns of w): a unit is a sequence, or a
-// segment of one.  Its waves have three roles:
+// One workgroup for a (unit, head): a unit is a sequence, or a segment of one.
+// It holds the whole state of od = 16 W rows, so that x, y and the scores are read
+// and formed once.  Its waves have three roles:
 //   - W compute waves hold 16 state rows each for the whole walk, as output
 //     tiles of the state update: lane (c, g) holds Z[c][32 j + 8 g + 0..7],
 //     which is also the fragment of Z in the product with x.  In step s they
@@ -339,25 +339,41 @@ __device__ __forceinline__ Gates chunk_gates(float gate, bool per_token, int lan
 //   - SW score waves form the scores x.y of chunk s + 1, with their decays, in
 //     registers: they do not depend on the state, and their arithmetic fills
 //     the issue slots that the compute waves' chain leaves;
-//   - SW copy waves copy the x and y rows of chunk s + 2 and the w rows of chunk
+//   - CW copy waves copy the x and y rows of chunk s + 2 and the w rows of chunk
 //     s + 1 to LDS (global-to-LDS loads) and form the gate factors of s + 2.
 //     They are waves of their own because a wave's LDS reads wait for all its
-//     global-to-LDS loads in flight.
+//     global-to-LDS loads in flight (copies by the score waves: 5.05 us a chunk
+//     of 64 tokens, 128 x 128; by waves of their own 3.0).
 // Two barriers a chunk: one behind its last reads, and one behind the score
 // waves' writing P^T for the next chunk (right after the former, while the
 // compute waves form Z x).
+//
+// Numerics beside bf16 inputs: the state stays fp32 in registers; Z and P enter
+// the products as two bf16 planes (2^-18 of a term, against 2^-9 of a bf16
+// output), three where the outputs also feed dg, whose sums run over a segment;
+// the decayed w that the state accumulates always as three (its full 24 bits).
+// fp32 inputs run on fp32 matrix instructions throughout.
+//
+// A chunk's matrix instructions (776 of 16 x 16 x 32 at 128 x 128, 16 cycles each on
+// one of four SIMDs) take 48% of its time, vector arithmetic about as much again:
+// the two do not overlap enough.  4 x 4096 tokens, 16 heads, bf16: 69 us for 16
+// chunks a workgroup after a prologue of 7.5 us, 110-115 us with the segments'
+// states and their chain (2.4 TB/s of q, k, v and o once).  Tried and not kept:
+// four compute waves of 32 rows each, which halve the LDS reads (119 us; the
+// gradient 381 against 343), matrix and vector instructions interleaved by
+// scheduling groups (123; 374-398), wave priorities (115; 345-354).
 template <Dt IN, int KD, int W, int PZ, bool DOT, int SW>
 struct ScanCfg {
   static constexpr int ES = IN == Dt::BF16 ? 2 : 4;
   static constexpr int C = IN == Dt::BF16 ? 64 : 32;  // tokens a chunk (fp32: half, for LDS)
   static constexpr int NT = C / 16, NB = C / 32;
   static constexpr int KB = KD / 32;          // 32-deep blocks over kd
-  static constexpr int VS = 16 * W;           // columns of w a workgroup
-  static constexpr int CHK = KD * ES / 16, CHV = VS * ES / 16;
+  static constexpr int OD = 16 * W;           // columns of w
+  static constexpr int CHK = KD * ES / 16, CHV = OD * ES / 16;
   static constexpr int CW = SW == 3 ? 1 : 4;  // copy waves
   static constexpr int THREADS = 64 * (W + SW + CW);
   // three buffers of x and y rows, two of w rows
-  static constexpr int X_BYTES = C * KD * ES, W_BYTES = C * VS * ES;
+  static constexpr int X_BYTES = C * KD * ES, W_BYTES = C * OD * ES;
   static constexpr int OFF_W = 3 * 2 * X_BYTES;
   // three of gate factors: G in log2 units as a sum of two floats, the factors
   // of Z x_t and of the update, e^{G_C}
@@ -408,11 +424,7 @@ __device__ __forceinline__ void scan_pass(const LinearBatch& b, const LinearPass
   constexpr int C = Cfg::C, NT = Cfg::NT, NB = Cfg::NB, KB = Cfg::KB, ES = Cfg::ES, PL = Cfg::PL;
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // the workgroups of one (unit, head) read the same x and y rows: one XCD
-  const int slices = p.od / Cfg::VS, xcd = blockIdx.x % kXcds, k0 = blockIdx.x / kXcds;
-  const int slice = k0 % slices, pair = (k0 / slices) * kXcds + xcd;
-  if (pair >= b.units * b.H) return;
-  const int h = pair % b.H;
+  const int pair = blockIdx.x, h = pair % b.H;
   Unit unit;
   if (!unit_at(b, pair / b.H, unit)) return;
   const int tb = unit.tb, te = unit.te;
@@ -432,12 +444,12 @@ __device__ __forceinline__ void scan_pass(const LinearBatch& b, const LinearPass
   if (wave >= W + SW) {  // ---- copy waves
     if (chunks == 0) return;
     const int cw = wave - W - SW;
-    auto rows = [&](const LinearRows& r, int width, int skip) {
-      return static_cast<const char*>(r.p) + (static_cast<size_t>(h / r.group) * width + skip) * ES;
+    auto rows = [&](const LinearRows& r, int width) {
+      return static_cast<const char*>(r.p) + static_cast<size_t>(h / r.group) * width * ES;
     };
-    const char* xs = rows(p.x, KD, 0);
-    const char* ys = rows(p.y, KD, 0);
-    const char* ws = rows(p.w, p.od, slice * Cfg::VS);
+    const char* xs = rows(p.x, KD);
+    const char* ys = rows(p.y, KD);
+    const char* ws = rows(p.w, Cfg::OD);
     const size_t xst = p.x.stride * ES, yst = p.y.stride * ES, wst = p.w.stride * ES;
     // Byte offsets of this lane's 16-byte pieces inside a chunk: 64 rows apart
     // they stay below 2^32 (strides are at most 2^24 elements).  In a chunk
@@ -532,7 +544,7 @@ __device__ __forceinline__ void scan_pass(const LinearBatch& b, const LinearPass
         for (int i = 0; i < W; ++i) sum += part[i * C + lane];
       }
       if (lane < len)
-        p.dot[(static_cast<size_t>(slice) * b.H + h) * b.T_total + tok + lane] = sum;
+        p.dot[static_cast<size_t>(h) * b.T_total + tok + lane] = sum;
     };
     for (int s = 0, buf = 2; s < chunks; ++s, buf = next(buf)) {
       float gate = 0.f;
@@ -654,8 +666,9 @@ __device__ __forceinline__ void scan_pass(const LinearBatch& b, const LinearPass
   }
 
   // ---- compute waves
-  const int od = slice * Cfg::VS + 16 * wave;  // this wave's columns of w
-  const size_t zbase = static_cast<size_t>(pair) * p.od * KD + (od + c) * p.row;
+  constexpr int OD = Cfg::OD;
+  const int od = 16 * wave;  // this wave's columns of w
+  const size_t zbase = static_cast<size_t>(pair) * OD * KD + (od + c) * p.row;
   floatx4 z[KD / 16];  // z[2 j + i][e] = Z[od + c][32 j + 8 g + 4 i + e]
 #pragma unroll
   for (int j = 0; j < KD / 16; ++j) {
@@ -669,9 +682,9 @@ __device__ __forceinline__ void scan_pass(const LinearBatch& b, const LinearPass
     lds_barrier();
   }
   const size_t out_es = p.out_dtype == 0 ? 2 : 4;
-  const uint32_t out_row = static_cast<uint32_t>(b.H * p.od * out_es);
+  const uint32_t out_row = static_cast<uint32_t>(b.H * OD * out_es);
   const uint32_t out_lane = c * out_row + static_cast<uint32_t>(4 * g * out_es);
-  const size_t e_col = DOT ? static_cast<size_t>(h / p.e.group) * p.od + od + 4 * g : 0;
+  const size_t e_col = DOT ? static_cast<size_t>(h / p.e.group) * OD + od + 4 * g : 0;
   int kl[KB], jl[KD / 32];
 #pragma unroll
   for (int kb = 0; kb < KB; ++kb) {
@@ -803,7 +816,7 @@ __device__ __forceinline__ void scan_pass(const LinearBatch& b, const LinearPass
       }
     }
     char* out = static_cast<char*>(p.out) +
-                ((static_cast<size_t>(tok) * b.H + h) * p.od + od) * out_es;
+                ((static_cast<size_t>(tok) * b.H + h) * OD + od) * out_es;
     auto store = [&](int tt) {
       const uint32_t at = out_lane + 16 * tt * out_row;
       if (p.out_dtype == 0) {
@@ -828,7 +841,7 @@ __device__ __forceinline__ void scan_pass(const LinearBatch& b, const LinearPass
 
   float ed = 0.f;
   const bool ends = p.end && (BACK ? unit.first : unit.last);
-  const size_t ebase = (static_cast<size_t>(unit.n) * b.H + h) * p.od * KD + (od + c) * p.row;
+  const size_t ebase = (static_cast<size_t>(unit.n) * b.H + h) * OD * KD + (od + c) * p.row;
 #pragma unroll
   for (int j = 0; j < KD / 16; ++j) {
     const size_t at = (32 * (j >> 1) + 8 * g + 4 * (j & 1)) * p.col;
@@ -852,44 +865,56 @@ __device__ __forceinline__ void scan_pass(const LinearBatch& b, const LinearPass
 template <int W>
 constexpr int score_waves() { return W == 8 ? 3 : 4; }
 
-template <Dt IN, int KD, int W, bool DOT, bool BACK>
-__global__ __launch_bounds__((ScanCfg<IN, KD, W, DOT ? 3 : 2, DOT, score_waves<W>()>::THREADS))
+template <Dt IN, int KD, int OD, bool DOT>
+using ScanCfgOf = ScanCfg<IN, KD, OD / 16, DOT ? 3 : 2, DOT, score_waves<OD / 16>()>;
+
+template <Dt IN, int KD, int OD>
+__global__ __launch_bounds__((ScanCfgOf<IN, KD, OD, false>::THREADS))
 void linear_scan_kernel(LinearBatch b, LinearPass p) {
-  constexpr int SW = score_waves<W>();
-  __shared__ __align__(1024) unsigned char lds[ScanCfg<IN, KD, W, DOT ? 3 : 2, DOT, SW>::BYTES];
-  scan_pass<IN, KD, W, DOT, BACK, SW>(b, p, lds);
+  __shared__ __align__(1024) unsigned char lds[ScanCfgOf<IN, KD, OD, false>::BYTES];
+  scan_pass<IN, KD, OD / 16, false, false, score_waves<OD / 16>()>(b, p, lds);
 }
 
-// The three passes of a gradient (dq, dv, dk) in one launch, where dk = dv: their
-// workgroups follow each other without the gaps of launches.
-template <Dt IN, int KD, int W>
-__global__ __launch_bounds__((ScanCfg<IN, KD, W, 3, true, score_waves<W>()>::THREADS))
+// The three passes of a gradient (dq, dv, dk) in one launch: their workgroups follow
+// each other without the gaps of launches, and run side by side where one pass does
+// not fill the GPU (6 fp32 sequences of up to 777 tokens, 8 heads, 64 x 128: 85 us
+// in three launches, 73 in one).
+template <Dt IN, int DK, int DV, bool DOT>
+struct GradCfg {
+  using K = ScanCfgOf<IN, DV, DK, DOT>;  // dq and dk
+  using V = ScanCfgOf<IN, DK, DV, DOT>;  // dv
+  static constexpr int THREADS = K::THREADS, BYTES = K::BYTES > V::BYTES ? K::BYTES : V::BYTES;
+  static_assert(V::THREADS == THREADS, "one launch");
+};
+template <Dt IN, int DK, int DV, bool DOT>
+__global__ __launch_bounds__((GradCfg<IN, DK, DV, DOT>::THREADS))
 void linear_grad_kernel(LinearBatch b, LinearPass pq, LinearPass pv, LinearPass pk) {
-  constexpr int SW = score_waves<W>();
-  __shared__ __align__(1024) unsigned char lds[ScanCfg<IN, KD, W, 3, true, SW>::BYTES];
-  if (blockIdx.y == 0) scan_pass<IN, KD, W, true, false, SW>(b, pq, lds);
-  else if (blockIdx.y == 1) scan_pass<IN, KD, W, true, true, SW>(b, pv, lds);
-  else scan_pass<IN, KD, W, false, true, SW>(b, pk, lds);
+  __shared__ __align__(1024) unsigned char lds[GradCfg<IN, DK, DV, DOT>::BYTES];
+  constexpr int WK = DK / 16, WV = DV / 16, SK = score_waves<WK>(), SV = score_waves<WV>();
+  if (blockIdx.y == 0) scan_pass<IN, DV, WK, DOT, false, SK>(b, pq, lds);
+  else if (blockIdx.y == 1) scan_pass<IN, DK, WV, DOT, true, SV>(b, pv, lds);
+  else scan_pass<IN, DV, WK, false, true, SK>(b, pk, lds);
 }
 
 // ---- states at the starts of segments
 //
 // A segment's own state, from zero: the update of the scan alone.  It is a
 // stream of y and w rows, so the copy waves run three chunks ahead (four buffers,
-// one barrier a chunk); one wave forms the gate factors.
+// one barrier a chunk); one wave forms the gate factors.  4 x 4096 tokens, 16 heads,
+// bf16: 36 us, 3.7 TB/s; bound by the copies and 10 us of start and end.
 template <Dt IN, int KD, int W>
 struct LocalCfg {
   static constexpr int ES = IN == Dt::BF16 ? 2 : 4;
   static constexpr int C = IN == Dt::BF16 ? 64 : 32;
   static constexpr int NB = C / 32;
-  static constexpr int VS = 16 * W;
-  static constexpr int CHK = KD * ES / 16, CHV = VS * ES / 16;
+  static constexpr int OD = 16 * W;
+  static constexpr int CHK = KD * ES / 16, CHV = OD * ES / 16;
   // copy waves: with four the fp32 form has 128 registers a wave and spills (4 x 2048
   // tokens, 16 heads: prompt 174 us, with two 157); bf16 prompts take 115 us with both
   static constexpr int CW = 2;
   static constexpr int THREADS = 64 * (W + CW + 1);
   static constexpr int STAGES = 4;
-  static constexpr int Y_BYTES = C * KD * ES, W_BYTES = C * VS * ES;
+  static constexpr int Y_BYTES = C * KD * ES, W_BYTES = C * OD * ES;
   static constexpr int BUF = Y_BYTES + W_BYTES;
   static constexpr int GATE_BYTES = (C + 4) * 4;  // update factors, e^{G_C}
   static constexpr int OFF_G = STAGES * BUF;
@@ -908,7 +933,7 @@ __device__ __forceinline__ void wait_vmem() {
 
 template <Dt IN, int KD, int W, bool BACK>
 __device__ __forceinline__ void local_states(const LinearBatch& b, const LinearStates& job,
-                                             int od_all, unsigned char* lds) {
+                                             unsigned char* lds) {
   using Cfg = LocalCfg<IN, KD, W>;
   constexpr int C = Cfg::C, NB = Cfg::NB, ES = Cfg::ES, NY = Cfg::NY, NW = Cfg::NW, CW = Cfg::CW;
   const LinearRows &y = job.y, &w = job.w;
@@ -916,10 +941,7 @@ __device__ __forceinline__ void local_states(const LinearBatch& b, const LinearS
   float *states = job.states, *decays = job.decays;
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int slices = od_all / Cfg::VS, xcd = blockIdx.x % kXcds, k0 = blockIdx.x / kXcds;
-  const int slice = k0 % slices, pair = (k0 / slices) * kXcds + xcd;
-  if (pair >= b.units * b.H) return;
-  const int h = pair % b.H;
+  const int pair = blockIdx.x, h = pair % b.H;
   Unit unit;
   if (!unit_at(b, pair / b.H, unit)) return;
   if (BACK ? unit.first : unit.last) return;  // nothing starts from its end
@@ -958,7 +980,7 @@ __device__ __forceinline__ void local_states(const LinearBatch& b, const LinearS
     const int cw = wave - W;
     const char* ys = static_cast<const char*>(y.p) + static_cast<size_t>(h / y.group) * KD * ES;
     const char* ws = static_cast<const char*>(w.p) +
-                     (static_cast<size_t>(h / w.group) * od_all + slice * Cfg::VS) * ES;
+                     static_cast<size_t>(h / w.group) * Cfg::OD * ES;
     const size_t yst = y.stride * ES, wst = w.stride * ES;
     auto piece = [&](int i, auto ch, int len, size_t stride) {
       constexpr int CH = decltype(ch)::value;
@@ -1011,7 +1033,7 @@ __device__ __forceinline__ void local_states(const LinearBatch& b, const LinearS
     return;
   }
   // ---- compute waves
-  const int od = slice * Cfg::VS + 16 * wave;
+  const int od = 16 * wave;
   floatx4 z[KD / 16];
 #pragma unroll
   for (int j = 0; j < KD / 16; ++j) z[j] = floatx4{0.f, 0.f, 0.f, 0.f};
@@ -1053,7 +1075,7 @@ __device__ __forceinline__ void local_states(const LinearBatch& b, const LinearS
     }
     lds_barrier();
   }
-  float* to = states + (static_cast<size_t>(pair) * od_all + od + c) * KD;
+  float* to = states + (static_cast<size_t>(pair) * Cfg::OD + od + c) * KD;
 #pragma unroll
   for (int j = 0; j < KD / 16; ++j)
     *reinterpret_cast<floatx4*>(to + 32 * (j >> 1) + 8 * g + 4 * (j & 1)) = z[j];
@@ -1063,15 +1085,16 @@ __device__ __forceinline__ void local_states(const LinearBatch& b, const LinearS
 // One job forwards (blockIdx.y = 0), one backwards (1).
 template <Dt IN, int KD, int W>
 __global__ __launch_bounds__((LocalCfg<IN, KD, W>::THREADS)) void linear_local_kernel(
-    LinearBatch b, LinearStates forward, LinearStates backward, int od_all) {
+    LinearBatch b, LinearStates forward, LinearStates backward) {
   __shared__ __align__(1024) unsigned char lds[LocalCfg<IN, KD, W>::BYTES];
-  if (blockIdx.y == 0) local_states<IN, KD, W, false>(b, forward, od_all, lds);
-  else local_states<IN, KD, W, true>(b, backward, od_all, lds);
+  if (blockIdx.y == 0) local_states<IN, KD, W, false>(b, forward, lds);
+  else local_states<IN, KD, W, true>(b, backward, lds);
 }
 
 // The chain over a sequence's segments, elementwise: states[u] becomes the state
 // in front of segment u's walk.  One thread has four elements; kAhead segments
-// are read before the first is needed.
+// are read before the first is needed (4 sequences of 4 segments, 16 heads: 8 us;
+// bound by its launch and two dependent reads).
 constexpr int kAhead = 8;
 __global__ __launch_bounds__(256) void linear_starts_kernel(LinearBatch b, int per,
                                                             LinearStates forward,
@@ -1121,8 +1144,7 @@ __global__ __launch_bounds__(256) void linear_starts_kernel(LinearBatch b, int p
 // so what the sums miss at the start is spread evenly over the unit's tokens (1024
 // tokens, 16 heads: relative error of dg 1.1e-6 without this, 6.7e-7 with it).
 __global__ __launch_bounds__(256) void linear_dg_kernel(LinearBatch b, const float* row,
-                                                        int row_parts, const float* col,
-                                                        int col_parts, const float* start_dot,
+                                                        const float* col, const float* start_dot,
                                                         int start_parts, const float* end_dot,
                                                         int end_parts, float* dg, double* unit_sum) {
   constexpr int B = 4, SPAN = 256 * B;
@@ -1131,7 +1153,7 @@ __global__ __launch_bounds__(256) void linear_dg_kernel(LinearBatch b, const flo
   Unit unit;
   double total = 0.0;
   if (unit_at(b, pair / b.H, unit) && unit.te > unit.tb) {
-    const size_t th = static_cast<size_t>(b.T_total) * b.H, units = static_cast<size_t>(b.units) * b.H;
+    const size_t units = static_cast<size_t>(b.units) * b.H;
     double acc = 0.0, start = 0.0;
     if (end_dot)
       for (int i = 0; i < end_parts; ++i) acc += end_dot[i * units + pair];
@@ -1141,8 +1163,7 @@ __global__ __launch_bounds__(256) void linear_dg_kernel(LinearBatch b, const flo
       double v = 0.0;
       if (t >= unit.tb) {
         const size_t at = static_cast<size_t>(h) * b.T_total + t;
-        for (int i = 0; i < row_parts; ++i) v += row[i * th + at];
-        for (int i = 0; i < col_parts; ++i) v -= col[i * th + at];
+        v = static_cast<double>(row[at]) - col[at];
       }
       return v;
     };
@@ -1243,7 +1264,9 @@ __global__ __launch_bounds__(256) void linear_group_sum_kernel(LinearBatch b, co
 // One token: row i of a state becomes alpha s_i + v_i k, its output scale s_i . q.
 // The state is read once and written once, and that stream is the whole cost:
 // 16 lanes to a row with 16-byte non-temporal accesses, ROWS rows of one head a
-// workgroup, every load issued before any arithmetic, no LDS.
+// workgroup, every load issued before any arithmetic, no LDS.  64 sequences, 32
+// heads, 128 x 128: 43.3 us, 6.2 TB/s of state; 3 sequences, 16 heads: 7.9 us, a
+// launch.
 constexpr int kDecodeThreads = 256;
 
 template <int DK, int DV, Dt IN, Dt OUT, int ROWS>
@@ -1325,62 +1348,45 @@ hipError_t launch_linear_decode(const void* q, const void* k, const void* v,
 
 namespace {
 
-// Calls go(IN, KD) with the types of a pass.
+// Calls go(IN, KD, OD) with the types of a pass.
 template <class F>
-hipError_t by_type(int in_dtype, int kd, F&& go) {
-  const std::integral_constant<Dt, Dt::BF16> bf16;
-  const std::integral_constant<Dt, Dt::F32> f32;
-  const std::integral_constant<int, 64> k64;
-  const std::integral_constant<int, 128> k128;
-  if (in_dtype == 0) return kd == 64 ? go(bf16, k64) : go(bf16, k128);
-  return kd == 64 ? go(f32, k64) : go(f32, k128);
+hipError_t by_type(int in_dtype, int kd, int od, F&& go) {
+  const std::integral_constant<int, 64> d64;
+  const std::integral_constant<int, 128> d128;
+  auto with = [&](auto in) {
+    if (kd == 64) return od == 64 ? go(in, d64, d64) : go(in, d64, d128);
+    return od == 64 ? go(in, d128, d64) : go(in, d128, d128);
+  };
+  return in_dtype == 0 ? with(std::integral_constant<Dt, Dt::BF16>())
+                       : with(std::integral_constant<Dt, Dt::F32>());
 }
 
-unsigned scan_grid(const LinearBatch& b, int slices) {
-  return static_cast<unsigned>((b.units * b.H + kXcds - 1) / kXcds * kXcds) * slices;
-}
+unsigned scan_grid(const LinearBatch& b) { return static_cast<unsigned>(b.units * b.H); }
 
 }  // namespace
 
-hipError_t launch_linear_pass(const LinearBatch& b, const LinearPass& p, hipStream_t stream) {
-  return by_type(b.in_dtype, p.kd, [&](auto in, auto kd) {
+hipError_t launch_linear_prompt(const LinearBatch& b, const LinearPass& p, hipStream_t stream) {
+  return by_type(b.in_dtype, p.kd, p.od, [&](auto in, auto kd, auto od) {
     constexpr Dt IN = decltype(in)::value;
-    constexpr int KD = decltype(kd)::value;
-    auto go = [&](auto w, auto dot, auto back) {
-      constexpr int W = decltype(w)::value;
-      constexpr bool DOT = decltype(dot)::value, BACK = decltype(back)::value;
-      constexpr int THREADS = ScanCfg<IN, KD, W, DOT ? 3 : 2, DOT, score_waves<W>()>::THREADS;
-      hipLaunchKernelGGL((linear_scan_kernel<IN, KD, W, DOT, BACK>),
-                         dim3(scan_grid(b, p.od / (16 * W))), dim3(THREADS), 0, stream, b, p);
-      return hipGetLastError();
-    };
-    const std::integral_constant<int, 4> w4;
-    const std::integral_constant<int, 8> w8;
-    const std::true_type yes;
-    const std::false_type no;
-    if (p.od == 128) {
-      if (p.dot) return p.backward ? go(w8, yes, yes) : go(w8, yes, no);
-      return p.backward ? go(w8, no, yes) : go(w8, no, no);
-    }
-    if (p.dot) return p.backward ? go(w4, yes, yes) : go(w4, yes, no);
-    return p.backward ? go(w4, no, yes) : go(w4, no, no);
+    constexpr int KD = decltype(kd)::value, OD = decltype(od)::value;
+    hipLaunchKernelGGL((linear_scan_kernel<IN, KD, OD>), dim3(scan_grid(b)),
+                       dim3(ScanCfgOf<IN, KD, OD, false>::THREADS), 0, stream, b, p);
+    return hipGetLastError();
   });
 }
 
 hipError_t launch_linear_grads(const LinearBatch& b, const LinearPass& pq, const LinearPass& pv,
                                const LinearPass& pk, hipStream_t stream) {
-  if (pq.kd != pv.kd || !pq.dot || !pv.dot) {
-    hipError_t e = launch_linear_pass(b, pq, stream);
-    if (e == hipSuccess) e = launch_linear_pass(b, pv, stream);
-    if (e == hipSuccess) e = launch_linear_pass(b, pk, stream);
-    return e;
-  }
-  return by_type(b.in_dtype, pq.kd, [&](auto in, auto kd) {
+  return by_type(b.in_dtype, pv.kd, pv.od, [&](auto in, auto dk, auto dv) {
     constexpr Dt IN = decltype(in)::value;
-    constexpr int KD = decltype(kd)::value, W = KD / 16;
-    constexpr int THREADS = ScanCfg<IN, KD, W, 3, true, score_waves<W>()>::THREADS;
-    hipLaunchKernelGGL((linear_grad_kernel<IN, KD, W>), dim3(scan_grid(b, 1), 3), dim3(THREADS), 0,
-                       stream, b, pq, pv, pk);
+    constexpr int DK = decltype(dk)::value, DV = decltype(dv)::value;
+    const dim3 grid(scan_grid(b), 3);
+    if (pq.dot)
+      hipLaunchKernelGGL((linear_grad_kernel<IN, DK, DV, true>), grid,
+                         dim3(GradCfg<IN, DK, DV, true>::THREADS), 0, stream, b, pq, pv, pk);
+    else
+      hipLaunchKernelGGL((linear_grad_kernel<IN, DK, DV, false>), grid,
+                         dim3(GradCfg<IN, DK, DV, false>::THREADS), 0, stream, b, pq, pv, pk);
     return hipGetLastError();
   });
 }
@@ -1389,16 +1395,12 @@ hipError_t launch_linear_starts(const LinearBatch& b, int od, int kd, const Line
                                 const LinearStates* backward, hipStream_t stream) {
   const int ways = backward ? 2 : 1;
   const LinearStates& back = backward ? *backward : forward;
-  const hipError_t e = by_type(b.in_dtype, kd, [&](auto in, auto kdim) {
+  const hipError_t e = by_type(b.in_dtype, kd, od, [&](auto in, auto kdim, auto odim) {
     constexpr Dt IN = decltype(in)::value;
-    constexpr int KD = decltype(kdim)::value;
-    auto go = [&](auto w_) {
-      constexpr int W = decltype(w_)::value;
-      hipLaunchKernelGGL((linear_local_kernel<IN, KD, W>), dim3(scan_grid(b, od / (16 * W)), ways),
-                         dim3(LocalCfg<IN, KD, W>::THREADS), 0, stream, b, forward, back, od);
-      return hipGetLastError();
-    };
-    return od == 128 ? go(std::integral_constant<int, 8>()) : go(std::integral_constant<int, 4>());
+    constexpr int KD = decltype(kdim)::value, W = decltype(odim)::value / 16;
+    hipLaunchKernelGGL((linear_local_kernel<IN, KD, W>), dim3(scan_grid(b), ways),
+                       dim3(LocalCfg<IN, KD, W>::THREADS), 0, stream, b, forward, back);
+    return hipGetLastError();
   });
   if (e != hipSuccess) return e;
   const int per = od * kd;
@@ -1407,12 +1409,11 @@ hipError_t launch_linear_starts(const LinearBatch& b, int od, int kd, const Line
   return hipGetLastError();
 }
 
-hipError_t launch_linear_dg(const LinearBatch& b, const float* row, int row_parts,
-                            const float* col, int col_parts, const float* start_dot,
-                            int start_parts, const float* end_dot, int end_parts, float* dg,
-                            double* unit_sum, hipStream_t stream) {
-  hipLaunchKernelGGL(linear_dg_kernel, dim3(b.units * b.H), dim3(256), 0, stream, b, row, row_parts,
-                     col, col_parts, start_dot, start_parts, end_dot, end_parts, dg, unit_sum);
+hipError_t launch_linear_dg(const LinearBatch& b, const float* row, const float* col,
+                            const float* start_dot, int start_parts, const float* end_dot,
+                            int end_parts, float* dg, double* unit_sum, hipStream_t stream) {
+  hipLaunchKernelGGL(linear_dg_kernel, dim3(b.units * b.H), dim3(256), 0, stream, b, row, col, start_dot,
+                     start_parts, end_dot, end_parts, dg, unit_sum);
   return hipGetLastError();
 }
 

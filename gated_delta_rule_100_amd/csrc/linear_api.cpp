@@ -73,14 +73,15 @@ gdr_status hip_fail(hipError_t e, const char* who, const char* what) {
 }
 
 // Tokens of a segment, or 0 to walk whole sequences.  A scan workgroup takes a
-// compute unit for one (unit, head), about 3.7 us a chunk of 64 tokens with all
-// of them at work, so segments are as long as 256 workgroups allow: fewer
-// states to form and pass on (4 x 4096 tokens, 16 heads: 115 us of scan, segment
-// states and chain at 1024 tokens, 137 at 512 and 168 at 2048; 131072 tokens, 4
-// heads: 220 at 2048, 246 at 1024; 8 sequences of 32768 tokens, 32 heads: 468 at
-// 4096, 505 at 2048).  The states cost three launches, so a sequence has to be
-// some chunks longer than a segment before that pays; the host knows only the
-// average length, and takes four times it for the longest one.
+// compute unit for one (unit, head), about 3.9 us a chunk of 64 tokens (bf16, 128 x
+// 128) with all of them at work, so segments are as long as 256 workgroups allow:
+// fewer states to form and pass on (4 x 4096 tokens, 16 heads: 115 us of scan,
+// segment states and chain at 1024 tokens, 137 at 512 and 168 at 2048; 131072
+// tokens, 4 heads: 220 at 2048, 246 at 1024).  The states cost two launches, so a
+// sequence has to be some chunks longer than a segment before that pays (gradient
+// of one sequence, 128 x 128, bf16 / fp32: 800 tokens, 4 heads 42 / 53 us in
+// segments, 66 / 156 without; 800 tokens, 16 heads 73 / 102 and 71 / 162); the host
+// knows only the average length, and takes four times it for the longest one.
 int segment_tokens(int T_total, int N, int H, bool gradient) {
   const int64_t th = static_cast<int64_t>(T_total) * H;
   const int64_t seg = (th + 256 * 64 - 1) / (256 * 64) * 64;
@@ -128,8 +129,7 @@ BackwardSizes backward_sizes(int T_total, int N, int H, int Hk, int dk, int dv) 
   const size_t th = static_cast<size_t>(T_total) * H * sizeof(float);
   const size_t pairs = static_cast<size_t>(z.seg.units) * H;
   if (H != Hk) z.part_q = z.part_k = align_up(th * dk);
-  z.row = align_up(th * gdr::linear_parts(dk));
-  z.col = align_up(th * gdr::linear_parts(dv));
+  z.row = z.col = align_up(th);
   z.start = align_up(pairs * (dv / 16) * sizeof(float));
   z.end = align_up(pairs * (dk / 16) * sizeof(float));
   z.sums = align_up(pairs * sizeof(double));
@@ -234,7 +234,7 @@ gdr_status gdr_linear_prefill(const void* q, const void* k, const void* v, const
     if (e != hipSuccess) return hip_fail(e, who, "segment states");
     p.start = states;
   }
-  return hip_fail(gdr::launch_linear_pass(b, p, st), who, "scan");
+  return hip_fail(gdr::launch_linear_prompt(b, p, st), who, "scan");
 }
 
 size_t gdr_linear_backward_workspace_bytes(int T_total, int N, int H, int Hk, int dk, int dv,
@@ -338,9 +338,9 @@ gdr_status gdr_linear_backward(const void* q, const void* k, const void* v, cons
   }
   if (dg) {
     const bool heads = decay == GDR_DECAY_HEAD;
-    e = gdr::launch_linear_dg(b, row, gdr::linear_parts(dk), col, gdr::linear_parts(dv),
-                              from ? start : nullptr, dv / 16, behind ? end : nullptr, dk / 16,
-                              heads ? nullptr : dg, heads ? sums : nullptr, st);
+    e = gdr::launch_linear_dg(b, row, col, from ? start : nullptr, dv / 16,
+                              behind ? end : nullptr, dk / 16, heads ? nullptr : dg,
+                              heads ? sums : nullptr, st);
     if (e == hipSuccess && heads) e = gdr::launch_linear_dg_heads(b, sums, dg, st);
     if (e != hipSuccess) return hip_fail(e, who, "gate gradient");
   }

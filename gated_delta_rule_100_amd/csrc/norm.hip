@@ -8,6 +8,11 @@
 // runs a fixed number of workgroups over the rows, so that each thread keeps
 // the weight gradients of its columns in registers; one workgroup's sums go to
 // the workspace and a second kernel adds them in order.
+//
+// TPR and E: eight consecutive elements a thread (16-byte accesses of bf16) as
+// long as a row then fits 64 threads, sixteen up to 1024 values, so that its sums
+// need no barrier; longer rows take 256 threads up to 4096 values and 1024 beyond,
+// where a wave's registers would not hold the row.
 #include <type_traits>
 
 #include "gdr_device.h"
@@ -160,6 +165,8 @@ __device__ __forceinline__ void widen(const RawRow<IN, E>& r, float (&x)[E]) {
   }
 }
 
+// 262144 rows of 128, bf16, gate: 42.7 us, 4.7 TB/s (a copy of this size reaches
+// 5.1); 64 rows of 2048 with both norms: 9 us, a launch.
 template <Dt IN, int TPR, int E, int NR, bool vec>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_kernel(BlockNorm p) {
   constexpr int THREADS = TPR > 256 ? TPR : 256, RPB = THREADS / TPR;
@@ -215,8 +222,17 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_kernel(Block
   }
 }
 
+// Eight streams of rows (x, gate, residual, dh, dy; dx, dgate, dresidual): 16384
+// rows of 2048, bf16, 147 us with the sum of the weights' gradients, 3.7 TB/s.  The
+// next row's reads are in flight while one is computed (without: 258 us), and
+// stores go past the caches, whose lines the reads want (through them: 155 us; the
+// forward kernel, one pass and one or two stores, is 2% faster through them).
+// Four waves a SIMD are asked for where the registers allow it.  Rows of more than
+// 8192 values spill registers: right, but slower.
 template <Dt IN, int TPR, int E, bool vec>
-__global__ __launch_bounds__(TPR > 256 ? TPR : 256, IN == Dt::BF16 && TPR <= 256 && E == 8 ? 4 : 1) void block_norm_backward_kernel(BlockNorm p) {
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256,
+                             IN == Dt::BF16 && TPR <= 256 && E == 8 ? 4 : 1)
+void block_norm_backward_kernel(BlockNorm p) {
   constexpr int THREADS = TPR > 256 ? TPR : 256, RPB = THREADS / TPR;
   __shared__ float lds[2][16];
   int slot = 0;
@@ -393,6 +409,8 @@ int rows_per_block(int D) { return D <= 64 ? 32 : D <= 128 ? 16 : D <= 256 ? 8 :
 
 }  // namespace
 
+// At most 1024, four on a compute unit: 16384 rows of 2048 take 150 us with 1024
+// workgroups, 152 with 768, 163 with 512 and 171 with 2048.
 int block_norm_backward_blocks(int64_t rows, int D) {
   const int64_t rpb = rows_per_block(D), n = (rows + rpb - 1) / rpb;
   return static_cast<int>(n < 1024 ? n : 1024);
@@ -420,7 +438,7 @@ hipError_t launch_block_norm(const BlockNorm& p, hipStream_t stream) {
     if constexpr (T <= 64 && E == 8) {
       const std::integral_constant<int, 2> two;
       // two rows a thread once one a thread would be more than 32 workgroups a
-      // compute unit
+      // compute unit (262144 rows of 128: 46.8 us with one, 42.7 with two)
       if (p.rows > 8192 * rpb) return p.in_dtype == 0 ? go(bf16, two) : go(f32, two);
     }
     return p.in_dtype == 0 ? go(bf16, one) : go(f32, one);
