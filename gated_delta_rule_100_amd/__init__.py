@@ -406,7 +406,9 @@ def _workspace(workspace, need, dev, stream):
         if stream is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         else:
-            with torch.cuda.stream(_stream_obj(stream)):
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=dev)
+            with torch.cuda.stream(stream):
                 workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     return _ptr(workspace, "workspace", (torch.uint8,), dev), workspace.numel(), workspace
 

@@ -2,7 +2,7 @@
 // and gradients in chunks of tokens on the matrix cores, single tokens as a
 // stream.
 //
-// A pass of the recurrence (launch.h, LinearPass) over one chunk, with G_t the
+// A pass of the recurrence (linear.h, LinearPass) over one chunk, with G_t the
 // prefix sums of the chunk's gates, C its last token and Z the state before it:
 //   out_t = os ( sum_{s <= t} e^{G_t - G_s} us (x_t . y_s) w_s + e^{G_t} Z x_t )
 //   Z    <- e^{G_C} Z + us sum_s e^{G_C - G_s} w_s y_s^T

@@ -312,6 +312,7 @@ gdr_status gdr_state_fixup(const float* L, const float* M, const float* state_in
  *     own chunk of 64 tokens non-finite as well as those after it; other
  *     sequences are not affected.
  *   - Every result is deterministic: no atomics.
+ *   - Calls that may run at the same time need workspaces of their own.
  */
 typedef enum { GDR_DECAY_TOKEN = 0, GDR_DECAY_HEAD = 1 } gdr_decay;
 
