@@ -354,14 +354,16 @@ __device__ __forceinline__ Gates chunk_gates(float gate, bool per_token, int lan
 // the decayed w that the state accumulates always as three (its full 24 bits).
 // fp32 inputs run on fp32 matrix instructions throughout.
 //
-// A chunk's matrix instructions (776 of 16 x 16 x 32 at 128 x 128, 16 cycles each on
-// one of four SIMDs) take 48% of its time, vector arithmetic about as much again:
-// the two do not overlap enough.  4 x 4096 tokens, 16 heads, bf16: 69 us for 16
-// chunks a workgroup after a prologue of 7.5 us, 110-115 us with the segments'
-// states and their chain (2.4 TB/s of q, k, v and o once).  Tried and not kept:
-// four compute waves of 32 rows each, which halve the LDS reads (119 us; the
-// gradient 381 against 343), matrix and vector instructions interleaved by
-// scheduling groups (123; 374-398), wave priorities (115; 345-354).
+// What bounds it is the chain of a step, read, multiply, barrier, read, multiply,
+// with two compute waves a SIMD to hide it: no unit is full (matrix instructions 48%
+// of a step, vector ones about as much, LDS 38%, memory 5 TB/s of q, k, v and o while
+// the steps run).  4 x 4096 tokens, 16 heads, bf16: 69 us for 16 chunks a workgroup
+// after a prologue of 7.5 us, 110-115 us with the segments' states and their chain
+// (2.4 TB/s of q, k, v and o once).  Tried and not kept: four compute waves of 32
+// rows each, which halve the LDS reads (119 us; the gradient 381 against 343); y
+// reads without their two-way bank conflicts, at twice the x reads (118; 350);
+// matrix and vector instructions interleaved by scheduling groups (123; 374-398);
+// wave priorities (115; 345-354).
 template <Dt IN, int KD, int W, int PZ, bool DOT, int SW>
 struct ScanCfg {
   static constexpr int ES = IN == Dt::BF16 ? 2 : 4;
@@ -878,7 +880,8 @@ void linear_scan_kernel(LinearBatch b, LinearPass p) {
 // The three passes of a gradient (dq, dv, dk) in one launch: their workgroups follow
 // each other without the gaps of launches, and run side by side where one pass does
 // not fill the GPU (6 fp32 sequences of up to 777 tokens, 8 heads, 64 x 128: 85 us
-// in three launches, 73 in one).
+// in three launches, 73 in one).  One pass after the other: the three of a unit side
+// by side, to share their rows in the caches, take 2% longer.
 template <Dt IN, int DK, int DV, bool DOT>
 struct GradCfg {
   using K = ScanCfgOf<IN, DV, DK, DOT>;  // dq and dk
