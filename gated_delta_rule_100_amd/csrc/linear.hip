@@ -135,7 +135,8 @@ __device__ __forceinline__ bool unit_at(const LinearBatch& b, int u, Unit& r) {
 // (lane (c, g) = (lane % 16, lane / 16)): one bf16x8 for bf16 inputs, eight
 // floats for fp32 ones, multiplied by one 16x16x32 bf16 product or eight
 // 16x16x4 fp32 products.  fp32 values beside bf16 inputs (P, the state, the
-// decayed w) are PL bf16 planes.
+// decayed w) are three bf16 planes.
+constexpr int kPlanes = 3;
 struct F32x8 {
   float v[8];
 };
@@ -146,9 +147,9 @@ struct FragOf<Dt::F32> { using type = F32x8; };
 template <Dt IN>
 using Frag = typename FragOf<IN>::type;
 
-template <Dt IN, int PL>
+template <Dt IN>
 struct Planes {
-  static constexpr int N = IN == Dt::F32 ? 1 : PL;
+  static constexpr int N = IN == Dt::F32 ? 1 : kPlanes;
   Frag<IN> p[N];
 };
 
@@ -160,27 +161,14 @@ __device__ __forceinline__ floatx4 mma(const F32x8& a, const F32x8& b, floatx4 a
   for (int i = 0; i < 8; ++i) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[i], b.v[i], acc, 0, 0, 0);
   return acc;
 }
-// Products of a planes operand, smallest plane first.
-template <Dt IN, int PL>
-__device__ __forceinline__ floatx4 mma(const Planes<IN, PL>& a, const Frag<IN>& b, floatx4 acc) {
-#pragma unroll
-  for (int i = Planes<IN, PL>::N - 1; i >= 0; --i) acc = mma(a.p[i], b, acc);
-  return acc;
-}
-template <Dt IN, int PL>
-__device__ __forceinline__ floatx4 mma(const Frag<IN>& a, const Planes<IN, PL>& b, floatx4 acc) {
-#pragma unroll
-  for (int i = Planes<IN, PL>::N - 1; i >= 0; --i) acc = mma(a, b.p[i], acc);
-  return acc;
-}
-template <Dt IN, int PL>
-__device__ __forceinline__ Planes<IN, PL> to_planes(const float (&x)[8]) {
-  Planes<IN, PL> r;
+template <Dt IN>
+__device__ __forceinline__ Planes<IN> to_planes(const float (&x)[8]) {
+  Planes<IN> r;
   if constexpr (IN == Dt::F32) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) r.p[0].v[i] = x[i];
   } else {
-    split8<PL>(x, r.p);
+    split8<kPlanes>(x, r.p);
   }
   return r;
 }
@@ -348,10 +336,12 @@ __device__ __forceinline__ Gates chunk_gates(float gate, bool per_token, int lan
 // waves' writing P^T for the next chunk (right after the former, while the
 // compute waves form Z x).
 //
-// Numerics beside bf16 inputs: the state stays fp32 in registers; Z and P enter
-// the products as two bf16 planes (2^-18 of a term, against 2^-9 of a bf16
-// output), three where the outputs also feed dg, whose sums run over a segment;
-// the decayed w that the state accumulates always as three (its full 24 bits).
+// Numerics beside bf16 inputs: the state stays fp32 in registers; Z, P and the
+// decayed w enter the products as three bf16 planes, their full 24 bits, whatever
+// the outputs' type and whether dg is wanted.  (Two planes of Z and P leave an
+// error of 2.5e-6, three 1.9e-7, fp32's own, which the sums of dg and of shared
+// heads and fp32 outputs need.  Two would take 3% less of 4 x 4096 tokens, 115
+// against 119 us, and 9% less of 32768 packed tokens, 361 against 398.)
 // fp32 inputs run on fp32 matrix instructions throughout.
 //
 // What bounds it is the chain of a step, read, multiply, barrier, read, multiply,
@@ -364,7 +354,7 @@ __device__ __forceinline__ Gates chunk_gates(float gate, bool per_token, int lan
 // reads without their two-way bank conflicts, at twice the x reads (118; 350);
 // matrix and vector instructions interleaved by scheduling groups (123; 374-398);
 // wave priorities (115; 345-354).
-template <Dt IN, int KD, int W, int PZ, bool DOT, int SW>
+template <Dt IN, int KD, int W, bool DOT, int SW>
 struct ScanCfg {
   static constexpr int ES = IN == Dt::BF16 ? 2 : 4;
   static constexpr int C = IN == Dt::BF16 ? 64 : 32;  // tokens a chunk (fp32: half, for LDS)
@@ -383,7 +373,7 @@ struct ScanCfg {
   static constexpr int OFF_G = OFF_W + 2 * W_BYTES;
   // P^T fragments (row tile, 32-deep block) on the walked side of the diagonal,
   // PL planes each, and the scores of a token with itself
-  static constexpr int PL = IN == Dt::F32 ? 1 : PZ;
+  static constexpr int PL = Planes<IN>::N;
   static constexpr int FRAG = IN == Dt::BF16 ? 1024 : 2048;
   static constexpr int FRAGS = NB == 2 ? 6 : 2;
   static constexpr int P_BYTES = FRAGS * PL * FRAG;
@@ -420,8 +410,7 @@ __device__ __forceinline__ void store_state4(float* p, int64_t col, const floatx
 template <Dt IN, int KD, int W, bool DOT, bool BACK, int SW>
 __device__ __forceinline__ void scan_pass(const LinearBatch& b, const LinearPass& p,
                                           unsigned char* lds) {
-  constexpr int PZ = DOT ? 3 : 2;
-  using Cfg = ScanCfg<IN, KD, W, PZ, DOT, SW>;
+  using Cfg = ScanCfg<IN, KD, W, DOT, SW>;
   constexpr int CW = Cfg::CW;
   constexpr int C = Cfg::C, NT = Cfg::NT, NB = Cfg::NB, KB = Cfg::KB, ES = Cfg::ES, PL = Cfg::PL;
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
@@ -729,7 +718,7 @@ __device__ __forceinline__ void scan_pass(const LinearBatch& b, const LinearPass
       }
       const float zz[8] = {z[2 * kb][0], z[2 * kb][1], z[2 * kb][2], z[2 * kb][3],
                            z[2 * kb + 1][0], z[2 * kb + 1][1], z[2 * kb + 1][2], z[2 * kb + 1][3]};
-      const Planes<IN, PZ> zp = to_planes<IN, PZ>(zz);
+      const Planes<IN> zp = to_planes<IN>(zz);
 #pragma unroll
       for (int q = PL - 1; q >= 0; --q)
 #pragma unroll
@@ -746,7 +735,7 @@ __device__ __forceinline__ void scan_pass(const LinearBatch& b, const LinearPass
     // + w^T P^T
 #pragma unroll
     for (int sb = 0; sb < NB; ++sb) {
-      Planes<IN, PZ> pf[NT];
+      Planes<IN> pf[NT];
 #pragma unroll
       for (int tt = 0; tt < NT; ++tt) {
         if (BACK ? sb < (tt >> 1) : sb > (tt >> 1)) continue;
@@ -791,12 +780,12 @@ __device__ __forceinline__ void scan_pass(const LinearBatch& b, const LinearPass
         u[e] = frag_value(wf[sb], e) * f0[e];
         u[4 + e] = frag_value(wf[sb], 4 + e) * f1[e];
       }
-      const Planes<IN, 3> up = to_planes<IN, 3>(u);
+      const Planes<IN> up = to_planes<IN>(u);
 #pragma unroll
       for (int jb = 0; jb < KD / 32; ++jb) {
         if (jb + 1 < KD / 32) read_y(jb + 1, yf[(jb + 1) & 1]);
 #pragma unroll
-        for (int q = Planes<IN, 3>::N - 1; q >= 0; --q)
+        for (int q = Planes<IN>::N - 1; q >= 0; --q)
 #pragma unroll
           for (int i = 0; i < 2; ++i) z[2 * jb + i] = mma(yf[jb & 1][i], up.p[q], z[2 * jb + i]);
       }
@@ -868,7 +857,7 @@ template <int W>
 constexpr int score_waves() { return W == 8 ? 3 : 4; }
 
 template <Dt IN, int KD, int OD, bool DOT>
-using ScanCfgOf = ScanCfg<IN, KD, OD / 16, DOT ? 3 : 2, DOT, score_waves<OD / 16>()>;
+using ScanCfgOf = ScanCfg<IN, KD, OD / 16, DOT, score_waves<OD / 16>()>;
 
 template <Dt IN, int KD, int OD>
 __global__ __launch_bounds__((ScanCfgOf<IN, KD, OD, false>::THREADS))
@@ -1063,7 +1052,7 @@ __device__ __forceinline__ void local_states(const LinearBatch& b, const LinearS
         u[e] = frag_value(wf, e) * f0[e];
         u[4 + e] = frag_value(wf, 4 + e) * f1[e];
       }
-      const Planes<IN, 3> up = to_planes<IN, 3>(u);
+      const Planes<IN> up = to_planes<IN>(u);
 #pragma unroll
       for (int j0 = 0; j0 < KD / 16; j0 += 4) {
         Frag<IN> yf[4];
@@ -1071,7 +1060,7 @@ __device__ __forceinline__ void local_states(const LinearBatch& b, const LinearS
         for (int j = 0; j < 4; ++j)
           yf[j] = col_frag_wide<IN, Cfg::CHK>(Y, 32 * sb, (j0 + j) >> 1, j & 1, c, g, jl[(j0 + j) >> 1]);
 #pragma unroll
-        for (int q = Planes<IN, 3>::N - 1; q >= 0; --q)
+        for (int q = Planes<IN>::N - 1; q >= 0; --q)
 #pragma unroll
           for (int j = 0; j < 4; ++j) z[j0 + j] = mma(yf[j], up.p[q], z[j0 + j]);
       }
