@@ -585,8 +585,7 @@ __device__ __forceinline__ void scan_pass(const LinearBatch& b, const LinearPass
         tts[i] = NT - 1 - tts[i];
         sts[i] = NT - 1 - sts[i];
       }
-    // the scale goes into the exponent: log2 of its size, and its sign
-    const float ps = p.us * p.os, ps2 = __builtin_amdgcn_logf(fabsf(ps));
+    const float ps = p.us * p.os;
     int kl[KB];
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) kl[kb] = row_lane<Cfg::CHK>(c, g, kb);
@@ -611,13 +610,15 @@ __device__ __forceinline__ void scan_pass(const LinearBatch& b, const LinearPass
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         const int t = 16 * tts[i] + c, s4 = 16 * sts[i] + 4 * g;
-        const float gh = gate[t], gl = BACK ? gate[C + t] - ps2 : gate[C + t] + ps2;
+        const float gh = gate[t], gl = gate[C + t];
         const floatx4 sh = *reinterpret_cast<const floatx4*>(gate + s4);
         const floatx4 sl = *reinterpret_cast<const floatx4*>(gate + C + s4);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float d = (gh - sh[e]) + (gl - sl[e]);
-          const float x = (ps < 0.f ? -acc[i][e] : acc[i][e]) * __builtin_amdgcn_exp2f(BACK ? -d : d);
+          // (the scale as a factor: as log2 of it in the exponent it would be off by up
+          // to |log2 scale| 2^-24 in every score)
+          const float x = acc[i][e] * (ps * __builtin_amdgcn_exp2f(BACK ? -d : d));
           const int sc = s4 + e;
           if (DOT && sc == t) own[i] = x;
           const bool in = BACK ? (DOT ? sc > t : sc >= t) && sc < len : (DOT ? sc < t : sc <= t);

@@ -32,3 +32,13 @@ def check_outputs(d):
 def test_fp32_outputs_hold_fp32(dtype, dk, dv, H, Hk):
     say(f"fp32 outputs of {dtype} inputs {dk}x{dv} H{H}/{Hk}")
     check_outputs(ref.make([300, 130, 65], H, Hk, dk, dv, dtype, "token", "slow", True, seed=38))
+
+
+@pytest.mark.parametrize("scale", [1e-20, -1e12])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_scales_far_from_one(scale, dtype):
+    """From zero states every value comes from the scores, so that their scale shows."""
+    say(f"scale {scale} of {dtype} inputs")
+    d = ref.make([64, 300, 7], 4, 2, 128, 128, dtype, "token", "slow", False, seed=39)
+    d["scale"] = scale
+    check_outputs(d)
