@@ -128,6 +128,17 @@ __device__ __forceinline__ float sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));
 }
 
+// s = sigmoid(z) and 1 - s = sigmoid(-z), both from e^-|z|: 1 - s of a rounded s
+// loses the slope of open gates (6% of it at z = 16, all from 17.4 on).
+struct Sigmoid {
+  float s, rest;
+};
+__device__ __forceinline__ Sigmoid sigmoid_and_rest(float z) {
+  const float a = __builtin_amdgcn_exp2f(-1.4426950408889634f * fabsf(z));
+  const float r = __builtin_amdgcn_rcpf(1.f + a), b = a * r;
+  return z < 0.f ? Sigmoid{b, r} : Sigmoid{r, b};
+}
+
 // A row's operands as loaded, for 16-byte accesses: the next row's are read while
 // one is computed.
 template <Dt IN, int E>
@@ -312,9 +323,9 @@ void block_norm_backward_kernel(BlockNorm p) {
 #pragma unroll
       for (int i = 0; i < E; ++i) {
         const float n = p.w_after ? x[i] * ix * wa[i] : x[i];
-        const float s = sigmoid(z[i]);
-        const float slope = p.act == 0 ? s * fmaf(z[i], 1.f - s, 1.f) : s * (1.f - s);
-        const float a = p.act == 0 ? s * z[i] : s;
+        const Sigmoid g = sigmoid_and_rest(z[i]);
+        const float slope = g.s * (p.act == 0 ? fmaf(z[i], g.rest, 1.f) : g.rest);
+        const float a = p.act == 0 ? g.s * z[i] : g.s;
         z[i] = d[i] * n * slope;
         d[i] *= a;
       }
