@@ -596,16 +596,21 @@ def _nothing():
 
 def _norm_after(o, norm, stream):
     """The call of gdr_block_norm on o that `norm` asks for, its arguments checked
-    now: by the library too, in a call for no rows, which launches nothing."""
+    now: by the library too, in a call for no rows, which launches nothing, and the
+    number of rows by the size of the gradient's workspace, 0 for rows that no norm
+    takes."""
     if norm is None:
         return _nothing
-    who, fn = "gdr_block_norm", _load().gdr_block_norm
+    who, lib = "gdr_block_norm", _load()
+    fn = lib.gdr_block_norm
     dev, ptrs, rows, tail = _norm_call(o, **norm)
     if norm.get("h") is None and norm.get("y") is None:
         raise GdrError(f"{who}: h or y is required")
     if (norm.get("y") is None) != (norm.get("w_before") is None):
         raise GdrError(f"{who}: y is given exactly when w_before is")
     _launch(who, fn, dev, stream, *ptrs, 0, *tail)
+    if rows and not lib.gdr_block_norm_backward_workspace_bytes(rows, tail[0]):
+        raise GdrError(f"{who}: rows={rows}")
     return lambda: _launch(who, fn, dev, stream, *ptrs, rows, *tail)
 
 
