@@ -150,15 +150,6 @@ def _code(dt: torch.dtype) -> int:
     raise GdrError(f"unsupported dtype {dt}")
 
 
-def _stream_obj(stream):
-    """The launch stream as a torch stream (a raw hipStream_t handle is wrapped)."""
-    if stream is None:
-        return torch.cuda.current_stream()
-    if isinstance(stream, torch.cuda.Stream):
-        return stream
-    return torch.cuda.ExternalStream(int(stream))
-
-
 def _stream(stream):
     if stream is None:
         return torch.cuda.current_stream().cuda_stream
@@ -186,12 +177,12 @@ def gdr_decode_step(q, k, v, g, beta, state, o, stream=None, *, norm=None) -> No
         raise GdrError("gdr_decode_step: inconsistent shapes")
     if k.dtype != q.dtype or v.dtype != q.dtype:
         raise GdrError("gdr_decode_step: q, k, v must share a dtype")
-    after = _norm_after(o, norm, stream)
-    st = _load().gdr_decode_step(
-        _dev_ptr(q, "q", _IO), _dev_ptr(k, "k", _IO), _dev_ptr(v, "v", _IO),
-        _dev_ptr(g, "g", _F32), _dev_ptr(beta, "beta", _F32), _dev_ptr(state, "state", _F32),
-        _dev_ptr(o, "o", _IO), N, H, dk, dv, _code(q.dtype), _code(o.dtype), _stream(stream))
-    _check(st, "gdr_decode_step")
+    dev = _device(q, "q")
+    after = _norm_after(o, norm, dev, stream)
+    _launch("gdr_decode_step", _load().gdr_decode_step, dev, stream,
+            _dev_ptr(q, "q", _IO), _dev_ptr(k, "k", _IO), _dev_ptr(v, "v", _IO),
+            _dev_ptr(g, "g", _F32), _dev_ptr(beta, "beta", _F32), _dev_ptr(state, "state", _F32),
+            _dev_ptr(o, "o", _IO), N, H, dk, dv, _code(q.dtype), _code(o.dtype))
     after()
 
 
@@ -212,14 +203,15 @@ def gdr_decode_mtp(q, k, v, g, beta, state_in, state_out, o, inter=None, stream=
         raise GdrError("gdr_decode_mtp: inconsistent shapes")
     if k.dtype != q.dtype or v.dtype != q.dtype:
         raise GdrError("gdr_decode_mtp: q, k, v must share a dtype")
-    after = _norm_after(o, norm, stream)
-    st = _load().gdr_decode_mtp(
-        _dev_ptr(q, "q", _IO), _dev_ptr(k, "k", _IO), _dev_ptr(v, "v", _IO),
-        _dev_ptr(g, "g", _F32), _dev_ptr(beta, "beta", _F32),
-        _dev_ptr(state_in, "state_in", _F32), _dev_ptr(state_out, "state_out", _F32, optional=True),
-        _dev_ptr(o, "o", _IO), _dev_ptr(inter, "inter", _F32, optional=True), N, T, H, dk, dv,
-        _code(q.dtype), _code(o.dtype), _stream(stream))
-    _check(st, "gdr_decode_mtp")
+    dev = _device(q, "q")
+    after = _norm_after(o, norm, dev, stream)
+    _launch("gdr_decode_mtp", _load().gdr_decode_mtp, dev, stream,
+            _dev_ptr(q, "q", _IO), _dev_ptr(k, "k", _IO), _dev_ptr(v, "v", _IO),
+            _dev_ptr(g, "g", _F32), _dev_ptr(beta, "beta", _F32),
+            _dev_ptr(state_in, "state_in", _F32),
+            _dev_ptr(state_out, "state_out", _F32, optional=True),
+            _dev_ptr(o, "o", _IO), _dev_ptr(inter, "inter", _F32, optional=True), N, T, H, dk, dv,
+            _code(q.dtype), _code(o.dtype))
     after()
 
 
@@ -293,15 +285,13 @@ def gdr_chunk_prefill(q, k, v, g, beta, cu_seqlens, state_in, state_out, o, *, c
     gdr_decode_step's."""
     args, (T, N, H, dk, dv) = _prefill_args(q, k, v, g, beta, cu_seqlens, state_in, state_out, o,
                                             chunk, L_out, M_out, fixed_out, "gdr_chunk_prefill")
-    after = _norm_after(o, norm, stream)
+    dev = _device(q, "q")
+    after = _norm_after(o, norm, dev, stream)
     if workspace is None:
         need = gdr_chunk_prefill_workspace_bytes(T, N, H, dk, dv, chunk, q.dtype)
-        with torch.cuda.stream(_stream_obj(stream)):
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
-    st = _load().gdr_chunk_prefill(
-        *args, _dev_ptr(workspace, "workspace", (torch.uint8,)), workspace.numel(),
-        _stream(stream))
-    _check(st, "gdr_chunk_prefill")
+        _, _, workspace = _workspace(None, max(need, 1), dev, stream)
+    _launch("gdr_chunk_prefill", _load().gdr_chunk_prefill, dev, stream, *args,
+            _dev_ptr(workspace, "workspace", (torch.uint8,)), workspace.numel())
     after()
 
 
@@ -315,9 +305,9 @@ def gdr_chunk_prefill_noalloc(q, k, v, g, beta, cu_seqlens, state_in, state_out,
     overlap on one device share the scratch and race."""
     args, _ = _prefill_args(q, k, v, g, beta, cu_seqlens, state_in, state_out, o, chunk, L_out,
                             M_out, fixed_out, "gdr_chunk_prefill_noalloc")
-    after = _norm_after(o, norm, stream)
-    st = _load().gdr_chunk_prefill_noalloc(*args, _stream(stream))
-    _check(st, "gdr_chunk_prefill_noalloc")
+    dev = _device(q, "q")
+    after = _norm_after(o, norm, dev, stream)
+    _launch("gdr_chunk_prefill_noalloc", _load().gdr_chunk_prefill_noalloc, dev, stream, *args)
     after()
 
 
@@ -338,9 +328,8 @@ def gdr_state_fixup(L, M, state_in, chunk_offsets, fixed, stream=None) -> None:
     _check(st, "gdr_state_fixup")
 
 
-# The binding below is on the path of single tokens, where a call costs about as
-# much on the host as on the GPU: the current stream is read as a raw handle and
-# the device is switched only when it has to be.
+# A single token's call costs about as much on the host as on the GPU: the current
+# stream is read as a raw handle and the device is switched only when it has to be.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
@@ -449,7 +438,7 @@ def gdr_linear_decode(q, k, v, g, state, o, *, scale=1.0, stream=None, norm=None
     kp, ks = _rows_ptr(k, "k", dev)
     vp, vs = _rows_ptr(v, "v", dev)
     gp, decay = _gates(g, N, H, dev, who)
-    after = _norm_after(o, norm, stream)
+    after = _norm_after(o, norm, dev, stream)
     _launch(who, _load().gdr_linear_decode, dev, stream, qp, kp, vp, gp,
             _ptr(state, "state", _F32, dev), _ptr(o, "o", _IO, dev), N, H, Hk, dk, dv, qs, ks, vs,
             scale, decay, _code(q.dtype), _code(o.dtype))
@@ -507,7 +496,7 @@ def gdr_linear_prefill(q, k, v, g, cu_seqlens, state_in, state_out, o, *, scale=
                                                                     state_in, (o,))
     if state_out is not None and state_out.shape != (N, H, dv, dk):
         raise GdrError(f"{who}: state_out must have shape {(N, H, dv, dk)}")
-    after = _norm_after(o, norm, stream)
+    after = _norm_after(o, norm, dev, stream)
     code, lib = _code(q.dtype), _load()
     wp, wb, workspace = _workspace(
         workspace, lib.gdr_linear_prefill_workspace_bytes(T, N, H, dk, dv, code), dev, stream)
@@ -594,16 +583,18 @@ def _nothing():
     pass
 
 
-def _norm_after(o, norm, stream):
-    """The call of gdr_block_norm on o that `norm` asks for, its arguments checked
-    now: by the library too, in a call for no rows, which launches nothing, and the
+def _norm_after(o, norm, dev, stream):
+    """The call of gdr_block_norm on o that `norm` asks for, on the stream of the
+    recurrence's launch on GPU `dev`, its arguments checked now: by the library too, in a call for no rows, which launches nothing, and the
     number of rows by the size of the gradient's workspace, 0 for rows that no norm
     takes."""
     if norm is None:
         return _nothing
     who, lib = "gdr_block_norm", _load()
     fn = lib.gdr_block_norm
-    dev, ptrs, rows, tail = _norm_call(o, **norm)
+    at, ptrs, rows, tail = _norm_call(o, **norm)
+    if at != dev:
+        raise GdrError("o is on another device than the first tensor")
     if norm.get("h") is None and norm.get("y") is None:
         raise GdrError(f"{who}: h or y is required")
     if (norm.get("y") is None) != (norm.get("w_before") is None):

@@ -104,3 +104,16 @@ def test_rows_that_the_norm_refuses_are_refused_before_anything_runs(host, name)
     assert lib.launches == []
     call(g, name, 1 << 10, 16, {}, **ws)
     assert [n for n, _, _ in lib.launches] == [name, "gdr_block_norm"]
+
+
+@pytest.mark.parametrize("name", RECURRENCES)
+@pytest.mark.parametrize("stream", [None, 7])
+def test_the_norm_follows_its_recurrence_on_the_stream_of_their_device(host, name, stream):
+    """With everything on GPU 1 while GPU 0 is the current one."""
+    g, lib, home = host
+    home[0] = 1
+    ws = dict(workspace=meta(1, dtype=torch.uint8)) if name in ("gdr_chunk_prefill",
+                                                                "gdr_linear_prefill") else {}
+    call(g, name, 128, 4, {}, stream=stream, **ws)
+    on = 101 if stream is None else stream
+    assert lib.launches == [(name, 1, on), ("gdr_block_norm", 1, on)]
