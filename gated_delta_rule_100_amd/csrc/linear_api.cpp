@@ -264,6 +264,9 @@ gdr_status gdr_linear_backward(const void* q, const void* k, const void* v, cons
                               {q, k, v, g, state_in, d_o, dstate_out, dq, dk_out, dv_out, dg,
                                dstate_in, workspace});
   if (s != GDR_OK) return s;
+  // the sums over shared heads: one launch of a thread for four values
+  if (H != Hk && static_cast<int64_t>(T_total) * Hk * dk > (int64_t{1} << 34) - 1024)
+    return fail(GDR_ERR_INVALID_ARG, "%s: tokens*Hk*dk too large for shared heads", who);
   const BackwardSizes z = backward_sizes(T_total, N, H, Hk, dk, dv);
   if (workspace_bytes < z.total() || (!workspace && z.total() > 0))
     return fail(GDR_ERR_INVALID_ARG, "%s: workspace of %zu bytes, need %zu", who, workspace_bytes, z.total());

@@ -379,6 +379,7 @@ size_t gdr_linear_prefill_workspace_bytes(int T_total, int N, int H, int dk, int
  *                decay of zero: 0
  *   dstate_in    [N, H, dv, dk]     fp32, or NULL
  *   workspace    gdr_linear_backward_workspace_bytes(...) bytes
+ * Where heads are shared (H above Hk), T_total * Hk * dk is at most 2^34 - 1024.
  * No output may overlap an input or another output (dstate_in not dstate_out).
  */
 gdr_status gdr_linear_backward(const void* q, const void* k, const void* v, const float* g,
