@@ -176,61 +176,50 @@ __device__ __forceinline__ void widen(const RawRow<IN, E>& r, float (&x)[E]) {
   }
 }
 
-// 262144 rows of 128, bf16, gate: 42.7 us, 4.7 TB/s (a copy of this size reaches
-// 5.1); 64 rows of 2048 with both norms: 9 us, a launch.
-template <Dt IN, int TPR, int E, int NR, bool vec>
+// 262144 rows of 128, bf16, gate: 39.3 us, 5.1 TB/s, the rate of a copy of this size
+// (two rows a thread, loaded together: 43.7); 64 rows of 2048 with both norms: 9 us,
+// a launch.
+template <Dt IN, int TPR, int E, bool vec>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_kernel(BlockNorm p) {
   constexpr int THREADS = TPR > 256 ? TPR : 256, RPB = THREADS / TPR;
   __shared__ float lds[2][16];
   int slot = 0;
   const int t = threadIdx.x % TPR;
   const float inv_d = 1.f / static_cast<float>(p.D);
-  const size_t row0 = static_cast<size_t>(blockIdx.x) * RPB * NR + threadIdx.x / TPR;
-  // NR rows a thread, all of them loaded first (NR > 1 only where a row is inside
-  // one wave, so that no barrier is missed)
-  float x[NR][E], z[NR][E], r[NR][E];
-#pragma unroll
-  for (int n = 0; n < NR; ++n) {
-    const size_t row = row0 + n * RPB;
-    if (row >= static_cast<size_t>(p.rows)) continue;
-    load_row<IN, TPR, E>(p.x, row, p.D, t, vec, x[n]);
-    if (p.gate) load_row<IN, TPR, E>(p.gate, row, p.D, t, vec, z[n]);
-    if (p.residual) load_row<IN, TPR, E>(p.residual, row, p.D, t, vec, r[n]);
-  }
-  float wa[E], wb[E];
+  const size_t row = static_cast<size_t>(blockIdx.x) * RPB + threadIdx.x / TPR;
+  // (rows of several waves have a workgroup each: no barrier is missed)
+  if (row >= static_cast<size_t>(p.rows)) return;
+  float x[E], z[E], r[E], wa[E], wb[E];
+  load_row<IN, TPR, E>(p.x, row, p.D, t, vec, x);
+  if (p.gate) load_row<IN, TPR, E>(p.gate, row, p.D, t, vec, z);
+  if (p.residual) load_row<IN, TPR, E>(p.residual, row, p.D, t, vec, r);
   if (p.w_after) load_weight<TPR, E>(p.w_after, p.w_dtype, p.D, t, vec, wa);
   if (p.w_before) load_weight<TPR, E>(p.w_before, p.w_dtype, p.D, t, vec, wb);
+  if (p.w_after) {
+    float ss = 0.f;
 #pragma unroll
-  for (int n = 0; n < NR; ++n) {
-    const size_t row = row0 + n * RPB;
-    if (row >= static_cast<size_t>(p.rows)) continue;
-    if (p.w_after) {
-      float ss = 0.f;
+    for (int i = 0; i < E; ++i) ss = fmaf(x[i], x[i], ss);
+    const float inv = rsqrtf(row_sum<TPR>(ss, lds, slot) * inv_d + p.eps);
 #pragma unroll
-      for (int i = 0; i < E; ++i) ss = fmaf(x[n][i], x[n][i], ss);
-      const float inv = rsqrtf(row_sum<TPR>(ss, lds, slot) * inv_d + p.eps);
-#pragma unroll
-      for (int i = 0; i < E; ++i) x[n][i] = x[n][i] * inv * wa[i];
-    }
-    if (p.gate) {
-#pragma unroll
-      for (int i = 0; i < E; ++i) x[n][i] *= sigmoid(z[n][i]) * (p.act == 0 ? z[n][i] : 1.f);
-    }
-#pragma unroll
-    for (int i = 0; i < E; ++i)
-      x[n][i] = p.residual ? fmaf(p.scale, x[n][i], r[n][i]) : p.scale * x[n][i];
-    if (p.w_before) {
-      float y[E];
-      float ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < E; ++i) ss = fmaf(x[n][i], x[n][i], ss);
-      const float inv = rsqrtf(row_sum<TPR>(ss, lds, slot) * inv_d + p.eps);
-#pragma unroll
-      for (int i = 0; i < E; ++i) y[i] = x[n][i] * inv * wb[i];
-      store_row<TPR, E>(p.y, p.out_dtype, row, p.D, t, vec, y);
-    }
-    if (p.h) store_row<TPR, E>(p.h, p.out_dtype, row, p.D, t, vec, x[n]);
+    for (int i = 0; i < E; ++i) x[i] = x[i] * inv * wa[i];
   }
+  if (p.gate) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[i] *= sigmoid(z[i]) * (p.act == 0 ? z[i] : 1.f);
+  }
+#pragma unroll
+  for (int i = 0; i < E; ++i) x[i] = p.residual ? fmaf(p.scale, x[i], r[i]) : p.scale * x[i];
+  if (p.w_before) {
+    float y[E];
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) ss = fmaf(x[i], x[i], ss);
+    const float inv = rsqrtf(row_sum<TPR>(ss, lds, slot) * inv_d + p.eps);
+#pragma unroll
+    for (int i = 0; i < E; ++i) y[i] = x[i] * inv * wb[i];
+    store_row<TPR, E>(p.y, p.out_dtype, row, p.D, t, vec, y);
+  }
+  if (p.h) store_row<TPR, E>(p.h, p.out_dtype, row, p.D, t, vec, x);
 }
 
 // Eight streams of rows (x, gate, residual, dh, dy; dx, dgate, dresidual): 16384
@@ -446,28 +435,16 @@ hipError_t launch_block_norm(const BlockNorm& p, hipStream_t stream) {
   const int64_t rpb = rows_per_block(p.D);
   return by_width(p.D, [&](auto tpr, auto el) {
     constexpr int T = decltype(tpr)::value, E = decltype(el)::value;
-    auto go = [&](auto in, auto nr) {
-      constexpr int NR = decltype(nr)::value;
-      const dim3 grid(static_cast<unsigned>((p.rows + rpb * NR - 1) / (rpb * NR)));
-      const dim3 block(T > 256 ? T : 256);
-      if (p.D % 8 == 0)
-        hipLaunchKernelGGL((block_norm_kernel<decltype(in)::value, T, E, NR, true>), grid, block, 0,
-                           stream, p);
-      else
-        hipLaunchKernelGGL((block_norm_kernel<decltype(in)::value, T, E, NR, false>), grid, block, 0,
-                           stream, p);
+    auto go = [&](auto in, auto vec) {
+      hipLaunchKernelGGL((block_norm_kernel<decltype(in)::value, T, E, decltype(vec)::value>),
+                         dim3(static_cast<unsigned>((p.rows + rpb - 1) / rpb)), dim3(T > 256 ? T : 256),
+                         0, stream, p);
       return hipGetLastError();
     };
     const std::integral_constant<Dt, Dt::BF16> bf16;
     const std::integral_constant<Dt, Dt::F32> f32;
-    const std::integral_constant<int, 1> one;
-    if constexpr (T <= 64 && E == 8) {
-      const std::integral_constant<int, 2> two;
-      // two rows a thread once one a thread would be more than 32 workgroups a
-      // compute unit (262144 rows of 128: 46.8 us with one, 42.7 with two)
-      if (p.rows > 8192 * rpb) return p.in_dtype == 0 ? go(bf16, two) : go(f32, two);
-    }
-    return p.in_dtype == 0 ? go(bf16, one) : go(f32, one);
+    if (p.D % 8 == 0) return p.in_dtype == 0 ? go(bf16, std::true_type()) : go(f32, std::true_type());
+    return p.in_dtype == 0 ? go(bf16, std::false_type()) : go(f32, std::false_type());
   });
 }
 
