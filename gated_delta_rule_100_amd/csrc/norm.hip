@@ -223,16 +223,23 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_kernel(Block
 }
 
 // Eight streams of rows (x, gate, residual, dh, dy; dx, dgate, dresidual): 16384
-// rows of 2048, bf16, 136 us, 3.9 TB/s (8 us more with the sum of the weights'
-// gradients).  The
-// next row's reads are in flight while one is computed (without: 258 us), and
-// stores go past the caches, whose lines the reads want (through them 6% longer; the
-// forward kernel, one pass and one or two stores, is 2% faster through them).
-// Four waves a SIMD are asked for where the registers allow it.  Rows of more than
-// 8192 values spill registers: right, but slower.
+// rows of 2048, bf16, 138 us with the sum of the weights' gradients, 3.9 TB/s.  The
+// next row's reads are in flight while one is computed (when built: 258 us without,
+// 168 with), and stores go past the caches, whose lines the reads want (through them
+// 6% longer; the forward kernel, one pass and one or two stores, is 2% faster through
+// them).
+//
+// Every optional operand is a run-time branch, so that all of them have registers at
+// once.  bf16 rows of up to 512 values are asked to fit four waves a SIMD all the same
+// and spill 58 registers, most of them of operands that a call does not have: 262144
+// rows of 128 with norm and gate take 74 us, 83 without the request; 131072 rows with
+// all operands 66 us with it and without.  Rows of 256 threads are not asked to: they
+// would spill 23 (16384 rows of 2048, norm and gate: 95 us, 87 without).  Rows of more
+// than 8192 values, whose 1024 threads have 128 registers at most, spill 256 to 275:
+// right, but slower.
 template <Dt IN, int TPR, int E, bool vec>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256,
-                             IN == Dt::BF16 && TPR <= 256 && E == 8 ? 4 : 1)
+                             IN == Dt::BF16 && TPR <= 64 && E == 8 ? 4 : 1)
 void block_norm_backward_kernel(BlockNorm p) {
   constexpr int THREADS = TPR > 256 ? TPR : 256, RPB = THREADS / TPR;
   __shared__ float lds[2][16];
