@@ -223,11 +223,11 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_kernel(Block
 }
 
 // Eight streams of rows (x, gate, residual, dh, dy; dx, dgate, dresidual): 16384
-// rows of 2048, bf16, 138 us with the sum of the weights' gradients, 3.9 TB/s.  The
-// next row's reads are in flight while one is computed (when built: 258 us without,
-// 168 with), and stores go past the caches, whose lines the reads want (through them
-// 6% longer; the forward kernel, one pass and one or two stores, is 2% faster through
-// them).
+// rows of 2048, bf16, 112 us with the sum of the weights' gradients, 4.8 TB/s.  The
+// next row's reads are in flight while one is computed (205 us without), and stores go
+// past the caches, whose lines the reads want (114 through them, 76 against 72 at
+// 262144 x 128; fp32 rows of 2048 are the exception, 215 through them and 235 past them.
+// The forward kernel, one pass and one or two stores, is 2% faster through them).
 //
 // Every optional operand is a run-time branch, so that all of them have registers at
 // once.  bf16 rows of up to 512 values are asked to fit four waves a SIMD all the same
@@ -431,11 +431,16 @@ int rows_per_block(int D) { return D <= 64 ? 32 : D <= 128 ? 16 : D <= 256 ? 8 :
 
 }  // namespace
 
-// At most 1024, four on a compute unit: 16384 rows of 2048 take 150 us with 1024
-// workgroups, 152 with 768, 163 with 512 and 171 with 2048.
+// Workgroups of the gradient: as many as a compute unit's registers hold at once, four
+// of rows inside a wave (up to 1024 values), two of rows of 256 threads and one of rows
+// of 1024 threads.  262144 rows of 128, bf16, norm and gate: 72 us with 1024 workgroups,
+// 78 with 512, 74 with 2048.  All operands: 16384 rows of 2048 112 us with 512, 116 with
+// 768, 138 with 1024, 128 with 2048; 8192 rows of 4096 119 with 512, 132 with 768, 131
+// with 1024; 4096 rows of 8192 159 with 256, 205 with 1024.
 int block_norm_backward_blocks(int64_t rows, int D) {
   const int64_t rpb = rows_per_block(D), n = (rows + rpb - 1) / rpb;
-  return static_cast<int>(n < 1024 ? n : 1024);
+  const int64_t most = D <= 1024 ? 1024 : D <= 4096 ? 512 : 256;
+  return static_cast<int>(n < most ? n : most);
 }
 
 hipError_t launch_block_norm(const BlockNorm& p, hipStream_t stream) {
