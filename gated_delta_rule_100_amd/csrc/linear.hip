@@ -47,8 +47,8 @@ struct SequenceUnits {
 // itself with one sequence a lane (a launch and a dependent read less than a
 // table in memory).  All whole segments come first, then the sequences' shorter
 // last ones by falling length: the hardware starts workgroups in order, so the
-// long walks start first (8 sequences of 32768 tokens, 32 heads: scan 348 us with
-// the last ones in the order of the sequences, 315 us this way).
+// long walks start first (32768 tokens in 8 sequences, 32 heads: 440 us with the last
+// ones in the order of the sequences, 409 this way).
 struct SegmentTable {
   int whole;      // inclusive prefix sum of whole segments, lane n for sequence n
   int tail;       // tokens of the shorter last segment, 0 for none
@@ -330,8 +330,8 @@ __device__ __forceinline__ Gates chunk_gates(float gate, bool per_token, int lan
 //   - CW copy waves copy the x and y rows of chunk s + 2 and the w rows of chunk
 //     s + 1 to LDS (global-to-LDS loads) and form the gate factors of s + 2.
 //     They are waves of their own because a wave's LDS reads wait for all its
-//     global-to-LDS loads in flight (copies by the score waves: 5.05 us a chunk
-//     of 64 tokens, 128 x 128; by waves of their own 3.0).
+//     global-to-LDS loads in flight (copies by the score waves: 5.05 us a chunk of
+//     64 tokens, 128 x 128, by waves of their own 3.0, at two planes of Z and P).
 // Two barriers a chunk: one behind its last reads, and one behind the score
 // waves' writing P^T for the next chunk (right after the former, while the
 // compute waves form Z x).
@@ -340,20 +340,20 @@ __device__ __forceinline__ Gates chunk_gates(float gate, bool per_token, int lan
 // decayed w enter the products as three bf16 planes, their full 24 bits, whatever
 // the outputs' type and whether dg is wanted.  (Two planes of Z and P leave an
 // error of 2.5e-6, three 1.9e-7, fp32's own, which the sums of dg and of shared
-// heads and fp32 outputs need.  Two would take 3% less of 4 x 4096 tokens, 115
-// against 119 us, and 9% less of 32768 packed tokens, 361 against 398.)
+// heads and fp32 outputs need.  Two take 4% less of 4 x 4096 tokens, 115 against 120
+// us, and 10% less of 32768 packed tokens, 361 against 403.)
 // fp32 inputs run on fp32 matrix instructions throughout.
 //
 // What bounds it is the chain of a step, read, multiply, barrier, read, multiply,
-// with two compute waves a SIMD to hide it: no unit is full (matrix instructions 48%
-// of a step, vector ones about as much, LDS 38%, memory 5 TB/s of q, k, v and o while
-// the steps run).  4 x 4096 tokens, 16 heads, bf16: 69 us for 16 chunks a workgroup
-// after a prologue of 7.5 us, 110-115 us with the segments' states and their chain
-// (2.4 TB/s of q, k, v and o once).  Tried and not kept: four compute waves of 32
-// rows each, which halve the LDS reads (119 us; the gradient 381 against 343); y
-// reads without their two-way bank conflicts, at twice the x reads (118; 350);
-// matrix and vector instructions interleaved by scheduling groups (123; 374-398);
-// wave priorities (115; 345-354).
+// with two compute waves a SIMD to hide it: no unit is full (matrix instructions 40%
+// of a step, vector ones 53%, LDS 42%, memory 3.9 TB/s of q, k, v and o while the steps
+// run).  4 x 4096 tokens, 16 heads, bf16: 81 us for 16 chunks a workgroup, 4.3 us a
+// chunk beside 12 us of start and end, and 120 us with the segments' states and their
+// chain (2.3 TB/s of q, k, v and o once).  Tried and not kept, against 115 us and a
+// gradient of 343, at two planes of Z and P in prompts: four compute waves of 32
+// rows each, which halve the LDS reads (119; 381); y reads without their two-way bank
+// conflicts, at twice the x reads (118; 350); matrix and vector instructions
+// interleaved by scheduling groups (123; 374-398); wave priorities (115; 345-354).
 template <Dt IN, int KD, int W, bool DOT, int SW>
 struct ScanCfg {
   static constexpr int ES = IN == Dt::BF16 ? 2 : 4;
@@ -894,7 +894,7 @@ void linear_grad_kernel(LinearBatch b, LinearPass pq, LinearPass pv, LinearPass 
 // A segment's own state, from zero: the update of the scan alone.  It is a
 // stream of y and w rows, so the copy waves run three chunks ahead (four buffers,
 // one barrier a chunk); one wave forms the gate factors.  4 x 4096 tokens, 16 heads,
-// bf16: 36 us, 3.7 TB/s; bound by the copies and 10 us of start and end.
+// bf16: 37 us, 3.6 TB/s; bound by the copies and 10 us of start and end.
 template <Dt IN, int KD, int W>
 struct LocalCfg {
   static constexpr int ES = IN == Dt::BF16 ? 2 : 4;
@@ -903,7 +903,7 @@ struct LocalCfg {
   static constexpr int OD = 16 * W;
   static constexpr int CHK = KD * ES / 16, CHV = OD * ES / 16;
   // copy waves: with four the fp32 form has 128 registers a wave and spills (4 x 2048
-  // tokens, 16 heads: prompt 174 us, with two 157); bf16 prompts take 115 us with both
+  // tokens, 16 heads: prompt 175 us, with two 158); bf16 prompts take as long with both
   static constexpr int CW = 2;
   static constexpr int THREADS = 64 * (W + CW + 1);
   static constexpr int STAGES = 4;
@@ -1135,7 +1135,8 @@ __global__ __launch_bounds__(256) void linear_starts_kernel(LinearBatch b, int p
 // fp64.  The roundings of row and col add up like a random walk over the unit, but
 // its value at both ends is known as a product of two states (start_dot, end_dot),
 // so what the sums miss at the start is spread evenly over the unit's tokens (1024
-// tokens, 16 heads: relative error of dg 1.1e-6 without this, 6.7e-7 with it).
+// tokens, 16 heads: relative error of dg, fp32 inputs, 1.6e-6 without this and 9.4e-7
+// with it at gates of -0.8 a token, 4.4e-7 and 2.9e-7 at -0.016).
 __global__ __launch_bounds__(256) void linear_dg_kernel(LinearBatch b, const float* row,
                                                         const float* col, const float* start_dot,
                                                         int start_parts, const float* end_dot,

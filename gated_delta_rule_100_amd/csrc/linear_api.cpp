@@ -73,15 +73,21 @@ gdr_status hip_fail(hipError_t e, const char* who, const char* what) {
 }
 
 // Tokens of a segment, or 0 to walk whole sequences.  A scan workgroup takes a
-// compute unit for one (unit, head), about 3.9 us a chunk of 64 tokens (bf16, 128 x
+// compute unit for one (unit, head), about 4.3 us a chunk of 64 tokens (bf16, 128 x
 // 128) with all of them at work, so segments are as long as 256 workgroups allow:
-// fewer states to form and pass on (4 x 4096 tokens, 16 heads: 115 us of scan,
-// segment states and chain at 1024 tokens, 137 at 512 and 168 at 2048; 131072
-// tokens, 4 heads: 220 at 2048, 246 at 1024).  The states cost two launches, so a
-// sequence has to be some chunks longer than a segment before that pays (gradient
-// of one sequence, 128 x 128, bf16 / fp32: 800 tokens, 4 heads 42 / 53 us in
-// segments, 66 / 156 without; 800 tokens, 16 heads 73 / 102 and 71 / 162); the host
-// knows only the average length, and takes four times it for the longest one.
+// fewer states to form and pass on (4 x 4096 tokens, 16 heads, two sets of inputs in
+// turn: 134 us of scan, segment states and chain at 1024 tokens, 154 at 512 and 176 at
+// 2048; 131072 tokens, 4 heads: 235 at 2048, 259 at 1024, 327 at 4096).  The states
+// cost two launches, so a sequence has to be some chunks longer than a segment before
+// that pays (gradient of one sequence, 128 x 128, bf16 / fp32: 800 tokens, 4 heads 43 /
+// 53 us in segments, 62 / 152 without; 800 tokens, 16 heads 74 / 102 and 64 / 156).
+//
+// The host knows only the average length, and takes four times it for the longest
+// one.  Many sequences of one length are right to be walked whole (32 of 1024 tokens,
+// 32 heads: 340 us, 385 in segments), but so are then those beside a much longer one,
+// whose walk takes its whole length: one of 16384 tokens beside 31 of 528, 32 heads,
+// 857 us (471 in segments); 131072 tokens beside 255 single ones, 4 heads, 6.7 ms
+// (0.29).  Such a sequence is faster in a call of its own.
 int segment_tokens(int T_total, int N, int H, bool gradient) {
   const int64_t th = static_cast<int64_t>(T_total) * H;
   const int64_t seg = (th + 256 * 64 - 1) / (256 * 64) * 64;

@@ -313,6 +313,9 @@ gdr_status gdr_state_fixup(const float* L, const float* M, const float* state_in
  *     sequences are not affected.
  *   - Every result is deterministic: no atomics.
  *   - Calls that may run at the same time need workspaces of their own.
+ *   - Long sequences are cut into segments that run side by side, by the average
+ *     length of the batch: one sequence far longer than four times that average is
+ *     walked as a whole, and is faster in a call of its own.
  */
 typedef enum { GDR_DECAY_TOKEN = 0, GDR_DECAY_HEAD = 1 } gdr_decay;
 
@@ -376,7 +379,11 @@ size_t gdr_linear_prefill_workspace_bytes(int T_total, int N, int H, int dk, int
  *   dv_out       [T_total, H, dv]   grad_dtype
  *   dg           fp32, the shape of g, or NULL.  For GDR_DECAY_HEAD the sum over
  *                all tokens.  Where g is below -110 the gradient is that of a
- *                decay of zero: 0
+ *                decay of zero: 0.  dg is formed by sums over the tokens behind, so
+ *                that its error is relative to the largest values of its
+ *                sequence and head (about 1e-6 of them), not to its own: at a nearly
+ *                closed gate (g of -15, say) between open ones, whose true gradient
+ *                is far smaller than that, dg is rounding
  *   dstate_in    [N, H, dv, dk]     fp32, or NULL
  *   workspace    gdr_linear_backward_workspace_bytes(...) bytes
  * Where heads are shared (H above Hk), T_total * Hk * dk is at most 2^34 - 1024.
