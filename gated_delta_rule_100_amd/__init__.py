@@ -38,6 +38,13 @@ __all__ = [
     "gdr_block_norm",
     "gdr_block_norm_backward",
     "gdr_block_norm_backward_workspace_bytes",
+    "gdr_block_norm8",
+    "gdr_product8",
+    "gdr_channel_decode",
+    "gdr_channel_prefill",
+    "gdr_channel_prefill_workspace_bytes",
+    "gdr_channel_backward",
+    "gdr_channel_backward_workspace_bytes",
     "gdr_status_string",
     "gdr_last_error",
 ]
@@ -47,6 +54,7 @@ GDR_FP32 = 1
 GDR_DECAY_TOKEN = 0
 GDR_DECAY_HEAD = 1
 GDR_GATES = {"silu": 0, "sigmoid": 1}
+GDR_CHANNEL_GATES = {"log": 0, "logit": 1}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libgdr.so")
@@ -107,6 +115,20 @@ def _load():
     lib.gdr_block_norm_backward.restype = I
     lib.gdr_block_norm_backward_workspace_bytes.argtypes = [L, I]
     lib.gdr_block_norm_backward_workspace_bytes.restype = S
+    lib.gdr_block_norm8.argtypes = [P] * 8 + [L, I, F, F, I, I, I, I, P]
+    lib.gdr_block_norm8.restype = I
+    lib.gdr_product8.argtypes = [P] * 5 + [I, I, I, I, P]
+    lib.gdr_product8.restype = I
+    lib.gdr_channel_decode.argtypes = [P, P, P, P, I, I, L, L, I, I, I, I, P]
+    lib.gdr_channel_decode.restype = I
+    lib.gdr_channel_prefill.argtypes = [P, P, P, I, P, P, P, I, I, L, L, I, I, I, I, P, S, P]
+    lib.gdr_channel_prefill.restype = I
+    lib.gdr_channel_backward.argtypes = [P, P, P, P, I, P, P, P, P, P, P, I, I, L, L, I, I, I, I,
+                                         P, S, P]
+    lib.gdr_channel_backward.restype = I
+    for name in ("gdr_channel_prefill_workspace_bytes", "gdr_channel_backward_workspace_bytes"):
+        getattr(lib, name).argtypes = [I, I]
+        getattr(lib, name).restype = S
     lib.gdr_status_string.argtypes = [I]
     lib.gdr_status_string.restype = ctypes.c_char_p
     lib.gdr_last_error.argtypes = []
@@ -169,7 +191,10 @@ def gdr_decode_step(q, k, v, g, beta, state, o, stream=None, *, norm=None) -> No
     o [N, H, dv] bf16 or fp32.  norm: a dict of gdr_block_norm's arguments after
     x (h, y, w_after, gate, ...): the norm and gate behind the heads, of every
     row of o, on the same stream; what it would refuse is refused before
-    anything runs."""
+    anything runs.  With y8 and y_scale instead of y it is gdr_block_norm8, and
+    project=dict(w=, w_scale=, out=) in it the product of gdr_product8 behind that:
+    out [N, F] from rows of w as long as a token's heads together (of whole blocks
+    of 128), or out [N, H, F] from rows as long as one head."""
     N, H, dk = q.shape
     dv = v.shape[2]
     if k.shape != q.shape or v.shape[:2] != (N, H) or g.shape != (N, H) or beta.shape != (N, H) \
@@ -590,6 +615,8 @@ def _norm_after(o, norm, dev, stream):
     takes."""
     if norm is None:
         return _nothing
+    if "y8" in norm:
+        return _norm8_after(o, dev, stream, **norm)
     who, lib = "gdr_block_norm", _load()
     fn = lib.gdr_block_norm
     at, ptrs, rows, tail = _norm_call(o, **norm)
@@ -633,3 +660,213 @@ def gdr_block_norm_backward(x, dh, dy, dx, *, w_after=None, gate=None, act="silu
             _ptr(dgate, "dgate", _IO, dev), _ptr(dresidual, "dresidual", _IO, dev),
             _ptr(dw_after, "dw_after", _F32, dev), _ptr(dw_before, "dw_before", _F32, dev),
             rows, D, scale, eps, ac, ic, wc, oc, wp, wb)
+
+
+_E4M3 = (torch.float8_e4m3fn,)
+
+
+def gdr_block_norm8(x, y8, y_scale, h=None, *, w_after=None, gate=None, act="silu", residual=None,
+                    scale=1.0, w_before=None, eps=1e-6, stream=None) -> None:
+    """gdr_block_norm with its result (y with w_before, h without) in 8 bits: y8 [..., D]
+    torch.float8_e4m3fn and y_scale [..., ceil(D / 128)] fp32, one scale for each 128
+    values of a row, max / 448.  D a multiple of 16.  h (like x, bf16 or fp32) is written
+    where given; everything else as gdr_block_norm's."""
+    dev, ptrs, rows, tail = _norm8_call(x, y8, y_scale, h, w_after, gate, act, residual, scale,
+                                        w_before, eps)
+    _launch("gdr_block_norm8", _load().gdr_block_norm8, dev, stream, *ptrs, rows, *tail)
+
+
+def _norm8_call(x, y8, y_scale, h=None, w_after=None, gate=None, act="silu", residual=None,
+                scale=1.0, w_before=None, eps=1e-6):
+    """Device and arguments of a gdr_block_norm8 call: pointers, rows and the rest."""
+    who = "gdr_block_norm8"
+    dev, rows, D, ac, ic, wc, oc = _norm_args(who, x, w_after, gate, act, residual, w_before, (),
+                                              (h,))
+    if y8.shape != x.shape or y_scale.shape != (*x.shape[:-1], -(-D // 128)):
+        raise GdrError(f"{who}: y8 must have the shape of x, y_scale {(*x.shape[:-1], -(-D // 128))}")
+    return dev, (_ptr(x, "x", _IO, dev), _ptr(w_after, "w_after", _IO, dev),
+                 _ptr(gate, "gate", _IO, dev), _ptr(residual, "residual", _IO, dev),
+                 _ptr(w_before, "w_before", _IO, dev), _ptr(h, "h", _IO, dev),
+                 _ptr(y8, "y8", _E4M3, dev), _ptr(y_scale, "y_scale", _F32, dev)), rows, \
+        (D, scale, eps, ac, ic, wc, oc)
+
+
+def gdr_product8(a, a_scale, w, w_scale, out, *, stream=None) -> None:
+    """out = (a a_scale) (w w_scale)^T of matrices in 8 bits: a [M, K], w [N, K]
+    torch.float8_e4m3fn; a_scale [M, ceil(K / 128)], w_scale [ceil(N / 128), ceil(K / 128)]
+    fp32; out [M, N] bf16 or fp32.  K a multiple of 16."""
+    dev, args = _product8_call(a, a_scale, w, w_scale, out)
+    _launch("gdr_product8", _load().gdr_product8, dev, stream, *args)
+
+
+def _norm8_after(o, dev, stream, *, project=None, **norm):
+    """_norm_after with a result in 8 bits (gdr_block_norm8), and behind it the product
+    that `project` asks for, a dict of gdr_product8's w, w_scale and out: rows of w are as
+    long as a row of o, or as all heads of a token where o has heads of whole blocks of
+    128.  Everything is checked now."""
+    who, lib = "gdr_block_norm8", _load()
+    at, ptrs, rows, tail = _norm8_call(o, **norm)
+    if at != dev:
+        raise GdrError("o is on another device than the first tensor")
+    _launch(who, lib.gdr_block_norm8, dev, stream, *ptrs, 0, *tail)
+    if rows and not lib.gdr_block_norm_backward_workspace_bytes(rows, tail[0]):
+        raise GdrError(f"{who}: rows={rows}")
+    first = lambda: _launch(who, lib.gdr_block_norm8, dev, stream, *ptrs, rows, *tail)  # noqa: E731
+    if project is None:
+        return first
+    w, out, D = project["w"], project["out"], o.shape[-1]
+    K = w.shape[-1]
+    if K != D and (D % 128 != 0 or o.dim() < 3 or K != o.shape[-2] * D):
+        raise GdrError(f"{who}: rows of w have {K} values, those of o {D}, in heads of whole "
+                       "blocks of 128")
+    M, F = o.numel() // K if K else 0, w.shape[0]
+    if out.shape != (*o.shape[:-1 if K == D else -2], F):
+        raise GdrError(f"{who}: out must have shape {(*o.shape[:-1 if K == D else -2], F)}")
+    on, args = _product8_call(norm["y8"].view(M, K), norm["y_scale"].view(M, -(-K // 128)), w,
+                              project["w_scale"], out.view(M, F))
+    if on != dev:
+        raise GdrError("y8 is on another device than the first tensor")
+    _launch("gdr_product8", lib.gdr_product8, dev, stream, *args[:5], 0, *args[6:])
+
+    def both():
+        first()
+        _launch("gdr_product8", lib.gdr_product8, dev, stream, *args)
+    return both
+
+
+def _product8_call(a, a_scale, w, w_scale, out):
+    """Device and arguments of a gdr_product8 call."""
+    who = "gdr_product8"
+    M, K = a.shape
+    N = w.shape[0]
+    kb = -(-K // 128)
+    if w.shape != (N, K) or a_scale.shape != (M, kb) or w_scale.shape != (-(-N // 128), kb) \
+            or out.shape != (M, N):
+        raise GdrError(f"{who}: inconsistent shapes")
+    dev = _device(a, "a")
+    return dev, (_ptr(a, "a", _E4M3, dev), _ptr(a_scale, "a_scale", _F32, dev),
+                 _ptr(w, "w", _E4M3, dev), _ptr(w_scale, "w_scale", _F32, dev),
+                 _ptr(out, "out", _IO, dev), M, N, K, _code(out.dtype))
+
+
+def _channel_rows(t, name, dev):
+    """Pointer and row stride of a [rows, D] tensor whose rows may be slices of wider
+    ones (stride 0: dense)."""
+    if t is None:
+        return None, 0
+    if t.is_contiguous():
+        return _ptr(t, name, _IO, dev), 0
+    if _device(t, name) != dev:
+        raise GdrError(f"{name} is on another device than the first tensor")
+    if t.dtype not in _IO:
+        raise GdrError(f"{name} has dtype {t.dtype}, expected one of {_IO}")
+    rows, D = t.shape
+    st, sd = t.stride()
+    if (D > 1 and sd != 1) or (rows > 1 and st < D):
+        raise GdrError(f"{name}: the channels of a token must be contiguous and tokens must not "
+                       "overlap")
+    return t.data_ptr(), st if rows > 1 else 0
+
+
+def _channel_form(who, gate, complement):
+    if gate not in GDR_CHANNEL_GATES:
+        raise GdrError(f"{who}: gate must be one of {sorted(GDR_CHANNEL_GATES)}")
+    return GDR_CHANNEL_GATES[gate], int(bool(complement))
+
+
+def gdr_channel_decode(x, g, state, h, *, gate="log", complement=False, stream=None,
+                       norm=None) -> None:
+    """One token of the recurrence with a decay for each channel, h = a state + b, state
+    updated in place: a = exp(g) (gate "log") or sigmoid(g) ("logit"), b = x or, with
+    complement, (1 - a) x.  x, g [N, D] (bf16 or fp32 each; rows may be slices of wider
+    tensors); state [N, D] fp32; h [N, D] the dtype of x.  norm: as gdr_decode_step's, of
+    every row of h."""
+    who = "gdr_channel_decode"
+    N, D = x.shape
+    if g.shape != (N, D) or state.shape != (N, D) or h.shape != (N, D):
+        raise GdrError(f"{who}: inconsistent shapes")
+    _same_dtype(who, "x, h", x, h)
+    form = _channel_form(who, gate, complement)
+    dev = _device(x, "x")
+    xp, xs = _channel_rows(x, "x", dev)
+    gp, gs = _channel_rows(g, "g", dev)
+    after = _norm_after(h, norm, dev, stream)
+    _launch(who, _load().gdr_channel_decode, dev, stream, xp, gp, _ptr(state, "state", _F32, dev),
+            _ptr(h, "h", _IO, dev), N, D, xs, gs, *form, _code(x.dtype), _code(g.dtype))
+    after()
+
+
+def gdr_channel_prefill_workspace_bytes(T_total, D) -> int:
+    return int(_load().gdr_channel_prefill_workspace_bytes(T_total, D))
+
+
+def gdr_channel_backward_workspace_bytes(T_total, D) -> int:
+    return int(_load().gdr_channel_backward_workspace_bytes(T_total, D))
+
+
+def _channel_states(who, cu_seqlens, D, **states):
+    N = cu_seqlens.shape[0] - 1
+    for name, t in states.items():
+        if t is not None and t.shape != (N, D):
+            raise GdrError(f"{who}: {name} must have shape {(N, D)}")
+    return N
+
+
+def gdr_channel_prefill(x, g, cu_seqlens, state_in, state_out, h, *, gate="log", complement=False,
+                        workspace=None, stream=None, norm=None) -> None:
+    """The recurrence with a decay for each channel over packed sequences: h_t = a_t h_{t-1}
+    + b_t, with a and b as gdr_channel_decode's.  x, g [T, D] (bf16 or fp32 each; rows may
+    be slices of wider tensors); cu_seqlens [N+1] int32 (device); state_in [N, D] fp32 or
+    None; state_out like it (may be state_in) or None; h [T, D] the dtype of x.
+    workspace: as gdr_chunk_prefill's, by gdr_channel_prefill_workspace_bytes.  norm: as
+    gdr_linear_prefill's, of the rows of h."""
+    who = "gdr_channel_prefill"
+    T, D = x.shape
+    if g.shape != (T, D) or h.shape != (T, D) or cu_seqlens.dim() != 1:
+        raise GdrError(f"{who}: inconsistent shapes")
+    _same_dtype(who, "x, h", x, h)
+    form = _channel_form(who, gate, complement)
+    N = _channel_states(who, cu_seqlens, D, state_in=state_in, state_out=state_out)
+    dev = _device(x, "x")
+    xp, xs = _channel_rows(x, "x", dev)
+    gp, gs = _channel_rows(g, "g", dev)
+    args = (xp, gp, _ptr(cu_seqlens, "cu_seqlens", _I32, dev), N,
+            _ptr(state_in, "state_in", _F32, dev), _ptr(state_out, "state_out", _F32, dev),
+            _ptr(h, "h", _IO, dev), T, D, xs, gs, *form, _code(x.dtype), _code(g.dtype))
+    after = _norm_after(h, norm, dev, stream)
+    lib = _load()
+    wp, wb, workspace = _workspace(workspace, lib.gdr_channel_prefill_workspace_bytes(T, D), dev,
+                                   stream)
+    _launch(who, lib.gdr_channel_prefill, dev, stream, *args, wp, wb)
+    after()
+
+
+def gdr_channel_backward(x, g, h, cu_seqlens, state_in, dh, dstate_out, dx, dg, *, dstate_in=None,
+                         gate="log", complement=False, workspace=None, stream=None) -> None:
+    """Gradients of gdr_channel_prefill from dh [T, D] and dstate_out ([N, D] fp32 or
+    None): dx [T, D], dg [T, D] (the dtype of g) and dstate_in ([N, D] fp32) where given.
+    x, g, cu_seqlens and state_in as the forward call had them (x may be None without
+    complement), h [T, D] as it left it; h, dh, dx and x share a dtype.  workspace: by
+    gdr_channel_backward_workspace_bytes."""
+    who = "gdr_channel_backward"
+    T, D = g.shape
+    if any(t.shape != (T, D) for t in (h, dh, dx, dg)) or cu_seqlens.dim() != 1 \
+            or (x is not None and x.shape != (T, D)):
+        raise GdrError(f"{who}: inconsistent shapes")
+    _same_dtype(who, "x, h, dh, dx", h, dh, dx, *(() if x is None else (x,)))
+    _same_dtype(who, "g, dg", g, dg)
+    form = _channel_form(who, gate, complement)
+    N = _channel_states(who, cu_seqlens, D, state_in=state_in, dstate_out=dstate_out,
+                        dstate_in=dstate_in)
+    dev = _device(g, "g")
+    xp, xs = _channel_rows(x, "x", dev)
+    gp, gs = _channel_rows(g, "g", dev)
+    lib = _load()
+    wp, wb, workspace = _workspace(workspace, lib.gdr_channel_backward_workspace_bytes(T, D), dev,
+                                   stream)
+    _launch(who, lib.gdr_channel_backward, dev, stream, xp, gp, _ptr(h, "h", _IO, dev),
+            _ptr(cu_seqlens, "cu_seqlens", _I32, dev), N, _ptr(state_in, "state_in", _F32, dev),
+            _ptr(dh, "dh", _IO, dev), _ptr(dstate_out, "dstate_out", _F32, dev),
+            _ptr(dx, "dx", _IO, dev), _ptr(dg, "dg", _IO, dev),
+            _ptr(dstate_in, "dstate_in", _F32, dev), T, D, xs, gs, *form, _code(h.dtype),
+            _code(g.dtype), wp, wb)

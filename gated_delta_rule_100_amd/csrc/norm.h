@@ -14,6 +14,8 @@ struct BlockNorm {
   void *h, *y;
   const void *dh, *dy;
   void *dx, *dgate, *dresidual;
+  void* y8;                         // the result in 8 bits and its scales
+  float* y_scale;
   float *part_after, *part_before;  // [block_norm_backward_blocks][D]
   int64_t rows;
   int D, act, in_dtype, w_dtype, out_dtype;
@@ -24,6 +26,8 @@ struct BlockNorm {
 int block_norm_backward_blocks(int64_t rows, int D);
 
 hipError_t launch_block_norm(const BlockNorm& p, hipStream_t stream);
+// y in 8 bits (y8 and y_scale instead of y); D % 16 == 0.
+hipError_t launch_block_norm8(const BlockNorm& p, hipStream_t stream);
 hipError_t launch_block_norm_backward(const BlockNorm& p, float* dw_after, float* dw_before,
                                       hipStream_t stream);
 

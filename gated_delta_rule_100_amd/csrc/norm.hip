@@ -176,10 +176,56 @@ __device__ __forceinline__ void widen(const RawRow<IN, E>& r, float (&x)[E]) {
   }
 }
 
+// Largest of x over the 16 (8 with HALF) consecutive lanes that share a scale, in each
+// of them: partners as in row16_sum.
+template <bool HALF>
+__device__ __forceinline__ float block_max(float x) {
+  auto with = [&](auto ctrl) {
+    x = fmaxf(x, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+                     0, __builtin_bit_cast(int, x), decltype(ctrl)::value, 0xF, 0xF, true)));
+  };
+  with(std::integral_constant<int, 0xB1>());
+  with(std::integral_constant<int, 0x4E>());
+  with(std::integral_constant<int, 0x141>());
+  if constexpr (!HALF) with(std::integral_constant<int, 0x128>());
+  return x;
+}
+
+// A row as e4m3 with one scale for each 128 values: 16 threads' pieces of 8 (rows of up
+// to 64 values: all 8 threads of the row).  The quotient is a product with 448 / max,
+// which the conversion rounds once more: a value within 2^-23 of the middle between two
+// e4m3 numbers may take the other one.  The largest becomes 448 (1 + 2^-23) at most and
+// rounds to 448, so nothing needs a clamp, which would lose a NaN.
+template <int TPR, int E>
+__device__ __forceinline__ void store_row8(void* y8, float* y_scale, size_t row, int D, int t,
+                                           const float (&x)[E]) {
+  const size_t blocks = static_cast<size_t>(D + 127) / 128;
+#pragma unroll
+  for (int j = 0; j < E / 8; ++j) {
+    const int c = (j * TPR + t) * 8;
+    float top = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[8 * j + e]));
+    top = block_max<TPR == 8>(top);
+    const bool some = !(top < 0x1p-100f);
+    const float f = some ? 448.f / top : 0.f;
+    if (c >= D) continue;
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float* v = x + 8 * j + 4 * i;
+      int q = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * f, v[1] * f, 0, false);
+      w[i] = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(v[2] * f, v[3] * f, q, true));
+    }
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(y8) + row * D + c) = make_uint2(w[0], w[1]);
+    if (c % 128 == 0) y_scale[row * blocks + c / 128] = some ? top / 448.f : 0.f;
+  }
+}
+
 // 262144 rows of 128, bf16, gate: 39.3 us, 5.1 TB/s, the rate of a copy of this size
 // (two rows a thread, loaded together: 43.7); 64 rows of 2048 with both norms: 9 us,
 // a launch.
-template <Dt IN, int TPR, int E, bool vec>
+template <Dt IN, int TPR, int E, bool vec, bool Q8>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_kernel(BlockNorm p) {
   constexpr int THREADS = TPR > 256 ? TPR : 256, RPB = THREADS / TPR;
   __shared__ float lds[2][16];
@@ -217,7 +263,10 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_kernel(Block
     const float inv = rsqrtf(row_sum<TPR>(ss, lds, slot) * inv_d + p.eps);
 #pragma unroll
     for (int i = 0; i < E; ++i) y[i] = x[i] * inv * wb[i];
-    store_row<TPR, E>(p.y, p.out_dtype, row, p.D, t, vec, y);
+    if constexpr (Q8) store_row8<TPR, E>(p.y8, p.y_scale, row, p.D, t, y);
+    else store_row<TPR, E>(p.y, p.out_dtype, row, p.D, t, vec, y);
+  } else if constexpr (Q8) {
+    store_row8<TPR, E>(p.y8, p.y_scale, row, p.D, t, x);
   }
   if (p.h) store_row<TPR, E>(p.h, p.out_dtype, row, p.D, t, vec, x);
 }
@@ -448,7 +497,7 @@ hipError_t launch_block_norm(const BlockNorm& p, hipStream_t stream) {
   return by_width(p.D, [&](auto tpr, auto el) {
     constexpr int T = decltype(tpr)::value, E = decltype(el)::value;
     auto go = [&](auto in, auto vec) {
-      hipLaunchKernelGGL((block_norm_kernel<decltype(in)::value, T, E, decltype(vec)::value>),
+      hipLaunchKernelGGL((block_norm_kernel<decltype(in)::value, T, E, decltype(vec)::value, false>),
                          dim3(static_cast<unsigned>((p.rows + rpb - 1) / rpb)), dim3(T > 256 ? T : 256),
                          0, stream, p);
       return hipGetLastError();
@@ -457,6 +506,21 @@ hipError_t launch_block_norm(const BlockNorm& p, hipStream_t stream) {
     const std::integral_constant<Dt, Dt::F32> f32;
     if (p.D % 8 == 0) return p.in_dtype == 0 ? go(bf16, std::true_type()) : go(f32, std::true_type());
     return p.in_dtype == 0 ? go(bf16, std::false_type()) : go(f32, std::false_type());
+  });
+}
+
+hipError_t launch_block_norm8(const BlockNorm& p, hipStream_t stream) {
+  const int64_t rpb = rows_per_block(p.D);
+  return by_width(p.D, [&](auto tpr, auto el) {
+    constexpr int T = decltype(tpr)::value, E = decltype(el)::value;
+    auto go = [&](auto in) {
+      hipLaunchKernelGGL((block_norm_kernel<decltype(in)::value, T, E, true, true>),
+                         dim3(static_cast<unsigned>((p.rows + rpb - 1) / rpb)), dim3(T > 256 ? T : 256),
+                         0, stream, p);
+      return hipGetLastError();
+    };
+    return p.in_dtype == 0 ? go(std::integral_constant<Dt, Dt::BF16>())
+                           : go(std::integral_constant<Dt, Dt::F32>());
   });
 }
 

@@ -81,6 +81,37 @@ gdr_status gdr_block_norm(const void* x, const void* w_after, const void* gate,
                     "gdr_block_norm launch");
 }
 
+gdr_status gdr_block_norm8(const void* x, const void* w_after, const void* gate,
+                           const void* residual, const void* w_before, void* h, void* y8,
+                           float* y_scale, int64_t rows, int D, float scale, float eps,
+                           gdr_gate act, gdr_dtype in_dtype, gdr_dtype w_dtype,
+                           gdr_dtype out_dtype, gdr_stream_t stream) {
+  const char* who = "gdr_block_norm8";
+  BlockNorm p{};
+  p.x = x; p.w_after = w_after; p.gate = gate; p.residual = residual; p.w_before = w_before;
+  p.h = h; p.y8 = y8; p.y_scale = y_scale;
+  p.rows = rows; p.D = D; p.act = act;
+  p.in_dtype = in_dtype; p.w_dtype = w_dtype; p.out_dtype = out_dtype;
+  p.scale = scale; p.eps = eps;
+  if (rows > 0 && (!x || !y8 || !y_scale)) return fail(GDR_ERR_INVALID_ARG, "%s: NULL tensor pointer", who);
+  for (const void* q : {x, gate, residual, static_cast<const void*>(h), static_cast<const void*>(y_scale)})
+    if (q && q == y8) return fail(GDR_ERR_INVALID_ARG, "%s: y8 must have a buffer of its own", who);
+  if (h && in_dtype != out_dtype)
+    for (const void* q : {x, gate, residual})
+      if (q == h) return fail(GDR_ERR_INVALID_ARG, "%s: in place needs one dtype", who);
+  gdr_status s = check_common(who, p);
+  if (s != GDR_OK) return s;
+  if (D % 16 != 0) return fail(GDR_ERR_UNSUPPORTED, "%s: D=%d is not a multiple of 16", who, D);
+  for (const void* q : {static_cast<const void*>(y8), static_cast<const void*>(y_scale)})
+    if ((reinterpret_cast<uintptr_t>(q) & 15u) != 0)
+      return fail(GDR_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", who);
+  if (rows == 0) return ok();
+  s = check_device();
+  if (s != GDR_OK) return s;
+  return hip_status(gdr::launch_block_norm8(p, static_cast<hipStream_t>(stream)),
+                    "gdr_block_norm8 launch");
+}
+
 size_t gdr_block_norm_backward_workspace_bytes(int64_t rows, int D) {
   if (D < 1 || D > kMaxWidth || !valid_rows(rows, D)) return 0;
   return 2 * partial_bytes(rows, D);

@@ -463,6 +463,148 @@ gdr_status gdr_block_norm_backward(const void* x, const void* w_after, const voi
 /* Device workspace of gdr_block_norm_backward; 0 also on bad arguments. */
 size_t gdr_block_norm_backward_workspace_bytes(int64_t rows, int D);
 
+/*
+ * gdr_block_norm8 -- gdr_block_norm with its result in 8 bits, for the product
+ * that follows (gdr_product8).  y (with w_before) or h (without) leaves as e4m3
+ * (OCP, torch.float8_e4m3fn) with one fp32 scale for each 128 consecutive values
+ * of a row, the last block of a row being shorter where D is no multiple of 128:
+ *
+ *     y_scale = max|y| / 448,  y8 = e4m3(y / y_scale)   (round to nearest even)
+ *
+ * from the unrounded fp32 values.  A block whose values are all below 2^-100 in
+ * magnitude, zeros among them, is stored as zeros with a scale of 0.  A NaN stays
+ * a NaN in its place; an infinity makes its block's scale infinite and itself a
+ * NaN, so that none of the block reads as a finite number.
+ *
+ *   x, w_after, gate, residual, w_before, act   as gdr_block_norm's
+ *   h         [rows, D]              out_dtype, or NULL: not written.  May be the
+ *                                    buffer of x, gate or residual when the dtypes
+ *                                    agree
+ *   y8        [rows, D]              e4m3
+ *   y_scale   [rows, ceil(D / 128)]  fp32
+ *   D a multiple of 16, otherwise the limits of gdr_block_norm.  y8 and y_scale
+ *   must not overlap anything else.
+ */
+gdr_status gdr_block_norm8(const void* x, const void* w_after, const void* gate,
+                           const void* residual, const void* w_before, void* h, void* y8,
+                           float* y_scale, int64_t rows, int D, float scale, float eps,
+                           gdr_gate act, gdr_dtype in_dtype, gdr_dtype w_dtype,
+                           gdr_dtype out_dtype, gdr_stream_t stream);
+
+/*
+ * gdr_product8 -- the product of rows in 8 bits with weights in 8 bits:
+ *
+ *     out[m][n] = sum_b a_scale[m][b] w_scale[n / 128][b] sum_{k in block b} a[m][k] w[n][k]
+ *
+ * over blocks b of 128 consecutive k.  Products are exact and every sum is fp32.
+ *
+ *   a        [M, K]                           e4m3, as gdr_block_norm8 writes it
+ *   a_scale  [M, ceil(K / 128)]               fp32
+ *   w        [N, K]                           e4m3
+ *   w_scale  [ceil(N / 128), ceil(K / 128)]   fp32: one for each 128 x 128 of w
+ *   out      [M, N]                           out_dtype
+ *   M >= 0, N > 0, K > 0 a multiple of 16; M, N, K <= 2^24 and M * N < 2^32
+ * A row of a, or of w, touches its own row, or column, of out only, NaN and
+ * infinite scales among them.  out must not overlap an input.  Deterministic.
+ */
+gdr_status gdr_product8(const void* a, const float* a_scale, const void* w, const float* w_scale,
+                        void* out, int M, int N, int K, gdr_dtype out_dtype, gdr_stream_t stream);
+
+/*
+ * The gated linear recurrence with a decay for each channel -- a recurrence whose
+ * state is a vector (gated recurrent units without a nonlinearity in time, the
+ * recurrent layers of hybrid models).  Per sequence and channel
+ *
+ *     h_t = a_t h_{t-1} + b_t
+ *     a_t = exp(g_t) (GDR_CHANNEL_LOG) or sigmoid(g_t) (GDR_CHANNEL_LOGIT)
+ *     b_t = x_t, or (1 - a_t) x_t with `complement`
+ *
+ * Conventions of gdr_channel_*, beyond those above:
+ *   - x, g, h and their gradients are rows of D channels, any D from 1 to 2^20.
+ *     x, h, dh and dx share io_dtype, g and dg have g_dtype.  States are fp32.
+ *   - x and g may be slices of wider token rows: x_stride and g_stride are the
+ *     elements from one row to the next, 0 for dense, at least D and at most 2^24.
+ *     Where D and both strides are multiples of 8, rows are read with 16-byte
+ *     loads, otherwise element by element.
+ *   - g <= 0 is expected of GDR_CHANNEL_LOG (a decay); -110 or less, -infinity among
+ *     it, is a decay of exactly zero.  1 - a is formed without cancellation.
+ *   - cu_seqlens[N] may be below T_total: rows behind the last sequence are not
+ *     written, and what they hold does not matter.
+ *   - N <= 2^20, N * D < 2^31, and T_total and D such that a launch holds them:
+ *     T_total / 64 + 1 times D / 64 + 1 below 2^24.
+ *   - An infinity or NaN in x or g spreads to later tokens of its own sequence and
+ *     channel (earlier ones in the gradient), and nowhere else.
+ *   - Every result is deterministic: sums are formed in one order, whatever the
+ *     order in which workgroups run.
+ *   - Calls that may run at the same time need workspaces of their own, two captured
+ *     graphs among them: a workspace holds what workgroups of one call tell each other.
+ */
+typedef enum { GDR_CHANNEL_LOG = 0, GDR_CHANNEL_LOGIT = 1 } gdr_channel_gate;
+
+/*
+ * gdr_channel_decode -- one token of N sequences, state updated IN PLACE.
+ *
+ *   x, g    [N, D]   rows x_stride / g_stride apart
+ *   state   [N, D]   fp32, read and overwritten with h_t
+ *   h       [N, D]   io_dtype; may be x's buffer where x is dense
+ */
+gdr_status gdr_channel_decode(const void* x, const void* g, float* state, void* h, int N, int D,
+                              int64_t x_stride, int64_t g_stride, gdr_channel_gate gate,
+                              int complement, gdr_dtype io_dtype, gdr_dtype g_dtype,
+                              gdr_stream_t stream);
+
+/*
+ * gdr_channel_prefill -- prompts: packed variable-length sequences.
+ *
+ *   x, g        [T_total, D]   rows x_stride / g_stride apart
+ *   cu_seqlens  [N+1] int32    device; sequence n is tokens [cu[n], cu[n+1])
+ *   state_in    [N, D] fp32, or NULL for zero states
+ *   state_out   [N, D] fp32 final states; may equal state_in; NULL: not written.
+ *               A sequence of length 0 passes its initial state on
+ *   h           [T_total, D]   io_dtype; may be x's buffer where x is dense
+ *   workspace   gdr_channel_prefill_workspace_bytes(...) bytes of device scratch
+ *               (NULL when that is 0); its contents do not matter
+ * No other overlap of outputs with inputs or each other.
+ */
+gdr_status gdr_channel_prefill(const void* x, const void* g, const int32_t* cu_seqlens, int N,
+                               const float* state_in, float* state_out, void* h, int T_total,
+                               int D, int64_t x_stride, int64_t g_stride, gdr_channel_gate gate,
+                               int complement, gdr_dtype io_dtype, gdr_dtype g_dtype,
+                               void* workspace, size_t workspace_bytes, gdr_stream_t stream);
+
+/* Device workspace of gdr_channel_prefill; 0 also on bad arguments. */
+size_t gdr_channel_prefill_workspace_bytes(int T_total, int D);
+
+/*
+ * gdr_channel_backward -- gradients of gdr_channel_prefill.  With r_t the gradient
+ * of h_t, from h's own and from later tokens,
+ *     r_t  = dh_t + a_{t+1} r_{t+1}       (dstate_out for the one after the last)
+ *     dx_t = r_t, or (1 - a_t) r_t with `complement`
+ *     dg_t = a' r_t (h_{t-1} [- x_t with `complement`]),  a' = a, or a (1 - a) of logits
+ *     dstate_in = a_1 r_1
+ *
+ *   x, g, cu_seqlens, state_in   as given to gdr_channel_prefill (x is read with
+ *               `complement` only, and may be NULL without)
+ *   h           [T_total, D]   io_dtype, as gdr_channel_prefill wrote it: dg takes
+ *               h_{t-1} from it, so that its relative error is that of h's rounding
+ *   dh          [T_total, D]   io_dtype
+ *   dstate_out  [N, D] fp32, or NULL for zero
+ *   dx, dg      [T_total, D]   io_dtype and g_dtype, dense
+ *   dstate_in   [N, D] fp32, or NULL: not written
+ *   workspace   gdr_channel_backward_workspace_bytes(...) bytes
+ * No output may overlap an input or another output.
+ */
+gdr_status gdr_channel_backward(const void* x, const void* g, const void* h,
+                                const int32_t* cu_seqlens, int N, const float* state_in,
+                                const void* dh, const float* dstate_out, void* dx, void* dg,
+                                float* dstate_in, int T_total, int D, int64_t x_stride,
+                                int64_t g_stride, gdr_channel_gate gate, int complement,
+                                gdr_dtype io_dtype, gdr_dtype g_dtype, void* workspace,
+                                size_t workspace_bytes, gdr_stream_t stream);
+
+/* Device workspace of gdr_channel_backward; 0 also on bad arguments. */
+size_t gdr_channel_backward_workspace_bytes(int T_total, int D);
+
 /* Static text for a status code. */
 const char* gdr_status_string(gdr_status s);
 
