@@ -1,5 +1,30 @@
 // channel.hip -- the recurrence with a decay for each channel (gdr_channel_* in
-// gdr.h) and its gradient on gfx950, one thread a sequence and channel.
+// gdr.h) and its gradient on gfx950.
+//
+// A token maps a channel's state s to a s + b.  Such maps join, (A', B') after (A, B)
+// being (A' A, A' B + B'), so a long sequence is cut up in time and every input is
+// still read once:
+//   - a thread holds L tokens of V channels in its registers and joins their maps;
+//   - the GROUPS threads of a channel in a workgroup meet in LDS: a tile of TT tokens;
+//   - tiles of one channel meet in memory: a workgroup publishes its tile's map, reads
+//     those of the tiles before it and so has the state that its tile starts from,
+//     while its rows wait in registers; then every thread walks its tokens and stores.
+// The packed batch is one time axis: the first token of a sequence has a map that
+// forgets what was before (A = 0, its own initial state in B), so that ragged batches
+// make no difference.  The gradient is the same scan from the last token to the first,
+// of c_t = a_t (dh_t + c_{t+1}), whose r_t = dh_t + c_{t+1} gives dx and dg.
+//
+// Order.  Every join happens in one fixed order, so results do not depend on which
+// workgroup is first: tiles of a span (kSpan of them) are folded from the span's first
+// on, spans from any span whose state is known, each by the same operation as the one
+// that published it.
+//
+// Waiting.  A workgroup takes its tile by a ticket (an atomic counter) and waits for
+// tiles of lower tickets only, which run already, so every wait ends whatever the order
+// of dispatch.  What is published is one word, written and read at once (map: two
+// floats in 8 bytes, state: 4 bytes), so no fence orders anything; all ones stand for
+// "not yet", which a fill kernel writes before each pass.  A wait is bounded all the
+// same (kPatience), for a workspace that two calls share against the rules.
 #include <type_traits>
 
 #include "channel.h"
@@ -9,10 +34,25 @@ namespace gdr {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kThreads = 256;
+constexpr int kSpan = 16;  // tiles of a span
+constexpr int kBack = 8;   // spans looked back at together
+constexpr int kPatience = 1 << 22;
+constexpr uint32_t kNone = 0xFFFFFFFFu;
 
-// Decay a and its complement 1 - a.
+// What workgroups of one pass tell each other, for `width` channels (whole columns).
+struct Links {
+  uint32_t* ticket;
+  unsigned long long* tile_map;  // [tiles][width]
+  unsigned long long* span_map;  // [spans][width]
+  uint32_t* span_end;            // [spans][width] state behind a span
+  int tiles, cols;
+  size_t width;
+};
+
+// Decay a, its complement 1 - a, and log2 a of a GDR_CHANNEL_LOG gate.
 struct Decay {
-  float a, rest;
+  float a, rest, log2;
 };
 
 // 1 - e^g without cancellation: for g above -1/2 the series to g^9 (its next term is
@@ -37,107 +77,514 @@ __device__ __forceinline__ Decay decay_of(float g) {
   if constexpr (LOGIT) {
     const float e = __builtin_amdgcn_exp2f(-kLog2e * fabsf(g));
     const float r = __builtin_amdgcn_rcpf(1.f + e), s = e * r;
-    return g < 0.f ? Decay{s, r} : Decay{r, s};
+    return g < 0.f ? Decay{s, r, 0.f} : Decay{r, s, 0.f};
   } else {
-    const float a = __builtin_amdgcn_exp2f(kLog2e * g);
-    return {a, REST ? rest_of_log(g, a) : 0.f};
+    const float l = kLog2e * g, a = __builtin_amdgcn_exp2f(l);
+    return {a, REST ? rest_of_log(g, a) : 0.f, l};
   }
 }
 
-template <Dt IO, Dt G, bool LOGIT, bool COMP>
-__global__ void channel_decode_kernel(Channel p) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i >= static_cast<int64_t>(p.N) * p.D) return;
-  const int64_t n = i / p.D, c = i % p.D;
-  const float x = load_scalar<IO>(p.x, n * p.x_stride + c);
-  const Decay d = decay_of<LOGIT, COMP>(load_scalar<G>(p.g, n * p.g_stride + c));
-  const float s = fmaf(d.a, p.state_in[i], COMP ? d.rest * x : x);
-  p.state_out[i] = s;
-  store_scalar<IO>(p.h, i, s);
-}
-
-template <Dt IO, Dt G, bool LOGIT, bool COMP>
-__global__ void channel_prefill_kernel(Channel p) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i >= static_cast<int64_t>(p.N) * p.D) return;
-  const int64_t n = i / p.D, c = i % p.D;
-  const int lo = min(max(p.cu[n], 0), p.T), hi = min(max(p.cu[n + 1], 0), p.T);
-  float s = p.state_in ? p.state_in[i] : 0.f;
-  for (int64_t t = lo; t < hi; ++t) {
-    const float x = load_scalar<IO>(p.x, t * p.x_stride + c);
-    const Decay d = decay_of<LOGIT, COMP>(load_scalar<G>(p.g, t * p.g_stride + c));
-    s = fmaf(d.a, s, COMP ? d.rest * x : x);
-    store_scalar<IO>(p.h, t * p.D + c, s);
+// V consecutive values of a row as loaded.
+template <Dt D, int V>
+struct Raw {
+  static constexpr int N = D == Dt::BF16 ? (V + 1) / 2 : V;
+  uint32_t w[N];
+  __device__ __forceinline__ void load(const void* base, size_t at) {
+    if constexpr (V == 1) {
+      if constexpr (D == Dt::BF16) w[0] = static_cast<const uint16_t*>(base)[at];
+      else w[0] = static_cast<const uint32_t*>(base)[at];
+    } else {
+      const char* p = static_cast<const char*>(base) + at * (D == Dt::BF16 ? 2 : 4);
+      if constexpr (N == 2) {
+        const uint2 t = *reinterpret_cast<const uint2*>(p);
+        w[0] = t.x; w[1] = t.y;
+      } else {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+          const uint4 t = reinterpret_cast<const uint4*>(p)[i];
+          w[4 * i] = t.x; w[4 * i + 1] = t.y; w[4 * i + 2] = t.z; w[4 * i + 3] = t.w;
+        }
+      }
+    }
   }
-  if (p.state_out) p.state_out[i] = s;
+  __device__ __forceinline__ float operator[](int i) const {
+    if constexpr (D == Dt::F32) return __uint_as_float(w[i]);
+    else return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+  }
+};
+
+template <Dt D, int V>
+__device__ __forceinline__ void store_vec(void* base, size_t at, const float (&x)[V]) {
+  if constexpr (V == 1) {
+    store_scalar<D>(base, at, x[0]);
+  } else if constexpr (D == Dt::F32) {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) p[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+  } else {
+    uint32_t w[V / 2];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i)
+      w[i] = f32_to_bf16_bits(x[2 * i]) | static_cast<uint32_t>(f32_to_bf16_bits(x[2 * i + 1])) << 16;
+    char* p = static_cast<char*>(base) + at * 2;
+    if constexpr (V == 4) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
 }
 
-template <Dt IO, Dt G, bool LOGIT, bool COMP>
-__global__ void channel_backward_kernel(Channel p) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+template <int V>
+__device__ __forceinline__ void load_state(const float* base, size_t at, float (&x)[V]) {
+  if (!base) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = 0.f;
+  } else {
+    Raw<Dt::F32, V> r;
+    r.load(base, at);
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = r[v];
+  }
+}
+
+// State behind a map (A, B) from state s.  A decay of zero forgets s, whatever it is:
+// states do not reach another sequence.
+__device__ __forceinline__ float through(float A, float B, float s) { return A == 0.f ? B : fmaf(A, s, B); }
+
+// Words that workgroups exchange: all ones is "not yet" (a NaN of these bits is
+// replaced by another).
+__device__ __forceinline__ uint32_t word(float x) {
+  const uint32_t w = __float_as_uint(x);
+  return w == kNone ? 0x7FC00000u : w;
+}
+__device__ __forceinline__ void tell(unsigned long long* at, float A, float B) {
+  __hip_atomic_store(at, static_cast<unsigned long long>(word(A)) << 32 | word(B), __ATOMIC_RELAXED,
+                     __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void tell(uint32_t* at, float x) {
+  __hip_atomic_store(at, word(x), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <class T>
+__device__ __forceinline__ T ask(const T* at) {
+  return __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+struct Map {
+  unsigned long long w;
+  __device__ __forceinline__ bool known() const { return static_cast<uint32_t>(w >> 32) != kNone; }
+  __device__ __forceinline__ float A() const { return __uint_as_float(static_cast<uint32_t>(w >> 32)); }
+  __device__ __forceinline__ float B() const { return __uint_as_float(static_cast<uint32_t>(w)); }
+};
+constexpr unsigned long long kNoMap = ~0ull;
+
+// State behind span `span` - 1 of channel ch: from the nearest span whose end state is
+// known, or that forgets what was before it, through the maps of those after it.
+__device__ __forceinline__ float span_start(const Links& k, int span, size_t ch) {
+  for (int tries = 0; tries < kPatience; ++tries) {
+    uint32_t end[kBack];
+    Map map[kBack];
+#pragma unroll
+    for (int i = 0; i < kBack; ++i) {
+      const int j = span - 1 - i;
+      end[i] = kNone;
+      map[i].w = kNoMap;
+      if (j >= 0) {
+        end[i] = ask(k.span_end + j * k.width + ch);
+        map[i].w = ask(k.span_map + j * k.width + ch);
+      }
+    }
+    int from = -1;
+    bool open = true;
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kBack; ++i) {
+      if (!open) continue;
+      if (end[i] != kNone) {
+        s = __uint_as_float(end[i]);
+        from = i;
+        open = false;
+      } else if (!map[i].known()) {
+        open = false;
+      } else if (map[i].A() == 0.f) {
+        s = map[i].B();
+        from = i;
+        open = false;
+      }
+    }
+    if (from >= 0) {
+#pragma unroll
+      for (int i = kBack - 2; i >= 0; --i)
+        if (i < from) s = through(map[i].A(), map[i].B(), s);
+      return s;
+    }
+    __builtin_amdgcn_s_sleep(2);
+  }
+  return __uint_as_float(0x7FC00000u);
+}
+
+// Publishes the map (A, B) of tile `i` (in the order of the pass) for channel ch and
+// returns the state that the tile starts from.
+__device__ __forceinline__ float tile_start(const Links& k, int i, size_t ch, float A, float B) {
+  tell(k.tile_map + i * k.width + ch, A, B);
+  const int span = i / kSpan, at = i % kSpan;
+  const unsigned long long* first = k.tile_map + static_cast<size_t>(span) * kSpan * k.width + ch;
+  Map map[kSpan - 1];
+#pragma unroll
+  for (int j = 0; j < kSpan - 1; ++j) {
+    map[j].w = kNoMap;
+    if (j < at) map[j].w = ask(first + j * k.width);
+  }
+  for (int tries = 0; tries < kPatience; ++tries) {
+    bool all = true;
+#pragma unroll
+    for (int j = 0; j < kSpan - 1; ++j)
+      if (j < at && !map[j].known()) all = false;
+    if (all) break;
+    __builtin_amdgcn_s_sleep(1);
+#pragma unroll
+    for (int j = 0; j < kSpan - 1; ++j)
+      if (j < at && !map[j].known()) map[j].w = ask(first + j * k.width);
+  }
+  // the maps before this tile, joined
+  float pa = 1.f, pb = 0.f;
+#pragma unroll
+  for (int j = 0; j < kSpan - 1; ++j)
+    if (j < at) {
+      pb = through(map[j].A(), map[j].B(), pb);
+      pa *= map[j].A();
+    }
+  const bool last = at == kSpan - 1;
+  const float sa = pa * A, sb = through(A, B, pb);
+  if (last) tell(k.span_map + span * k.width + ch, sa, sb);
+  float s = 0.f;
+  if (span > 0 && pa != 0.f) s = span_start(k, span, ch);
+  if (last) tell(k.span_end + span * k.width + ch, through(sa, sb, s));
+  return through(pa, pb, s);
+}
+
+__global__ void channel_clear_kernel(uint32_t* words, size_t n) {
+  const size_t i = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (i < n) reinterpret_cast<uint4*>(words)[i] = i < 16 ? make_uint4(0, 0, 0, 0) : make_uint4(kNone, kNone, kNone, kNone);
+}
+
+// First m in [0, N] with cu[m] >= t (N + 1 if none), by 64 probes of a wave at a time.
+__device__ __forceinline__ int first_at(const int32_t* cu, int N, int t) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, len = N + 1;  // the answer is in [lo, lo + len]
+  while (len > 0) {
+    const int step = (len + 63) / 64, i = lo + lane * step;
+    const bool below = i < lo + len && cu[i] < t;
+    const int c = __popcll(__ballot(below));
+    if (step == 1) return lo + c;
+    if (c == 0) return lo;
+    lo += (c - 1) * step + 1;
+    const int rest = N + 1 - lo;
+    len = step - 1 < rest ? step - 1 : rest;
+  }
+  return lo;
+}
+
+// Token t of a pass over TT tokens by L per thread, V channels a thread.
+template <int V, int L_>
+struct Shape {
+  static constexpr int L = L_, CC = V == 1 ? 64 : 128, LANES = CC / V, GROUPS = kThreads / LANES,
+                       TT = GROUPS * L;
+};
+
+// BACK: the gradient, from the last token to the first.
+template <Dt IO, Dt G, bool LOGIT, bool COMP, int V, int L, bool BACK>
+__global__ __launch_bounds__(kThreads) void channel_scan_kernel(Channel p, Links k) {
+  using S = Shape<V, L>;
+  constexpr int CC = S::CC, TT = S::TT, GROUPS = S::GROUPS;
+  constexpr bool REST = COMP || (BACK && LOGIT);
+  __shared__ int ticket;
+  __shared__ int first_of[TT], last_of[TT];  // sequence that starts, or ends, at a token
+  __shared__ float map_a[GROUPS][CC], map_b[GROUPS][CC];
+  const int tid = threadIdx.x, lane = tid % S::LANES, group = tid / S::LANES;
+  int work = blockIdx.x;
+  if (k.tiles > 1) {
+    if (tid == 0) ticket = static_cast<int>(atomicAdd(k.ticket, 1u));
+    __syncthreads();
+    work = ticket;
+  }
+  const int order = work / k.cols, col = work % k.cols;
+  const int tile = BACK ? k.tiles - 1 - order : order;
+  const int t0 = tile * TT, tg = t0 + group * L;
+  const int c = col * CC + lane * V;
+  const bool mine = c < p.D;
+  // rows: u is x, or dh of the gradient
+  Raw<IO, V> u[L], x[COMP && BACK ? L : 1], prev[BACK ? L : 1];
+  Raw<G, V> g[L];
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    const int t = tg + i;
+    if (mine && t < p.T) {
+      const size_t row = static_cast<size_t>(t);
+      g[i].load(p.g, row * p.g_stride + c);
+      if constexpr (BACK) {
+        u[i].load(p.dh, row * p.D + c);
+        if (t > 0) prev[i].load(p.h, (row - 1) * p.D + c);
+        else prev[i] = {};
+        if constexpr (COMP) x[i].load(p.x, row * p.x_stride + c);
+      } else {
+        u[i].load(p.x, row * p.x_stride + c);
+      }
+    }
+  }
+  // where sequences start and end among the tile's tokens
+  for (int i = tid; i < TT; i += kThreads) first_of[i] = last_of[i] = -1;
+  __syncthreads();
+  const auto cu = [&](int m) { return min(max(p.cu[m], 0), p.T); };
+  const int valid = cu(p.N), m0 = first_at(p.cu, p.N, t0);
+  const int until = tile == k.tiles - 1 ? p.T : t0 + TT - 1;  // empty sequences are this tile's up to here
+  for (int m = m0 + tid; m <= p.N; m += kThreads) {
+    const int at = cu(m);
+    if (at > t0 + TT) break;
+    if (at < t0) continue;
+    if (m < p.N && at < t0 + TT && cu(m + 1) > at) first_of[at - t0] = m;
+    if (m > 0 && at > t0 && cu(m - 1) < at) last_of[at - 1 - t0] = m - 1;
+  }
+  // empty sequences pass their state on
+  const float* from = BACK ? p.dstate_out : p.state_in;
+  float* to = BACK ? p.dstate_in : p.state_out;
+  if (to && mine)
+    for (int m = m0 + group; m < p.N; m += GROUPS) {
+      const int at = cu(m);
+      if (at > until) break;
+      if (cu(m + 1) > at) continue;
+      float s[V];
+      load_state<V>(from, static_cast<size_t>(m) * p.D + c, s);
+      store_vec<Dt::F32, V>(to, static_cast<size_t>(m) * p.D + c, s);
+    }
+  __syncthreads();
+  // the maps of this thread's tokens, joined.  `enter`: sequences whose first token of
+  // the pass is here; the state of the latest is kept, for its buffer may be written
+  // by the thread that holds the sequence's end (in place) before the walk below.
+  const int* enter = BACK ? last_of : first_of;
+  float A[V], B[V], kept[V];
+  int kept_at = -1;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    A[v] = LOGIT ? 1.f : 0.f;
+    B[v] = 0.f;
+  }
+  bool forget = false;
+  if (mine) {
+#pragma unroll
+    for (int ii = 0; ii < L; ++ii) {
+      const int i = BACK ? L - 1 - ii : ii;
+      if (tg + i >= valid) continue;
+      const int n = enter[group * L + i];
+      if (n >= 0) {
+        load_state<V>(from, static_cast<size_t>(n) * p.D + c, kept);
+        kept_at = i;
+        forget = true;
+#pragma unroll
+        for (int v = 0; v < V; ++v) B[v] = kept[v];
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const Decay d = decay_of<LOGIT, COMP && !BACK>(g[i][v]);
+        if constexpr (BACK) B[v] = d.a * (u[i][v] + B[v]);
+        else B[v] = fmaf(d.a, B[v], COMP ? d.rest * u[i][v] : u[i][v]);
+        if constexpr (LOGIT) A[v] *= d.a;
+        else A[v] += d.log2;  // one exponential of the sum below: one rounding for L decays
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if constexpr (!LOGIT) A[v] = __builtin_amdgcn_exp2f(A[v]);
+      if (forget) A[v] = 0.f;
+    }
+    store_vec<Dt::F32, V>(&map_a[group][0], lane * V, A);
+    store_vec<Dt::F32, V>(&map_b[group][0], lane * V, B);
+  }
+  __syncthreads();
+  // one thread a channel: the tile's map, the state it starts from, and each group's
+  if (tid < CC && col * CC + tid < p.D) {
+    float s = 0.f;
+    if (k.tiles > 1) {
+      float ta = 1.f, tb = 0.f;
+#pragma unroll
+      for (int j = 0; j < GROUPS; ++j) {
+        const int at = BACK ? GROUPS - 1 - j : j;
+        const float ga = map_a[at][tid];
+        tb = through(ga, map_b[at][tid], tb);
+        ta *= ga;
+      }
+      s = tile_start(k, order, static_cast<size_t>(col) * CC + tid, ta, tb);
+    }
+#pragma unroll
+    for (int j = 0; j < GROUPS; ++j) {
+      const int at = BACK ? GROUPS - 1 - j : j;
+      const float ga = map_a[at][tid], gb = map_b[at][tid];
+      map_b[at][tid] = s;
+      s = through(ga, gb, s);
+    }
+  }
+  __syncthreads();
+  if (!mine) return;
+  float s[V];
+  {
+    Raw<Dt::F32, V> r;
+    r.load(&map_b[group][0], lane * V);
+#pragma unroll
+    for (int v = 0; v < V; ++v) s[v] = r[v];
+  }
+  // the walk
+#pragma unroll
+  for (int ii = 0; ii < L; ++ii) {
+    const int i = BACK ? L - 1 - ii : ii, t = tg + i;
+    if (t >= valid) continue;
+    const size_t at = static_cast<size_t>(t) * p.D + c;
+    const int first = first_of[group * L + i], last = last_of[group * L + i];
+    const int in = BACK ? last : first, out = BACK ? first : last;
+    if (in >= 0) {
+      if (i == kept_at) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) s[v] = kept[v];
+      } else {
+        load_state<V>(from, static_cast<size_t>(in) * p.D + c, s);
+      }
+    }
+    if constexpr (BACK) {
+      float before[V], dx[V], dg[V];
+      if (first >= 0) {
+        load_state<V>(p.state_in, static_cast<size_t>(first) * p.D + c, before);
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) before[v] = prev[i][v];
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const Decay d = decay_of<LOGIT, REST>(g[i][v]);
+        const float r = u[i][v] + s[v];
+        s[v] = d.a * r;
+        dx[v] = COMP ? d.rest * r : r;
+        if constexpr (COMP) before[v] -= x[i][v];
+        dg[v] = s[v] * before[v];
+        if constexpr (LOGIT) dg[v] *= d.rest;
+      }
+      store_vec<IO, V>(p.dx, at, dx);
+      store_vec<G, V>(p.dg, at, dg);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const Decay d = decay_of<LOGIT, REST>(g[i][v]);
+        s[v] = fmaf(d.a, s[v], COMP ? d.rest * u[i][v] : u[i][v]);
+      }
+      store_vec<IO, V>(p.h, at, s);
+    }
+    if (out >= 0 && to) store_vec<Dt::F32, V>(to, static_cast<size_t>(out) * p.D + c, s);
+  }
+}
+
+// One token: a thread holds V channels of a sequence.
+template <Dt IO, Dt G, bool LOGIT, bool COMP, int V>
+__global__ __launch_bounds__(kThreads) void channel_decode_kernel(Channel p) {
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * V;
   if (i >= static_cast<int64_t>(p.N) * p.D) return;
   const int64_t n = i / p.D, c = i % p.D;
-  const int lo = min(max(p.cu[n], 0), p.T), hi = min(max(p.cu[n + 1], 0), p.T);
-  float carry = p.dstate_out ? p.dstate_out[i] : 0.f;
-  for (int64_t t = hi - 1; t >= lo; --t) {
-    const Decay d = decay_of<LOGIT, COMP || LOGIT>(load_scalar<G>(p.g, t * p.g_stride + c));
-    const float r = carry + load_scalar<IO>(p.dh, t * p.D + c);
-    float prev = t > lo ? load_scalar<IO>(p.h, (t - 1) * p.D + c) : p.state_in ? p.state_in[i] : 0.f;
-    if (COMP) prev -= load_scalar<IO>(p.x, t * p.x_stride + c);
-    carry = d.a * r;
-    store_scalar<IO>(p.dx, t * p.D + c, COMP ? d.rest * r : r);
-    store_scalar<G>(p.dg, t * p.D + c, carry * prev * (LOGIT ? d.rest : 1.f));
+  Raw<IO, V> x;
+  Raw<G, V> g;
+  float s[V];
+  x.load(p.x, n * p.x_stride + c);
+  g.load(p.g, n * p.g_stride + c);
+  load_state<V>(p.state_in, i, s);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const Decay d = decay_of<LOGIT, COMP>(g[v]);
+    s[v] = fmaf(d.a, s[v], COMP ? d.rest * x[v] : x[v]);
   }
-  if (p.dstate_in) p.dstate_in[i] = carry;
+  store_vec<Dt::F32, V>(p.state_out, i, s);
+  store_vec<IO, V>(p.h, i, s);
 }
 
-// Calls go(IO, G, LOGIT, COMP) for an operand's types and form.
+// Calls go(IO, G, LOGIT, COMP, V) for an operand's types and form.  V fills 16 bytes of
+// a row of io_dtype where rows allow it, and is 1 elsewhere.
 template <class F>
 hipError_t by_form(const Channel& p, F&& go) {
   using std::bool_constant;
-  auto form = [&](auto io, auto g) {
+  using std::integral_constant;
+  const bool vec = p.D % 8 == 0 && p.x_stride % 8 == 0 && p.g_stride % 8 == 0;
+  auto form = [&](auto io, auto g, auto v) {
     if (p.gate == 0)
-      return p.complement ? go(io, g, bool_constant<false>(), bool_constant<true>())
-                          : go(io, g, bool_constant<false>(), bool_constant<false>());
-    return p.complement ? go(io, g, bool_constant<true>(), bool_constant<true>())
-                        : go(io, g, bool_constant<true>(), bool_constant<false>());
+      return p.complement ? go(io, g, bool_constant<false>(), bool_constant<true>(), v)
+                          : go(io, g, bool_constant<false>(), bool_constant<false>(), v);
+    return p.complement ? go(io, g, bool_constant<true>(), bool_constant<true>(), v)
+                        : go(io, g, bool_constant<true>(), bool_constant<false>(), v);
   };
-  const std::integral_constant<Dt, Dt::BF16> bf16;
-  const std::integral_constant<Dt, Dt::F32> f32;
-  if (p.io_dtype == 0) return p.g_dtype == 0 ? form(bf16, bf16) : form(bf16, f32);
-  return p.g_dtype == 0 ? form(f32, bf16) : form(f32, f32);
+  auto width = [&](auto io, auto g) {
+    if (vec) return form(io, g, integral_constant<int, io.value == Dt::BF16 ? 8 : 4>());
+    return form(io, g, integral_constant<int, 1>());
+  };
+  const integral_constant<Dt, Dt::BF16> bf16;
+  const integral_constant<Dt, Dt::F32> f32;
+  if (p.io_dtype == 0) return p.g_dtype == 0 ? width(bf16, bf16) : width(bf16, f32);
+  return p.g_dtype == 0 ? width(f32, bf16) : width(f32, f32);
 }
 
-dim3 grid(const Channel& p) {
-  return dim3(static_cast<unsigned>((static_cast<int64_t>(p.N) * p.D + 255) / 256));
+// Tokens of a tile and channels of a column are 64 at least, and columns are as wide as
+// 128 channels at most.
+constexpr int kLeastTile = 64, kWidestColumn = 128;
+constexpr size_t kTicketBytes = 256;
+
+size_t links_bytes(size_t tiles, size_t width) {
+  const size_t spans = (tiles + kSpan - 1) / kSpan;
+  return tiles > 1 ? kTicketBytes + width * (8 * tiles + 12 * spans) : 0;
+}
+
+template <bool BACK>
+hipError_t launch_scan(const Channel& p, void* workspace, hipStream_t stream) {
+  return by_form(p, [&](auto io, auto g, auto logit, auto comp, auto v) {
+    constexpr int V = decltype(v)::value, L = V == 1 ? 16 : 8;
+    using S = Shape<V, L>;
+    static_assert(S::TT >= kLeastTile && S::CC <= kWidestColumn, "workspace sizes");
+    Links k{};
+    k.tiles = p.T > 0 ? (p.T + S::TT - 1) / S::TT : 1;
+    k.cols = (p.D + S::CC - 1) / S::CC;
+    k.width = static_cast<size_t>(k.cols) * S::CC;
+    if (k.tiles > 1) {
+      const size_t spans = (k.tiles + kSpan - 1) / kSpan;
+      char* at = static_cast<char*>(workspace);
+      k.ticket = reinterpret_cast<uint32_t*>(at);
+      k.tile_map = reinterpret_cast<unsigned long long*>(at + kTicketBytes);
+      k.span_map = k.tile_map + k.tiles * k.width;
+      k.span_end = reinterpret_cast<uint32_t*>(k.span_map + spans * k.width);
+      const size_t n = links_bytes(k.tiles, k.width) / 16;
+      hipLaunchKernelGGL(channel_clear_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256),
+                         0, stream, k.ticket, n);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL((channel_scan_kernel<io.value, g.value, logit.value, comp.value, V, L, BACK>),
+                       dim3(static_cast<unsigned>(k.tiles) * k.cols), dim3(kThreads), 0, stream, p, k);
+    return hipGetLastError();
+  });
 }
 
 }  // namespace
 
-size_t channel_workspace_bytes(int, int) { return 0; }
+size_t channel_workspace_bytes(int T, int D) {
+  const size_t tiles = (static_cast<size_t>(T) + kLeastTile - 1) / kLeastTile;
+  const size_t width = (static_cast<size_t>(D) + kWidestColumn - 1) / kWidestColumn * kWidestColumn;
+  return links_bytes(tiles, width);
+}
 
 hipError_t launch_channel_decode(const Channel& p, hipStream_t stream) {
-  return by_form(p, [&](auto io, auto g, auto logit, auto comp) {
-    hipLaunchKernelGGL((channel_decode_kernel<io.value, g.value, logit.value, comp.value>), grid(p),
-                       dim3(256), 0, stream, p);
+  return by_form(p, [&](auto io, auto g, auto logit, auto comp, auto v) {
+    constexpr int V = decltype(v)::value;
+    const int64_t threads = static_cast<int64_t>(p.N) * p.D / V;
+    hipLaunchKernelGGL((channel_decode_kernel<io.value, g.value, logit.value, comp.value, V>),
+                       dim3(static_cast<unsigned>((threads + kThreads - 1) / kThreads)), dim3(kThreads),
+                       0, stream, p);
     return hipGetLastError();
   });
 }
 
-hipError_t launch_channel_prefill(const Channel& p, void*, hipStream_t stream) {
-  return by_form(p, [&](auto io, auto g, auto logit, auto comp) {
-    hipLaunchKernelGGL((channel_prefill_kernel<io.value, g.value, logit.value, comp.value>), grid(p),
-                       dim3(256), 0, stream, p);
-    return hipGetLastError();
-  });
+hipError_t launch_channel_prefill(const Channel& p, void* workspace, hipStream_t stream) {
+  return launch_scan<false>(p, workspace, stream);
 }
 
-hipError_t launch_channel_backward(const Channel& p, void*, hipStream_t stream) {
-  return by_form(p, [&](auto io, auto g, auto logit, auto comp) {
-    hipLaunchKernelGGL((channel_backward_kernel<io.value, g.value, logit.value, comp.value>), grid(p),
-                       dim3(256), 0, stream, p);
-    return hipGetLastError();
-  });
+hipError_t launch_channel_backward(const Channel& p, void* workspace, hipStream_t stream) {
+  return launch_scan<true>(p, workspace, stream);
 }
 
 }  // namespace gdr

@@ -104,6 +104,19 @@ def test_many_tiles(D, gate, dtype):
     check_all(ref.make([9000, 1, 6155], D, gate, False, dtype, dtype, kind="slow", seed=6))
 
 
+def test_constant_decays_close_to_one():
+    """A decay of e^-1e-4 at every token: its rounding does not add up over 20000 tokens."""
+    d = ref.make([20000], 8, "log", False, "f32", "f32", seed=7)
+    d["g"] = torch.full_like(d["g"], -1e-4)
+    d["x"] = d["x"].abs()
+    want, _ = ref.forward(d)
+    h, _ = forward(d)
+    err = ((h.cpu().double() - want).norm() / want.norm()).item()
+    # a unit in the last place (2^-24) of the decay of 8 tokens, the same one each time, over a
+    # reach of 1e4 tokens, and what the 8 tokens themselves leave
+    assert err < 1e4 / 8 * 2.0 ** -24 + 16 * 2.0 ** -24, err
+
+
 def test_gradient_of_zero_outside_operands():
     """No dstate_out, no states, x left out."""
     d = ref.make([100, 30], 32, "log", False, "bf16", "f32", state=False, seed=8)
