@@ -34,15 +34,14 @@ namespace gdr {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kThreads = 256;
-constexpr int kSpan = 16;  // tiles of a span
-constexpr int kBack = 8;   // spans looked back at together
+constexpr int kSpan = 8;   // tiles of a span
+constexpr int kBack = 4;   // spans looked back at together
 constexpr int kPatience = 1 << 22;
 constexpr uint32_t kNone = 0xFFFFFFFFu;
 
 // What workgroups of one pass tell each other, for `width` channels (whole columns).
 struct Links {
-  uint32_t* ticket;
+  uint32_t* ticket;              // [cols] counters, kTicketStep apart
   unsigned long long* tile_map;  // [tiles][width]
   unsigned long long* span_map;  // [spans][width]
   uint32_t* span_end;            // [spans][width] state behind a span
@@ -71,18 +70,22 @@ __device__ __forceinline__ float rest_of_log(float g, float a) {
 }
 
 // By the hardware's base-2 exponential and reciprocal (one unit in the last place
-// each).  A logit's two halves both come from e^-|z|, so neither is a difference.
+// each).  A logit's 1 - a is e^-z a, no difference; e^-z ends at 2^126, where a is 2^-126
+// (minimum passes a NaN on).
 template <bool LOGIT, bool REST>
 __device__ __forceinline__ Decay decay_of(float g) {
   if constexpr (LOGIT) {
-    const float e = __builtin_amdgcn_exp2f(-kLog2e * fabsf(g));
-    const float r = __builtin_amdgcn_rcpf(1.f + e), s = e * r;
-    return g < 0.f ? Decay{s, r, 0.f} : Decay{r, s, 0.f};
+    const float e = __builtin_amdgcn_exp2f(__builtin_elementwise_minimum(-kLog2e * g, 126.f));
+    const float a = __builtin_amdgcn_rcpf(1.f + e);
+    return {a, e * a, 0.f};
   } else {
     const float l = kLog2e * g, a = __builtin_amdgcn_exp2f(l);
     return {a, REST ? rest_of_log(g, a) : 0.f, l};
   }
 }
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // V consecutive values of a row as loaded.
 template <Dt D, int V>
@@ -101,7 +104,7 @@ struct Raw {
       } else {
 #pragma unroll
         for (int i = 0; i < N / 4; ++i) {
-          const uint4 t = reinterpret_cast<const uint4*>(p)[i];
+          const u32x4 t = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p) + i);
           w[4 * i] = t.x; w[4 * i + 1] = t.y; w[4 * i + 2] = t.z; w[4 * i + 3] = t.w;
         }
       }
@@ -127,8 +130,8 @@ __device__ __forceinline__ void store_vec(void* base, size_t at, const float (&x
     for (int i = 0; i < V / 2; ++i)
       w[i] = f32_to_bf16_bits(x[2 * i]) | static_cast<uint32_t>(f32_to_bf16_bits(x[2 * i + 1])) << 16;
     char* p = static_cast<char*>(base) + at * 2;
-    if constexpr (V == 4) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-    else *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    if constexpr (V == 4) __builtin_nontemporal_store(u32x2{w[0], w[1]}, reinterpret_cast<u32x2*>(p));
+    else __builtin_nontemporal_store(u32x4{w[0], w[1], w[2], w[3]}, reinterpret_cast<u32x4*>(p));
   }
 }
 
@@ -173,6 +176,7 @@ struct Map {
   __device__ __forceinline__ float B() const { return __uint_as_float(static_cast<uint32_t>(w)); }
 };
 constexpr unsigned long long kNoMap = ~0ull;
+constexpr int kTicketStep = 32;  // a column's counter has 128 bytes to itself
 
 // State behind span `span` - 1 of channel ch: from the nearest span whose end state is
 // known, or that forgets what was before it, through the maps of those after it.
@@ -226,6 +230,8 @@ __device__ __forceinline__ float tile_start(const Links& k, int i, size_t ch, fl
   const int span = i / kSpan, at = i % kSpan;
   const unsigned long long* first = k.tile_map + static_cast<size_t>(span) * kSpan * k.width + ch;
   Map map[kSpan - 1];
+  uint32_t before = kNone;  // the end of the span before, mostly known by now
+  if (span > 0) before = ask(k.span_end + (span - 1) * k.width + ch);
 #pragma unroll
   for (int j = 0; j < kSpan - 1; ++j) {
     map[j].w = kNoMap;
@@ -254,14 +260,15 @@ __device__ __forceinline__ float tile_start(const Links& k, int i, size_t ch, fl
   const float sa = pa * A, sb = through(A, B, pb);
   if (last) tell(k.span_map + span * k.width + ch, sa, sb);
   float s = 0.f;
-  if (span > 0 && pa != 0.f) s = span_start(k, span, ch);
+  if (span > 0 && pa != 0.f) s = before != kNone ? __uint_as_float(before) : span_start(k, span, ch);
   if (last) tell(k.span_end + span * k.width + ch, through(sa, sb, s));
   return through(pa, pb, s);
 }
 
-__global__ void channel_clear_kernel(uint32_t* words, size_t n) {
+__global__ void channel_clear_kernel(uint32_t* words, size_t tickets, size_t n) {
   const size_t i = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i < n) reinterpret_cast<uint4*>(words)[i] = i < 16 ? make_uint4(0, 0, 0, 0) : make_uint4(kNone, kNone, kNone, kNone);
+  const uint32_t w = i < tickets ? 0 : kNone;
+  if (i < n) reinterpret_cast<uint4*>(words)[i] = make_uint4(w, w, w, w);
 }
 
 // First m in [0, N] with cu[m] >= t (N + 1 if none), by 64 probes of a wave at a time.
@@ -282,29 +289,28 @@ __device__ __forceinline__ int first_at(const int32_t* cu, int N, int t) {
 }
 
 // Token t of a pass over TT tokens by L per thread, V channels a thread.
-template <int V, int L_>
+template <int V, int L, int THREADS>
 struct Shape {
-  static constexpr int L = L_, CC = V == 1 ? 64 : 128, LANES = CC / V, GROUPS = kThreads / LANES,
-                       TT = GROUPS * L;
+  static constexpr int CC = V == 1 ? 64 : 128, LANES = CC / V, GROUPS = THREADS / LANES, TT = GROUPS * L;
 };
 
 // BACK: the gradient, from the last token to the first.
-template <Dt IO, Dt G, bool LOGIT, bool COMP, int V, int L, bool BACK>
-__global__ __launch_bounds__(kThreads) void channel_scan_kernel(Channel p, Links k) {
-  using S = Shape<V, L>;
+template <Dt IO, Dt G, bool LOGIT, bool COMP, int V, int L, int THREADS, bool BACK>
+__global__ __launch_bounds__(THREADS, BACK ? 1 : IO == Dt::BF16 && G == Dt::F32 && V > 1 ? 3 : 4) void channel_scan_kernel(Channel p, Links k) {
+  using S = Shape<V, L, THREADS>;
   constexpr int CC = S::CC, TT = S::TT, GROUPS = S::GROUPS;
   constexpr bool REST = COMP || (BACK && LOGIT);
   __shared__ int ticket;
   __shared__ int first_of[TT], last_of[TT];  // sequence that starts, or ends, at a token
   __shared__ float map_a[GROUPS][CC], map_b[GROUPS][CC];
   const int tid = threadIdx.x, lane = tid % S::LANES, group = tid / S::LANES;
-  int work = blockIdx.x;
+  const int col = blockIdx.x % k.cols;
+  int order = 0;
   if (k.tiles > 1) {
-    if (tid == 0) ticket = static_cast<int>(atomicAdd(k.ticket, 1u));
+    if (tid == 0) ticket = static_cast<int>(atomicAdd(k.ticket + col * kTicketStep, 1u));
     __syncthreads();
-    work = ticket;
+    order = ticket;
   }
-  const int order = work / k.cols, col = work % k.cols;
   const int tile = BACK ? k.tiles - 1 - order : order;
   const int t0 = tile * TT, tg = t0 + group * L;
   const int c = col * CC + lane * V;
@@ -329,12 +335,12 @@ __global__ __launch_bounds__(kThreads) void channel_scan_kernel(Channel p, Links
     }
   }
   // where sequences start and end among the tile's tokens
-  for (int i = tid; i < TT; i += kThreads) first_of[i] = last_of[i] = -1;
+  for (int i = tid; i < TT; i += THREADS) first_of[i] = last_of[i] = -1;
   __syncthreads();
   const auto cu = [&](int m) { return min(max(p.cu[m], 0), p.T); };
   const int valid = cu(p.N), m0 = first_at(p.cu, p.N, t0);
   const int until = tile == k.tiles - 1 ? p.T : t0 + TT - 1;  // empty sequences are this tile's up to here
-  for (int m = m0 + tid; m <= p.N; m += kThreads) {
+  for (int m = m0 + tid; m <= p.N; m += THREADS) {
     const int at = cu(m);
     if (at > t0 + TT) break;
     if (at < t0) continue;
@@ -382,8 +388,11 @@ __global__ __launch_bounds__(kThreads) void channel_scan_kernel(Channel p, Links
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const Decay d = decay_of<LOGIT, COMP && !BACK>(g[i][v]);
-        if constexpr (BACK) B[v] = d.a * (u[i][v] + B[v]);
-        else B[v] = fmaf(d.a, B[v], COMP ? d.rest * u[i][v] : u[i][v]);
+        if constexpr (BACK) {
+          B[v] = d.a * (u[i][v] + B[v]);
+        } else {
+          B[v] = fmaf(d.a, B[v], COMP ? d.rest * u[i][v] : u[i][v]);
+        }
         if constexpr (LOGIT) A[v] *= d.a;
         else A[v] += d.log2;  // one exponential of the sum below: one rounding for L decays
       }
@@ -477,9 +486,10 @@ __global__ __launch_bounds__(kThreads) void channel_scan_kernel(Channel p, Links
 }
 
 // One token: a thread holds V channels of a sequence.
+constexpr int kDecodeThreads = 256;
 template <Dt IO, Dt G, bool LOGIT, bool COMP, int V>
-__global__ __launch_bounds__(kThreads) void channel_decode_kernel(Channel p) {
-  const int64_t i = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * V;
+__global__ __launch_bounds__(kDecodeThreads) void channel_decode_kernel(Channel p) {
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * kDecodeThreads + threadIdx.x) * V;
   if (i >= static_cast<int64_t>(p.N) * p.D) return;
   const int64_t n = i / p.D, c = i % p.D;
   Raw<IO, V> x;
@@ -503,7 +513,7 @@ template <class F>
 hipError_t by_form(const Channel& p, F&& go) {
   using std::bool_constant;
   using std::integral_constant;
-  const bool vec = p.D % 8 == 0 && p.x_stride % 8 == 0 && p.g_stride % 8 == 0;
+  const int64_t by = p.D | p.x_stride | p.g_stride;
   auto form = [&](auto io, auto g, auto v) {
     if (p.gate == 0)
       return p.complement ? go(io, g, bool_constant<false>(), bool_constant<true>(), v)
@@ -512,7 +522,8 @@ hipError_t by_form(const Channel& p, F&& go) {
                         : go(io, g, bool_constant<true>(), bool_constant<false>(), v);
   };
   auto width = [&](auto io, auto g) {
-    if (vec) return form(io, g, integral_constant<int, io.value == Dt::BF16 ? 8 : 4>());
+    constexpr int V = io.value == Dt::BF16 ? 8 : 4;
+    if (by % V == 0) return form(io, g, integral_constant<int, V>());
     return form(io, g, integral_constant<int, 1>());
   };
   const integral_constant<Dt, Dt::BF16> bf16;
@@ -521,22 +532,23 @@ hipError_t by_form(const Channel& p, F&& go) {
   return p.g_dtype == 0 ? width(f32, bf16) : width(f32, f32);
 }
 
-// Tokens of a tile and channels of a column are 64 at least, and columns are as wide as
-// 128 channels at most.
-constexpr int kLeastTile = 64, kWidestColumn = 128;
-constexpr size_t kTicketBytes = 256;
+// Tokens of a tile and channels of a column are 64 at least, and columns 128 channels at
+// most.
+constexpr int kLeastTile = 64, kLeastColumn = 64, kWidestColumn = 128;
 
-size_t links_bytes(size_t tiles, size_t width) {
+size_t ticket_bytes(size_t cols) { return cols * kTicketStep * sizeof(uint32_t); }
+
+size_t links_bytes(size_t tiles, size_t cols, size_t width) {
   const size_t spans = (tiles + kSpan - 1) / kSpan;
-  return tiles > 1 ? kTicketBytes + width * (8 * tiles + 12 * spans) : 0;
+  return tiles > 1 ? ticket_bytes(cols) + width * (8 * tiles + 12 * spans) : 0;
 }
 
 template <bool BACK>
 hipError_t launch_scan(const Channel& p, void* workspace, hipStream_t stream) {
   return by_form(p, [&](auto io, auto g, auto logit, auto comp, auto v) {
-    constexpr int V = decltype(v)::value, L = V == 1 ? 16 : 8;
-    using S = Shape<V, L>;
-    static_assert(S::TT >= kLeastTile && S::CC <= kWidestColumn, "workspace sizes");
+    constexpr int V = decltype(v)::value, L = V == 1 ? 16 : 8, THREADS = 256;
+    using S = Shape<V, L, THREADS>;
+    static_assert(S::TT >= kLeastTile && S::CC >= kLeastColumn && S::CC <= kWidestColumn, "workspace sizes");
     Links k{};
     k.tiles = p.T > 0 ? (p.T + S::TT - 1) / S::TT : 1;
     k.cols = (p.D + S::CC - 1) / S::CC;
@@ -545,17 +557,17 @@ hipError_t launch_scan(const Channel& p, void* workspace, hipStream_t stream) {
       const size_t spans = (k.tiles + kSpan - 1) / kSpan;
       char* at = static_cast<char*>(workspace);
       k.ticket = reinterpret_cast<uint32_t*>(at);
-      k.tile_map = reinterpret_cast<unsigned long long*>(at + kTicketBytes);
+      k.tile_map = reinterpret_cast<unsigned long long*>(at + ticket_bytes(k.cols));
       k.span_map = k.tile_map + k.tiles * k.width;
       k.span_end = reinterpret_cast<uint32_t*>(k.span_map + spans * k.width);
-      const size_t n = links_bytes(k.tiles, k.width) / 16;
+      const size_t n = links_bytes(k.tiles, k.cols, k.width) / 16;
       hipLaunchKernelGGL(channel_clear_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256),
-                         0, stream, k.ticket, n);
+                         0, stream, k.ticket, ticket_bytes(k.cols) / 16, n);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((channel_scan_kernel<io.value, g.value, logit.value, comp.value, V, L, BACK>),
-                       dim3(static_cast<unsigned>(k.tiles) * k.cols), dim3(kThreads), 0, stream, p, k);
+    hipLaunchKernelGGL((channel_scan_kernel<io.value, g.value, logit.value, comp.value, V, L, THREADS, BACK>),
+                       dim3(static_cast<unsigned>(k.tiles) * k.cols), dim3(THREADS), 0, stream, p, k);
     return hipGetLastError();
   });
 }
@@ -565,7 +577,7 @@ hipError_t launch_scan(const Channel& p, void* workspace, hipStream_t stream) {
 size_t channel_workspace_bytes(int T, int D) {
   const size_t tiles = (static_cast<size_t>(T) + kLeastTile - 1) / kLeastTile;
   const size_t width = (static_cast<size_t>(D) + kWidestColumn - 1) / kWidestColumn * kWidestColumn;
-  return links_bytes(tiles, width);
+  return links_bytes(tiles, width / kLeastColumn, width);
 }
 
 hipError_t launch_channel_decode(const Channel& p, hipStream_t stream) {
@@ -573,7 +585,7 @@ hipError_t launch_channel_decode(const Channel& p, hipStream_t stream) {
     constexpr int V = decltype(v)::value;
     const int64_t threads = static_cast<int64_t>(p.N) * p.D / V;
     hipLaunchKernelGGL((channel_decode_kernel<io.value, g.value, logit.value, comp.value, V>),
-                       dim3(static_cast<unsigned>((threads + kThreads - 1) / kThreads)), dim3(kThreads),
+                       dim3(static_cast<unsigned>((threads + kDecodeThreads - 1) / kDecodeThreads)), dim3(kDecodeThreads),
                        0, stream, p);
     return hipGetLastError();
   });
