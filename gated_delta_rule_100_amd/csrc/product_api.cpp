@@ -12,7 +12,8 @@ namespace {
 
 using gdr::fail;
 
-constexpr int kMaxSize = 1 << 24;
+// (a tile's rows are addressed by 32 bits)
+constexpr int kMaxSize = 1 << 24, kMaxDepth = 1 << 22;
 
 }  // namespace
 
@@ -21,8 +22,8 @@ extern "C" {
 gdr_status gdr_product8(const void* a, const float* a_scale, const void* w, const float* w_scale,
                         void* out, int M, int N, int K, gdr_dtype out_dtype, gdr_stream_t stream) {
   const char* who = "gdr_product8";
-  if (M < 0 || N <= 0 || K <= 0 || M > kMaxSize || N > kMaxSize || K > kMaxSize ||
-      static_cast<int64_t>(M) * N >= int64_t{1} << 32)
+  if (M < 0 || N <= 0 || K <= 0 || M > kMaxSize || N > kMaxSize || K > kMaxDepth ||
+      static_cast<int64_t>(M) * N >= int64_t{1} << 36)
     return fail(GDR_ERR_INVALID_ARG, "%s: M=%d N=%d K=%d", who, M, N, K);
   if (K % 16 != 0) return fail(GDR_ERR_UNSUPPORTED, "%s: K=%d is not a multiple of 16", who, K);
   if (out_dtype != GDR_BF16 && out_dtype != GDR_FP32)
