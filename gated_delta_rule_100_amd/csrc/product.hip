@@ -19,10 +19,21 @@ namespace {
 
 typedef _Float16 halfx2 __attribute__((ext_vector_type(2)));
 typedef _Float16 halfx8 __attribute__((ext_vector_type(8)));
+typedef uint32_t uintx4 __attribute__((ext_vector_type(4)));
 typedef int intx4 __attribute__((ext_vector_type(4)));
 typedef int intx8 __attribute__((ext_vector_type(8)));
 
 constexpr int kBlock = 128;
+
+// f(0), f(1), ... with their arguments as constants (the loop is too long for the compiler
+// to unroll).
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void steps(const F& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>());
+    steps<N, I + 1>(f);
+  }
+}
 
 // A lane's 32 values of a row, as the matrix instructions take them.
 template <Dt OUT>
@@ -87,14 +98,37 @@ __device__ __forceinline__ void store4(void* out, size_t at, int some, bool vec,
   }
 }
 
-// 16 or 4 bytes a lane from memory to consecutive LDS.
-__device__ __forceinline__ void copy16(const void* src, void* lds) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(src),
-                                   (__attribute__((address_space(3))) void*)(lds), 16, 0, 0);
+// Two tiles side by side (n = 4 q + r of each at lane q) as bf16, eight consecutive n of both
+// together a lane: lane q has n = 8 q to 8 q + 7.  Halves of the wave change places, then its
+// rows of 16 lanes; the lanes of one row m go the same way, so all of them are to be there.
+__device__ __forceinline__ uintx4 pair_of_tiles(floatx4 a, floatx4 b) {
+  const auto two = [](float lo, float hi) {
+    return f32_to_bf16_bits(lo) | static_cast<uint32_t>(f32_to_bf16_bits(hi)) << 16;
+  };
+  const uint32_t x[2] = {two(a[0], a[1]), two(a[2], a[3])}, y[2] = {two(b[0], b[1]), two(b[2], b[3])};
+  uint32_t lo[2], hi[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const auto h = __builtin_amdgcn_permlane32_swap(x[i], y[i], false, false);
+    const auto r = __builtin_amdgcn_permlane16_swap(h[0], h[1], false, false);
+    lo[i] = r[0];
+    hi[i] = r[1];
+  }
+  return uintx4{lo[0], lo[1], hi[0], hi[1]};
 }
-__device__ __forceinline__ void copy4(const void* src, void* lds) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(src),
-                                   (__attribute__((address_space(3))) void*)(lds), 4, 0, 0);
+
+// 16 or 4 bytes a lane from memory, `off` behind a scalar base, to consecutive LDS.  The
+// compiler would wait for the builtin's copy before every later read of LDS, of the other
+// buffer too; written out, the copy has no register that it returns, and arrive() below is
+// what waits for it.
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) void*)(p)));
+}
+__device__ __forceinline__ void copy16(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "m0");
+}
+__device__ __forceinline__ void copy4(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base) : "m0");
 }
 
 // Tile (im, in) of the grid's tm x tn for workgroup `id`: workgroups go round the 8 XCDs,
@@ -108,125 +142,277 @@ __device__ __forceinline__ void tile_of(int id, int tm, int tn, int* im, int* in
   *in = rest / rows;
 }
 
-// A BM x BN tile by WM x WN waves.  Blocks of 128 k of both operands go through LDS,
-// straight from memory, one while the one before it is multiplied.  A row of a block is
-// 8 pieces of 16 bytes, piece c at c ^ (row / 2 % 8): the 16 rows that lanes read at once
-// then fall on all banks.
-template <Dt OUT, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(WM * WN * 64, 2) void product8_tile_kernel(Product8 p, int tm, int tn) {
-  constexpr int WAVES = WM * WN, MT = BM / WM / 16, NT = BN / WN / 16;
+// Tiles of BM x BN by WM x WN waves, in KG groups of them that take every KG-th block of 128 k
+// and add up at a tile's end; a workgroup stays for every gridDim.x-th tile and takes the
+// blocks of all of them as one sequence.  Blocks of both operands go through NB buffers of LDS
+// a group, straight from memory.  A wave holds a block's rows of a in registers and passes
+// over its rows of w; during the last pass it reads the next block's rows of a in the places
+// of those that it has used, so the one barrier of a block stands before that pass, in the
+// middle of products whose operands are there:
+//   - behind the barrier the next block has landed, and nobody reads this one's buffer any
+//     more: its copies for NB blocks on start;
+//   - no product waits for LDS, and a tile's first products not for the stores of the tile
+//     before it.
+// A row of a block is 8 pieces of 16 bytes, piece c at c ^ (row / 2 % 8): the 16 rows that
+// lanes read at once then fall on all banks.  The scales of a come 8 blocks at a time, since
+// a row's are 32 bytes of one line then (a third of all L2 requests were for them, one by one).
+//
+// 256 x 256, bf16 results, 16384 x 8192 x 2048: 279 us, 1970 TFLOP/s (348 with the barrier
+// between blocks and copies waited for there); 8192 x 8192 x 8192: 467 us, 2350 TFLOP/s.
+// What bounds it: the matrix cores are busy 60% of the time at the 1.9 GHz that the card
+// holds under this load (4 multiply-adds behind each product share the issue slots of two
+// waves), and at K = 2048 the results' 268 MB take 53 us more, as if nothing ran beside them.
+constexpr int kScales = 8;
+template <Dt OUT, int BM, int BN, int WM, int WN, int KG, int NB>
+__global__ __launch_bounds__(WM * WN * KG * 64, 2) void product8_tile_kernel(Product8 p, int tm, int tn) {
+  constexpr int WAVES = WM * WN, MT = BM / WM / 16, NT = BN / WN / 16, STEPS = MT * NT;
   static_assert(kBlock % (BN / WN) == 0, "a wave's columns share a scale");
   constexpr int COPIES = (BM + BN) / 8 / WAVES;  // of 8 rows, a wave
-  static_assert(COPIES * WAVES * 8 == BM + BN && BM % 8 == 0, "copies");
-  struct Stage {
-    uint8_t rows[BN + BM][kBlock];  // w, then a
-    float sa[BM < 64 ? 64 : BM];
-  };
-  __shared__ Stage stage[2];
-  int im, in;
-  tile_of(blockIdx.x, tm, tn, &im, &in);
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  constexpr int SCALES = BM * kScales / 64 / WAVES;
+  static_assert(COPIES * WAVES * 8 == BM + BN && BN / 8 % WAVES == 0, "copies");
+  static_assert(SCALES * WAVES * 64 == BM * kScales, "scales");
+  static_assert(WAVES % 2 == 0, "a lane's piece");
+  static_assert(NT % 2 == 0, "rows of w in two places");
+  __shared__ uint8_t all_rows[KG][NB][BN + BM][kBlock];  // of w, then of a
+  __shared__ float all_scales[KG][NB][BM][kScales];
+  __shared__ floatx4 sums[KG > 1 ? KG - 1 : 1][KG > 1 ? WAVES : 1][KG > 1 ? STEPS : 1][64];
+  const int lane = threadIdx.x & 63, any_wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kg = any_wave / WAVES, wave = any_wave % WAVES;
   const int wm = wave / WN, wn = wave % WN, c16 = lane & 15, q = lane >> 4;
-  const int m0 = im * BM, n0 = in * BN, kb = (p.K + kBlock - 1) / kBlock;
-  const uint8_t* a0 = p.a + static_cast<size_t>(m0) * p.K;
-  const uint8_t* w0 = p.w + static_cast<size_t>(n0) * p.K;
-  // bytes from a tile's first row to what this lane copies; rows past the end are the last
-  uint32_t from[COPIES];
-  int piece[COPIES];
-#pragma unroll
-  for (int i = 0; i < COPIES; ++i) {
-    const int g = i * WAVES + wave, r = g * 8 + (lane >> 3);
-    piece[i] = (lane & 7) ^ (r >> 1 & 7);
-    const int row = g < BN / 8 ? min(r, p.N - 1 - n0) : min(r - BN, p.M - 1 - m0);
-    from[i] = static_cast<uint32_t>(row) * p.K + piece[i] * 16;
-  }
-  const int sm = min(wave * 64 + lane, min(BM - 1, p.M - 1 - m0));
-  const float* sa0 = p.a_scale + static_cast<size_t>(m0 + sm) * kb;
-  const float* sw0 = p.w_scale + static_cast<size_t>(min(n0 + wn * (BN / WN), p.N - 1) / kBlock) * kb;
-  const auto issue = [&](int b) {
-    Stage& s = stage[b & 1];
-    const bool whole = (b + 1) * kBlock <= p.K;
-#pragma unroll
-    for (int i = 0; i < COPIES; ++i) {
-      const int g = i * WAVES + wave;
-      const uint8_t* src = (g < BN / 8 ? w0 : a0) + static_cast<size_t>(b) * kBlock;
-      if (whole) {
-        copy16(src + from[i], s.rows[g * 8]);
-      } else {  // the last block: zeros behind the rows' end
-        intx4 x = {0, 0, 0, 0};
-        if (b * kBlock + piece[i] * 16 < p.K) x = *reinterpret_cast<const intx4*>(src + from[i]);
-        *reinterpret_cast<intx4*>(&s.rows[g * 8][0] + lane * 16) = x;
-      }
-    }
-    if (wave * 64 < BM) copy4(sa0 + b, s.sa + wave * 64);
+  const int kb = (p.K + kBlock - 1) / kBlock, turns = (kb + KG - 1) / KG, tiles = tm * tn;
+  auto& rows = all_rows[kg];
+  auto& scales = all_scales[kg];
+  // The lane for addresses that are needed once in a while: formed from it each time, they
+  // take no registers in between.
+  const auto anew = [&] {
+    int l = lane;
+    asm volatile("" : "+v"(l));
+    return l;
   };
-  floatx4 acc[MT][NT];
+  // A place in the sequence of blocks, the buffer of its rows and that of its scales; behind
+  // the last tile it stays there.
+  struct Cursor {
+    int tile, m0, n0, turn, rows, scales;
+  };
+  const auto block = [&](const Cursor& c) { return c.turn * KG + kg; };
+  const auto enter = [&](Cursor& c) {
+    if (c.tile >= tiles) return;
+    int im, in;
+    tile_of(c.tile, tm, tn, &im, &in);
+    c.m0 = im * BM;
+    c.n0 = in * BN;
+  };
+  const auto advance = [&](Cursor& c) {
+    c.rows = c.rows + 1 == NB ? 0 : c.rows + 1;
+    if (++c.turn == turns) {
+      c.turn = 0;
+      c.tile += gridDim.x;
+      enter(c);
+    }
+    if (c.turn % kScales == 0) c.scales = c.scales + 1 == NB ? 0 : c.scales + 1;
+  };
+  // A lane copies the same piece of each row; rows past the end are the last.  Where a last
+  // block has no such piece, it takes the row's first bytes of the block, and writes zeros
+  // over them before they are read.
+  const uint32_t piece = ((lane & 7) ^ ((wave * 4 + (lane >> 4)) & 7)) * 16;
+  const auto missing = [&](int b) { return b * kBlock + static_cast<int>(piece) >= p.K; };
+  const auto copy_rows = [&](const Cursor& c, auto copy) {
+    constexpr int i = decltype(copy)::value;
+    constexpr bool w = i < BN / 8 / WAVES;
+    const int g = i * WAVES + wave, r = g * 8 + (anew() >> 3);
+    const int row = w ? min(r, p.N - 1 - c.n0) : min(r - BN, p.M - 1 - c.m0);
+    const uint8_t* src = (w ? p.w + static_cast<size_t>(c.n0) * p.K : p.a + static_cast<size_t>(c.m0) * p.K) +
+                         static_cast<size_t>(min(block(c), kb - 1)) * kBlock;
+    copy16(src, static_cast<uint32_t>(row) * p.K + (missing(block(c)) ? 0u : piece), lds_address(rows[c.rows][g * 8]));
+  };
+  const auto copy_scales = [&](const Cursor& c) {
+    if (c.turn % kScales != 0) return;
 #pragma unroll
-  for (int j = 0; j < MT; ++j)
-#pragma unroll
-    for (int i = 0; i < NT; ++i) acc[j][i] = floatx4{0.f, 0.f, 0.f, 0.f};
-  const int near = c16 * kBlock + ((q ^ (c16 >> 1)) * 16), far = near ^ 64;
-  issue(0);
-  float next_sw = sw0[0];
-  for (int b = 0; b < kb; ++b) {
-    const float sw = next_sw;
+    for (int i = 0; i < SCALES; ++i) {
+      const int r = (i * WAVES + wave) * (64 / kScales), l = anew();
+      const int m = min(r + l / kScales, p.M - 1 - c.m0), b = min(block(c) + l % kScales * KG, kb - 1);
+      copy4(p.a_scale + static_cast<size_t>(c.m0) * kb, (static_cast<uint32_t>(m) * kb + b) * 4,
+            lds_address(scales[c.scales][r]));
+    }
+  };
+  // Waits for this wave's LDS accesses and for all its memory accesses but the copies of the
+  // NB - 2 blocks behind the next (scales among them only make it wait for more) and, where
+  // they came last, a whole tile's stores; then for the other waves.
+  constexpr int STORES = OUT == Dt::BF16 ? STEPS / 2 : STEPS, LATER = (NB - 2) * COPIES;
+  static_assert(LATER + STORES < 64, "vmcnt");
+  const auto arrive = [&](bool stores) {
+    constexpr int all = LATER + STORES;
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0), lgkmcnt(0)
+    if (stores) __builtin_amdgcn_s_waitcnt(0x0070 | (all & 15) | (all >> 4) << 14);
+    else __builtin_amdgcn_s_waitcnt(0x0070 | (LATER & 15) | (LATER >> 4) << 14);  // lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if (b + 1 < kb) {
-      next_sw = sw0[b + 1];
-      issue(b + 1);
-    }
-    const Stage& s = stage[b & 1];
-    const uint8_t* wr = s.rows[wn * (BN / WN)];
-    const uint8_t* ar = s.rows[BN + wm * (BM / WM)];
-    const auto read = [&](const uint8_t* rows, int t) {
-      return join(*reinterpret_cast<const intx4*>(rows + t * 16 * kBlock + near),
-                  *reinterpret_cast<const intx4*>(rows + t * 16 * kBlock + far));
-    };
-    Frag<OUT> wf[NT];
+  };
+  const int near = c16 * kBlock + ((q ^ (c16 >> 1)) * 16), far = near ^ 64;
+  const auto read = [&](const uint8_t* at, int t) {
+    return join(*reinterpret_cast<const intx4*>(at + t * 16 * kBlock + near),
+                *reinterpret_cast<const intx4*>(at + t * 16 * kBlock + far));
+  };
+  const auto rows_of_w = [&](int buffer) { return rows[buffer][wn * (BN / WN)]; };
+  const auto rows_of_a = [&](int buffer) { return rows[buffer][BN + wm * (BM / WM)]; };
+  const auto zero_missing = [&](int buffer) {
+    const int l = anew();
 #pragma unroll
-    for (int i = 0; i < NT; ++i) wf[i].set(read(wr, i));
-    float scale[MT];
+    for (int i = 0; i < COPIES; ++i)
+      *reinterpret_cast<intx4*>(&rows[buffer][(i * WAVES + wave) * 8][0] + l * 16) = intx4{0, 0, 0, 0};
+  };
+  // A block's scales of this lane's rows of a, and the wave's scale of w.
+  const auto scale_of_a = [&](const Cursor& c, int j) {
+    return scales[c.scales][wm * (BM / WM) + j * 16 + c16][c.turn % kScales];
+  };
+  const auto scale_of_w = [&](const Cursor& c) {  // (constant address space: a scalar load)
+    return ((const __attribute__((address_space(4))) float*)(p.w_scale))
+        [static_cast<size_t>(min(c.n0 + wn * (BN / WN), p.N - 1) / kBlock) * kb + min(block(c), kb - 1)];
+  };
+
+  // `to` is what is copied, `next` what is read, `now` what is multiplied
+  constexpr int HALF = COPIES / 2;
+  Cursor to{static_cast<int>(blockIdx.x), 0, 0, 0, 0, 0};
+  enter(to);
+  Cursor now = to, next = to;
+  advance(next);
 #pragma unroll
-    for (int j = 0; j < MT; ++j) scale[j] = s.sa[wm * (BM / WM) + j * 16 + c16] * sw;
-    floatx4 part[2][NT];
-#pragma unroll
-    for (int j = 0; j <= MT; ++j) {
-      if (j < MT) {
-        Frag<OUT> af;
-        af.set(read(ar, j));
-#pragma unroll
-        for (int i = 0; i < NT; ++i) part[j & 1][i] = block_sum(wf[i], af);
-      }
-      if (j > 0) {
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            acc[j - 1][i][r] = fmaf(scale[j - 1], part[(j - 1) & 1][i][r], acc[j - 1][i][r]);
-      }
-    }
+  for (int d = 0; d < NB - 1; ++d) {
+    copy_scales(to);
+    steps<COPIES>([&](auto i) { copy_rows(to, i); });
+    advance(to);
   }
-  const bool vec = p.N % 4 == 0;
+  arrive(false);
+  const bool ragged = p.K % (kBlock * KG) != 0;
+  if (ragged && turns == 1) {
+    if (missing(kg)) zero_missing(0);
+    arrive(false);
+  }
+  copy_scales(to);
+  steps<HALF>([&](auto i) { copy_rows(to, i); });
+  intx8 ar[MT], wr[2];
+  float sa[MT], sw = scale_of_w(now);
 #pragma unroll
   for (int j = 0; j < MT; ++j) {
-    const int m = m0 + wm * (BM / WM) + j * 16 + c16;
-    if (m >= p.M) continue;
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const int n = n0 + wn * (BN / WN) + i * 16 + 4 * q;
-      if (n < p.N) store4<OUT>(p.out, static_cast<size_t>(m) * p.N + n, p.N - n, vec, acc[j][i]);
-    }
+    ar[j] = read(rows_of_a(0), j);
+    sa[j] = scale_of_a(now, j);
   }
+  wr[0] = read(rows_of_w(0), 0);
+  bool copied = false, stores = false;  // all of `to` is on its way; stores came after it
+  while (now.tile < tiles) {
+    floatx4 acc[MT][NT];
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (int i = 0; i < NT; ++i) acc[j][i] = floatx4{0.f, 0.f, 0.f, 0.f};
+    int m_at = 0, n_at = 0;
+    int left = turns;
+    do {
+    float next_sw = 0.f;
+    Frag<OUT> af[MT], wf;
+    floatx4 part[4];
+    float scale[MT];
+    steps<STEPS + 3>([&](auto step) {
+      constexpr int t = decltype(step)::value, i = t / MT, j = t % MT;
+      if constexpr (t < STEPS) {
+        if constexpr (j == 0) {
+          if constexpr (i == NT - 1) {  // the next block has landed
+            arrive(stores);
+            if (ragged && next.turn == turns - 1) {
+              if (missing(block(next))) zero_missing(next.rows);
+              arrive(stores);
+            }
+            next_sw = scale_of_w(next);
+            advance(to);
+            copy_scales(to);
+          }
+          wf.set(wr[i & 1]);
+          wr[(i + 1) & 1] = i < NT - 1 ? read(rows_of_w(now.rows), i + 1) : read(rows_of_w(next.rows), 0);
+        }
+        if constexpr (i == 0) {
+          af[j].set(ar[j]);
+          scale[j] = sa[j] * sw;
+        }
+        part[t & 3] = block_sum(wf, af[j]);
+        if constexpr (i == NT - 1) {
+          ar[j] = read(rows_of_a(next.rows), j);
+          sa[j] = scale_of_a(next, j);
+        }
+        // half of the copies in this pass, half in the next block's first
+        steps<(j + 1) * HALF / MT - j * HALF / MT>([&](auto c) {
+          constexpr int at = j * HALF / MT + decltype(c)::value;
+          if constexpr (i == NT - 1) copy_rows(to, std::integral_constant<int, at>());
+          if constexpr (i == 0)
+            if (!copied) copy_rows(to, std::integral_constant<int, HALF + at>());
+        });
+      }
+      // a block sum meets the scales three products later
+      if constexpr (t >= 3) {
+        constexpr int u = t - 3;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          acc[u % MT][u / MT][r] = fmaf(scale[u % MT], part[u & 3][r], acc[u % MT][u / MT][r]);
+        // (here: the compiler would put it off past the branches of a block's middle, with
+        // every block sum in registers until then)
+        asm volatile("" : "+v"(acc[u % MT][u / MT]));
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    sw = next_sw;
+    m_at = now.m0;
+    n_at = now.n0;
+    now = next;
+    advance(next);
+    copied = stores = false;
+    } while (--left > 0);
+    steps<COPIES - HALF>([&](auto c) { copy_rows(to, std::integral_constant<int, HALF + decltype(c)::value>()); });
+    copied = true;
+    if constexpr (KG > 1) {
+      if (kg > 0) steps<STEPS>([&](auto t) { sums[kg - 1][wave][decltype(t)::value][lane] = acc[decltype(t)::value / NT][decltype(t)::value % NT]; });
+      lds_barrier();
+      if (kg > 0) continue;
+      steps<STEPS>([&](auto t) {
+#pragma unroll
+        for (int g = 0; g < KG - 1; ++g) acc[decltype(t)::value / NT][decltype(t)::value % NT] += sums[g][wave][decltype(t)::value][lane];
+      });
+    }
+    stores = m_at + BM <= p.M && n_at + BN <= p.N && p.N % 8 == 0;
+    asm volatile("" ::: "memory");
+    const bool vec = p.N % 4 == 0;
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+      const int l = anew(), m = m_at + wm * (BM / WM) + j * 16 + (l & 15);
+      const int n0 = n_at + wn * (BN / WN);
+      if (m >= p.M) continue;
+      const size_t at = static_cast<size_t>(m) * p.N;
+      if (OUT == Dt::BF16 && p.N % 8 == 0) {
+        // lanes change parts, so that four of them have 64 bytes of a row
+#pragma unroll
+        for (int i = 0; i < NT; i += 2) {
+          const int n = n0 + i * 16 + (l >> 4) * 8;
+          const uintx4 x = pair_of_tiles(acc[j][i], acc[j][i + 1]);
+          if (n < p.N) *reinterpret_cast<uintx4*>(static_cast<uint16_t*>(p.out) + at + n) = x;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          const int n = n0 + i * 16 + 4 * (l >> 4);
+          if (n < p.N) store4<OUT>(p.out, at + n, p.N - n, vec, acc[j][i]);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    asm volatile("" ::: "memory");
+  }
+  __builtin_amdgcn_s_waitcnt(0x0070);  // no copy outlives the workgroup's LDS
 }
 
-// Few rows: up to 16 MT of a against 16 NT of w, whose bytes come straight from memory to
-// the matrix instructions' registers.  The waves take every kWaves-th block of k and add up
-// in LDS at the end.
+// Few outputs: 16 MT rows of a against 16 NT of w, whose bytes come straight from memory to
+// the matrix instructions' registers.  The waves take every kWaves-th block of k, without a
+// barrier, and add up in LDS at the end.  1 x 2048 x 2048: 3.8 us, 16 x 8192 x 4096: 10.0 us,
+// 3.4 TB/s (a launch and one read of memory each).
 constexpr int kWaves = 8;
-template <Dt OUT, int MT, int NT>
+template <Dt OUT, int MT, int NT, int AHEAD>
 __global__ __launch_bounds__(kWaves * 64) void product8_rows_kernel(Product8 p) {
   __shared__ floatx4 sums[kWaves][MT * NT][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -243,52 +429,84 @@ __global__ __launch_bounds__(kWaves * 64) void product8_rows_kernel(Product8 p) 
 #pragma unroll
   for (int i = 0; i < NT; ++i) wr[i] = p.w + static_cast<size_t>(min(n0 + i * 16 + c16, p.N - 1)) * p.K + q * 16;
   const float* sw = p.w_scale + static_cast<size_t>(n0 / kBlock) * kb;
+  // A block as loaded.  Lanes behind the rows' end load the row's first bytes, without a
+  // branch, and have them taken for zeros when they are used.
   struct Block {
-    intx8 w[NT], a[MT];
-    float scale[MT];
+    intx4 w[NT][2], a[MT][2];
+    float sa[MT], sw;
   };
   const auto read = [&](int b, Block& x) {
-    const int64_t k = static_cast<int64_t>(b) * kBlock;
-    const bool lo = k + q * 16 < p.K, hi = k + 64 + q * 16 < p.K;
-    const auto row = [&](const uint8_t* r) {
-      const intx4 zero = {0, 0, 0, 0};
-      return join(lo ? *reinterpret_cast<const intx4*>(r + k) : zero,
-                  hi ? *reinterpret_cast<const intx4*>(r + k + 64) : zero);
-    };
+    const int k = b * kBlock, lo = k + q * 16 < p.K ? k : 0, hi = k + 64 + q * 16 < p.K ? k + 64 : 0;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) x.w[i] = row(wr[i]);
+    for (int i = 0; i < NT; ++i) {
+      x.w[i][0] = *reinterpret_cast<const intx4*>(wr[i] + lo);
+      x.w[i][1] = *reinterpret_cast<const intx4*>(wr[i] + hi);
+    }
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
-      x.a[j] = row(ar[j]);
-      x.scale[j] = sa[j][b] * sw[b];
+      x.a[j][0] = *reinterpret_cast<const intx4*>(ar[j] + lo);
+      x.a[j][1] = *reinterpret_cast<const intx4*>(ar[j] + hi);
+      x.sa[j] = sa[j][b];
     }
+    x.sw = sw[b];
   };
   floatx4 acc[MT][NT];
 #pragma unroll
   for (int j = 0; j < MT; ++j)
 #pragma unroll
     for (int i = 0; i < NT; ++i) acc[j][i] = floatx4{0.f, 0.f, 0.f, 0.f};
-  Block x, y;
-  if (wave < kb) read(wave, x);
-  for (int b = wave; b < kb; b += kWaves) {
-    const bool more = b + kWaves < kb;
-    if (more) read(b + kWaves, y);
+  const auto multiply = [&](int b, Block& x) {
+    if ((b + 1) * kBlock > p.K) {
+      const intx4 zero = {0, 0, 0, 0};
+      const bool lo = b * kBlock + q * 16 < p.K, hi = b * kBlock + 64 + q * 16 < p.K;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        x.w[i][0] = lo ? x.w[i][0] : zero;
+        x.w[i][1] = hi ? x.w[i][1] : zero;
+      }
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        x.a[j][0] = lo ? x.a[j][0] : zero;
+        x.a[j][1] = hi ? x.a[j][1] : zero;
+      }
+    }
     Frag<OUT> wf[NT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) wf[i].set(x.w[i]);
+    for (int i = 0; i < NT; ++i) wf[i].set(join(x.w[i][0], x.w[i][1]));
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
       Frag<OUT> af;
-      af.set(x.a[j]);
+      af.set(join(x.a[j][0], x.a[j][1]));
+      const float scale = x.sa[j] * x.sw;
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         const floatx4 part = block_sum(wf[i], af);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[j][i][r] = fmaf(x.scale[j], part[r], acc[j][i][r]);
+        for (int r = 0; r < 4; ++r) acc[j][i][r] = fmaf(scale, part[r], acc[j][i][r]);
       }
     }
-    if (more) x = y;
-  }
+  };
+  // `mine` blocks, AHEAD of them on their way: the loop's reads are unconditional, so that a
+  // block is waited for without those behind it.
+  const int mine = wave < kb ? (kb - wave + kWaves - 1) / kWaves : 0;
+  const auto block = [&](int s) { return wave + s * kWaves; };
+  Block ring[AHEAD];
+#pragma unroll
+  for (int d = 0; d < AHEAD; ++d)
+    if (d < mine) read(block(d), ring[d]);
+  int s = 0;
+  for (; s + 2 * AHEAD <= mine; s += AHEAD)
+#pragma unroll
+    for (int d = 0; d < AHEAD; ++d) {
+      multiply(block(s + d), ring[d]);
+      read(block(s + AHEAD + d), ring[d]);
+    }
+#pragma unroll
+  for (int d = 0; d < 2 * AHEAD - 1; ++d)
+    if (s + d < mine) {
+      multiply(block(s + d), ring[d % AHEAD]);
+      if (d < AHEAD - 1 && s + AHEAD + d < mine) read(block(s + AHEAD + d), ring[d % AHEAD]);
+    }
 #pragma unroll
   for (int j = 0; j < MT; ++j)
 #pragma unroll
@@ -306,32 +524,50 @@ __global__ __launch_bounds__(kWaves * 64) void product8_rows_kernel(Product8 p) 
   }
 }
 
-template <Dt OUT, int BM, int BN, int WM, int WN>
+template <Dt OUT, int BM, int BN, int WM, int WN, int KG, int NB>
 hipError_t launch_tiles(const Product8& p, hipStream_t stream) {
   const int tm = (p.M + BM - 1) / BM, tn = (p.N + BN - 1) / BN;
-  hipLaunchKernelGGL((product8_tile_kernel<OUT, BM, BN, WM, WN>), dim3(static_cast<unsigned>(tm) * tn),
-                     dim3(WM * WN * 64), 0, stream, p, tm, tn);
+  const int64_t tiles = static_cast<int64_t>(tm) * tn, most = WM * WN * KG > 4 ? 256 : 512;
+  hipLaunchKernelGGL((product8_tile_kernel<OUT, BM, BN, WM, WN, KG, NB>), dim3(static_cast<unsigned>(tiles < most ? tiles : most)),
+                     dim3(WM * WN * KG * 64), 0, stream, p, tm, tn);
   return hipGetLastError();
 }
 
-template <Dt OUT, int MT, int NT>
+template <Dt OUT, int MT, int NT, int AHEAD>
 hipError_t launch_rows(const Product8& p, hipStream_t stream) {
-  hipLaunchKernelGGL((product8_rows_kernel<OUT, MT, NT>),
+  hipLaunchKernelGGL((product8_rows_kernel<OUT, MT, NT, AHEAD>),
                      dim3((p.N + NT * 16 - 1) / (NT * 16), (p.M + MT * 16 - 1) / (MT * 16)),
                      dim3(kWaves * 64), 0, stream, p);
   return hipGetLastError();
 }
 
+// By how many workgroups a shape gives, one or two a compute unit being what hides latency.
+// Measured (us, replayed graph, weights from memory; rows of 16 x 16 and 16 x 32, tiles of 32,
+// of 64, of 64 x 128, of 128):
+//      16 x 2048 x 2048    4.8   5.7   6.4   8.9  13.6  18.1
+//      64 x 2048 x 2048    7.0   5.9   6.7   9.2  14.1  18.9
+//     128 x 2048 x 2048   11.5   9.6   6.9   9.2  14.1  19.1
+//      64 x 8192 x 4096   38.0  30.8  15.7  14.7  24.0  36.3
+//     512 x 2048 x 2048   37.8  31.4  17.4   9.9  14.0  19.5
+//    1024 x 2048 x 2048   72.6  60.1  29.9  16.2  14.7  19.9
+//     512 x 8192 x 4096    281   226  93.6  47.8  33.7  40.2
+//    1024 x 8192 x 4096    558   448   183  90.9  61.4  52.6   (tiles of 256: 48.7)
+// Up to 16 rows every workgroup reads a alone, and what counts is w's stream: 16 x 8192 x 4096
+// 12.3 and 10.1 with 16 and 32 columns.
 template <Dt OUT>
 hipError_t launch(const Product8& p, hipStream_t stream) {
-  const int64_t big = static_cast<int64_t>((p.M + 255) / 256) * ((p.N + 255) / 256);
-  if (p.M <= 16) return p.N >= 8192 ? launch_rows<OUT, 1, 2>(p, stream) : launch_rows<OUT, 1, 1>(p, stream);
-  if (p.M <= 32) return p.N >= 8192 ? launch_rows<OUT, 2, 2>(p, stream) : launch_rows<OUT, 2, 1>(p, stream);
-  if (p.M <= 64) return p.N >= 8192 ? launch_rows<OUT, 4, 2>(p, stream) : launch_rows<OUT, 4, 1>(p, stream);
+  const auto tiles = [&](int bm, int bn) {
+    return static_cast<int64_t>((p.M + bm - 1) / bm) * ((p.N + bn - 1) / bn);
+  };
+  if (p.M <= 16 ? p.N <= 4096 : tiles(16, 16) <= 256) return launch_rows<OUT, 1, 1, 4>(p, stream);
+  if (p.M <= 16 || tiles(16, 32) <= 256) return launch_rows<OUT, 1, 2, 4>(p, stream);
+  if (tiles(32, 32) <= 256) return launch_tiles<OUT, 32, 32, 2, 1, 4, 3>(p, stream);
+  if (tiles(64, 64) <= 256) return launch_tiles<OUT, 64, 64, 2, 2, 2, 3>(p, stream);
+  if (tiles(64, 128) <= 512) return launch_tiles<OUT, 64, 128, 2, 2, 1, 3>(p, stream);
   // (fp32 results: the larger tile would spill registers)
   if constexpr (OUT == Dt::BF16)
-    if (big >= 192) return launch_tiles<OUT, 256, 256, 2, 4>(p, stream);
-  return launch_tiles<OUT, 128, 128, 2, 2>(p, stream);
+    if (tiles(256, 256) >= 192) return launch_tiles<OUT, 256, 256, 4, 2, 1, 2>(p, stream);
+  return launch_tiles<OUT, 128, 128, 2, 2, 1, 2>(p, stream);
 }
 
 }  // namespace

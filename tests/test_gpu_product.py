@@ -39,6 +39,24 @@ def test_depths(M, K):
     ref.check(f"{M} {K}", run(d), d)
 
 
+# a size for each shape of workgroup: rows of 16 x 16 and 16 x 32, tiles of 32, 64, 64 x 128,
+# 128 and (bf16 results) 256
+SHAPES = [(40, 100), (100, 1000), (128, 2000), (300, 1000), (1000, 2000), (2000, 4000), (4100, 4100)]
+
+
+@pytest.mark.parametrize("K", [16, 112, 128, 144, 256, 272, 400, 512, 528, 1024, 1152, 2064])
+@pytest.mark.parametrize("M, N", SHAPES)
+def test_depths_of_every_shape(M, N, K):
+    """One block, blocks that do not go round the groups of waves, last blocks that are not
+    whole, one group of eight scales and more."""
+    say(f"product M {M} N {N} K {K}")
+    d = ref.make(M, N, K, seed=K + M)
+    x = cuda(d)
+    want = ref.product(x, "cuda")
+    for dtype in (torch.float32, torch.bfloat16):
+        ref.check(f"{M} {N} {K}", run(d, dtype), d, want)
+
+
 @pytest.mark.parametrize("M, N, K", [(4096, 2048, 2048), (2048, 4100, 1024), (3000, 1024, 8192),
                                      (1024, 128, 640), (8, 16384, 512), (40, 200, 16384)])
 def test_large(M, N, K):
@@ -50,25 +68,28 @@ def test_large(M, N, K):
     ref.check("bf16", run(d, torch.bfloat16), d, want)
 
 
-@pytest.mark.parametrize("M", [5, 70, 300, 700])
-def test_rows_and_columns_by_themselves(M):
+@pytest.mark.parametrize("M, N", [(5, 270), (70, 270), (700, 270)] + SHAPES)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_and_columns_by_themselves(M, N, dtype):
     """NaN and infinite scales, NaN values and zero scales touch their own row or column only."""
-    d = ref.make(M, 270, 400, seed=2)
-    clean = run(d)
+    if N < 270:
+        N = 270
+    d = ref.make(M, N, 400, seed=2)
+    clean = run(d, dtype)
     d["sa"][1, 2], d["sa"][M - 1, 0] = float("nan"), float("inf")
     d["a"].view(torch.uint8)[3, 17] = 0x7F
     d["w"].view(torch.uint8)[200, 399] = 0xFF
-    got = run(d)
+    got = run(d, dtype)
     bad = torch.zeros_like(got, dtype=torch.bool)
     bad[1] = bad[3] = bad[M - 1] = True
     bad[:, 200] = True
     assert torch.equal(got[~bad], clean[~bad]) and not torch.isfinite(got[bad]).any()
-    d = ref.make(M, 270, 400, seed=3)
+    d = ref.make(M, N, 400, seed=3)
     d["sa"][2] = 0
     d["sw"][1] = 0
-    got = run(d)
+    got = run(d, dtype)
     assert not got[2].any() and not got[:, 128:256].any()
-    ref.check("zero scales", got, d)
+    ref.check("zero scales", got, d, ref.product(cuda(d), "cuda"))
 
 
 def test_whole_range_of_scales():
@@ -79,7 +100,8 @@ def test_whole_range_of_scales():
     ref.check("far apart", run(d), d)
 
 
-@pytest.mark.parametrize("M, N, K", [(64, 1000, 2064), (700, 500, 1040), (5, 128, 4096)])
+@pytest.mark.parametrize("M, N, K", [(64, 1000, 2064), (700, 500, 1040), (5, 128, 4096)] +
+                         [(*s, 1040) for s in SHAPES])
 def test_repeated_streams_and_graph(M, N, K):
     import gated_delta_rule_100_amd as gdr
     d = ref.make(M, N, K, seed=5)
