@@ -103,7 +103,9 @@ __device__ __forceinline__ void store4(void* out, size_t at, int some, bool vec,
 // rows of 16 lanes; the lanes of one row m go the same way, so all of them are to be there.
 __device__ __forceinline__ uintx4 pair_of_tiles(floatx4 a, floatx4 b) {
   const auto two = [](float lo, float hi) {
-    return f32_to_bf16_bits(lo) | static_cast<uint32_t>(f32_to_bf16_bits(hi)) << 16;
+    typedef float floatx2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((floatx2{lo, hi}), bf16x2));
   };
   const uint32_t x[2] = {two(a[0], a[1]), two(a[2], a[3])}, y[2] = {two(b[0], b[1]), two(b[2], b[3])};
   uint32_t lo[2], hi[2];
@@ -124,8 +126,10 @@ __device__ __forceinline__ uintx4 pair_of_tiles(floatx4 a, floatx4 b) {
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) void*)(p)));
 }
+template <int AT>
 __device__ __forceinline__ void copy16(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "m0");
+  asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base),
+               "i"(AT) : "m0", "scc");
 }
 __device__ __forceinline__ void copy4(const void* base, uint32_t off, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base) : "m0");
@@ -189,50 +193,92 @@ __global__ __launch_bounds__(WM * WN * KG * 64, 2) void product8_tile_kernel(Pro
     asm volatile("" : "+v"(l));
     return l;
   };
-  // A place in the sequence of blocks, the buffer of its rows and that of its scales; behind
-  // the last tile it stays there.
-  struct Cursor {
-    int tile, m0, n0, turn, rows, scales;
+  // A place in the sequence of blocks: tile and turn, and in LDS the offset of its buffer of
+  // rows and of its scales.  Past the last tile the numbers stay those of the last.  What a
+  // block does with scalars is kept to few instructions: two waves of a SIMD have no others
+  // beside them, and each instruction takes as long from a wave as a multiply-add.
+  constexpr uint32_t kRows = (BN + BM) * kBlock, kScale = BM * kScales * 4;
+  struct Place {
+    int tile, m0, n0, turn;
+    uint32_t rows, scales;
   };
-  const auto block = [&](const Cursor& c) { return c.turn * KG + kg; };
-  const auto enter = [&](Cursor& c) {
+  const auto block = [&](const Place& c) { return c.turn * KG + kg; };
+  const auto enter = [&](Place& c) {
     if (c.tile >= tiles) return;
     int im, in;
     tile_of(c.tile, tm, tn, &im, &in);
     c.m0 = im * BM;
     c.n0 = in * BN;
   };
-  const auto advance = [&](Cursor& c) {
-    c.rows = c.rows + 1 == NB ? 0 : c.rows + 1;
+  const bool ragged = p.K % (kBlock * KG) != 0;
+  // Calls `turned` in a tile's next turn, `entered` in the first of another tile.
+  const auto advance = [&](Place& c, auto turned, auto entered) {
+    c.rows = c.rows + kRows == NB * kRows ? 0 : c.rows + kRows;
+    c.scales += 4;
     if (++c.turn == turns) {
       c.turn = 0;
       c.tile += gridDim.x;
       enter(c);
+      entered();
+    } else {
+      turned();
     }
-    if (c.turn % kScales == 0) c.scales = c.scales + 1 == NB ? 0 : c.scales + 1;
+    if (c.turn % kScales == 0) {  // a row's scales in the next buffer
+      c.scales = (c.scales - 4) / kScale * kScale + kScale;
+      if (c.scales == NB * kScale) c.scales = 0;
+    }
   };
   // A lane copies the same piece of each row; rows past the end are the last.  Where a last
   // block has no such piece, it takes the row's first bytes of the block, and writes zeros
-  // over them before they are read.
+  // over them before they are read.  `to` is what is copied, from these addresses.
   const uint32_t piece = ((lane & 7) ^ ((wave * 4 + (lane >> 4)) & 7)) * 16;
   const auto missing = [&](int b) { return b * kBlock + static_cast<int>(piece) >= p.K; };
-  const auto copy_rows = [&](const Cursor& c, auto copy) {
-    constexpr int i = decltype(copy)::value;
-    constexpr bool w = i < BN / 8 / WAVES;
-    const int g = i * WAVES + wave, r = g * 8 + (anew() >> 3);
-    const int row = w ? min(r, p.N - 1 - c.n0) : min(r - BN, p.M - 1 - c.m0);
-    const uint8_t* src = (w ? p.w + static_cast<size_t>(c.n0) * p.K : p.a + static_cast<size_t>(c.m0) * p.K) +
-                         static_cast<size_t>(min(block(c), kb - 1)) * kBlock;
-    copy16(src, static_cast<uint32_t>(row) * p.K + (missing(block(c)) ? 0u : piece), lds_address(rows[c.rows][g * 8]));
+  Place to{static_cast<int>(blockIdx.x), 0, 0, 0, 0, 0};
+  const uint8_t *from_w, *from_a;
+  uint32_t from[COPIES];
+  constexpr int WCOPIES = BN / 8 / WAVES;
+  // A tile's last block may be short, or not there at all.  (The lane's difference is formed
+  // here: as a branch of the lane's own it would make the numbers of a Place the lane's.)
+  const uint32_t lost = missing((turns - 1) * KG + kg) ? piece : 0;
+  const auto last_turn = [&] {
+    if (!ragged || to.turn != turns - 1) return;
+#pragma unroll
+    for (int i = 0; i < COPIES; ++i) from[i] -= lost;
   };
-  const auto copy_scales = [&](const Cursor& c) {
-    if (c.turn % kScales != 0) return;
+  const auto aim = [&] {
+    const int first = min(kg, kb - 1) * kBlock;
+    from_w = p.w + static_cast<size_t>(to.n0) * p.K + first;
+    from_a = p.a + static_cast<size_t>(to.m0) * p.K + first;
+#pragma unroll
+    for (int i = 0; i < COPIES; ++i) {
+      const int r = (i * WAVES + wave) * 8 + (anew() >> 3);
+      const int row = i < WCOPIES ? min(r, p.N - 1 - to.n0) : min(r - BN, p.M - 1 - to.m0);
+      from[i] = static_cast<uint32_t>(row) * p.K + piece;
+    }
+    last_turn();
+  };
+  const auto advance_to = [&] {
+    advance(to, [&] {
+      if (block(to) < kb) {
+        from_w += KG * kBlock;
+        from_a += KG * kBlock;
+      }
+      last_turn();
+    }, aim);
+  };
+  const uint32_t rows_lds = lds_address(rows[0][wave * 8]);
+  const auto copy_rows = [&](auto copy) {
+    constexpr int i = decltype(copy)::value;
+    copy16<i * WAVES * 8 * kBlock>(i < WCOPIES ? from_w : from_a, from[i], rows_lds + to.rows);
+  };
+  const auto copy_scales = [&] {
+    if (to.turn % kScales != 0) return;
 #pragma unroll
     for (int i = 0; i < SCALES; ++i) {
       const int r = (i * WAVES + wave) * (64 / kScales), l = anew();
-      const int m = min(r + l / kScales, p.M - 1 - c.m0), b = min(block(c) + l % kScales * KG, kb - 1);
-      copy4(p.a_scale + static_cast<size_t>(c.m0) * kb, (static_cast<uint32_t>(m) * kb + b) * 4,
-            lds_address(scales[c.scales][r]));
+      const int m = min(r + l / kScales, p.M - 1 - to.m0), b = min(block(to) + l % kScales * KG, kb - 1);
+      copy4(p.a_scale + static_cast<size_t>(to.m0) * kb, (static_cast<uint32_t>(m) * kb + b) * 4,
+            lds_address(scales[0][r]) + to.scales);
     }
   };
   // Waits for this wave's LDS accesses and for all its memory accesses but the copies of the
@@ -253,51 +299,58 @@ __global__ __launch_bounds__(WM * WN * KG * 64, 2) void product8_tile_kernel(Pro
     return join(*reinterpret_cast<const intx4*>(at + t * 16 * kBlock + near),
                 *reinterpret_cast<const intx4*>(at + t * 16 * kBlock + far));
   };
-  const auto rows_of_w = [&](int buffer) { return rows[buffer][wn * (BN / WN)]; };
-  const auto rows_of_a = [&](int buffer) { return rows[buffer][BN + wm * (BM / WM)]; };
-  const auto zero_missing = [&](int buffer) {
+  const uint8_t* const rows_of_w = rows[0][wn * (BN / WN)];
+  const uint8_t* const rows_of_a = rows[0][BN + wm * (BM / WM)];
+  const auto zero_missing = [&](uint32_t buffer) {
     const int l = anew();
 #pragma unroll
     for (int i = 0; i < COPIES; ++i)
-      *reinterpret_cast<intx4*>(&rows[buffer][(i * WAVES + wave) * 8][0] + l * 16) = intx4{0, 0, 0, 0};
+      *reinterpret_cast<intx4*>(&rows[0][(i * WAVES + wave) * 8][0] + buffer + l * 16) = intx4{0, 0, 0, 0};
   };
   // A block's scales of this lane's rows of a, and the wave's scale of w.
-  const auto scale_of_a = [&](const Cursor& c, int j) {
-    return scales[c.scales][wm * (BM / WM) + j * 16 + c16][c.turn % kScales];
+  const uint8_t* const scales_of_a = reinterpret_cast<const uint8_t*>(scales[0][wm * (BM / WM) + c16]);
+  const auto scale_of_a = [&](const Place& c, int j) {
+    return *reinterpret_cast<const float*>(scales_of_a + c.scales + j * 16 * kScales * 4);
   };
-  const auto scale_of_w = [&](const Cursor& c) {  // (constant address space: a scalar load)
-    return ((const __attribute__((address_space(4))) float*)(p.w_scale))
-        [static_cast<size_t>(min(c.n0 + wn * (BN / WN), p.N - 1) / kBlock) * kb + min(block(c), kb - 1)];
+  Place now = to, next = to;
+  const float* scale_of_w;  // of `next`'s tile
+  const auto aim_scale = [&] {
+    scale_of_w = p.w_scale + static_cast<size_t>(min(next.n0 + wn * (BN / WN), p.N - 1) / kBlock) * kb;
   };
+  const auto next_scale_of_w = [&] {  // (constant address space: a scalar load)
+    return ((const __attribute__((address_space(4))) float*)(scale_of_w))[min(block(next), kb - 1)];
+  };
+  const auto advance_next = [&] { advance(next, [] {}, aim_scale); };
 
   // `to` is what is copied, `next` what is read, `now` what is multiplied
   constexpr int HALF = COPIES / 2;
-  Cursor to{static_cast<int>(blockIdx.x), 0, 0, 0, 0, 0};
   enter(to);
-  Cursor now = to, next = to;
-  advance(next);
+  aim();
+  now = next = to;
+  aim_scale();
+  float sw = next_scale_of_w();
+  advance_next();
 #pragma unroll
   for (int d = 0; d < NB - 1; ++d) {
-    copy_scales(to);
-    steps<COPIES>([&](auto i) { copy_rows(to, i); });
-    advance(to);
+    copy_scales();
+    steps<COPIES>(copy_rows);
+    advance_to();
   }
   arrive(false);
-  const bool ragged = p.K % (kBlock * KG) != 0;
   if (ragged && turns == 1) {
     if (missing(kg)) zero_missing(0);
     arrive(false);
   }
-  copy_scales(to);
-  steps<HALF>([&](auto i) { copy_rows(to, i); });
+  copy_scales();
+  steps<HALF>(copy_rows);
   intx8 ar[MT], wr[2];
-  float sa[MT], sw = scale_of_w(now);
+  float sa[MT];
 #pragma unroll
   for (int j = 0; j < MT; ++j) {
-    ar[j] = read(rows_of_a(0), j);
+    ar[j] = read(rows_of_a, j);
     sa[j] = scale_of_a(now, j);
   }
-  wr[0] = read(rows_of_w(0), 0);
+  wr[0] = read(rows_of_w, 0);
   bool copied = false, stores = false;  // all of `to` is on its way; stores came after it
   while (now.tile < tiles) {
     floatx4 acc[MT][NT];
@@ -322,12 +375,12 @@ __global__ __launch_bounds__(WM * WN * KG * 64, 2) void product8_tile_kernel(Pro
               if (missing(block(next))) zero_missing(next.rows);
               arrive(stores);
             }
-            next_sw = scale_of_w(next);
-            advance(to);
-            copy_scales(to);
+            next_sw = next_scale_of_w();
+            advance_to();
+            copy_scales();
           }
           wf.set(wr[i & 1]);
-          wr[(i + 1) & 1] = i < NT - 1 ? read(rows_of_w(now.rows), i + 1) : read(rows_of_w(next.rows), 0);
+          wr[(i + 1) & 1] = i < NT - 1 ? read(rows_of_w + now.rows, i + 1) : read(rows_of_w + next.rows, 0);
         }
         if constexpr (i == 0) {
           af[j].set(ar[j]);
@@ -335,15 +388,15 @@ __global__ __launch_bounds__(WM * WN * KG * 64, 2) void product8_tile_kernel(Pro
         }
         part[t & 3] = block_sum(wf, af[j]);
         if constexpr (i == NT - 1) {
-          ar[j] = read(rows_of_a(next.rows), j);
+          ar[j] = read(rows_of_a + next.rows, j);
           sa[j] = scale_of_a(next, j);
         }
         // half of the copies in this pass, half in the next block's first
         steps<(j + 1) * HALF / MT - j * HALF / MT>([&](auto c) {
           constexpr int at = j * HALF / MT + decltype(c)::value;
-          if constexpr (i == NT - 1) copy_rows(to, std::integral_constant<int, at>());
+          if constexpr (i == NT - 1) copy_rows(std::integral_constant<int, at>());
           if constexpr (i == 0)
-            if (!copied) copy_rows(to, std::integral_constant<int, HALF + at>());
+            if (!copied) copy_rows(std::integral_constant<int, HALF + at>());
         });
       }
       // a block sum meets the scales three products later
@@ -362,10 +415,10 @@ __global__ __launch_bounds__(WM * WN * KG * 64, 2) void product8_tile_kernel(Pro
     m_at = now.m0;
     n_at = now.n0;
     now = next;
-    advance(next);
+    advance_next();
     copied = stores = false;
     } while (--left > 0);
-    steps<COPIES - HALF>([&](auto c) { copy_rows(to, std::integral_constant<int, HALF + decltype(c)::value>()); });
+    steps<COPIES - HALF>([&](auto c) { copy_rows(std::integral_constant<int, HALF + decltype(c)::value>()); });
     copied = true;
     if constexpr (KG > 1) {
       if (kg > 0) steps<STEPS>([&](auto t) { sums[kg - 1][wave][decltype(t)::value][lane] = acc[decltype(t)::value / NT][decltype(t)::value % NT]; });
@@ -391,7 +444,7 @@ __global__ __launch_bounds__(WM * WN * KG * 64, 2) void product8_tile_kernel(Pro
         for (int i = 0; i < NT; i += 2) {
           const int n = n0 + i * 16 + (l >> 4) * 8;
           const uintx4 x = pair_of_tiles(acc[j][i], acc[j][i + 1]);
-          if (n < p.N) *reinterpret_cast<uintx4*>(static_cast<uint16_t*>(p.out) + at + n) = x;
+          if (stores || n < p.N) *reinterpret_cast<uintx4*>(static_cast<uint16_t*>(p.out) + at + n) = x;
         }
       } else {
 #pragma unroll
