@@ -119,6 +119,20 @@ __device__ __forceinline__ uintx4 pair_of_tiles(floatx4 a, floatx4 b) {
   return uintx4{lo[0], lo[1], hi[0], hi[1]};
 }
 
+// Four tiles side by side as bf16, a row's 128 bytes in eight lanes, rows 0 to 7 in `first` and
+// 8 to 15 in `second`: lane c of 16 has row c % 8, and the second 64 bytes from c = 8 on.
+// Stores of whole lines: 16384 x 8192 x 2048 takes 264 us with them, 277 with halves of lines
+// that follow each other and 300 where the other columns' stores are between the halves.
+__device__ __forceinline__ void lines_of_tiles(bool low, const floatx4* x, uintx4* first, uintx4* second) {
+  const uintx4 left = pair_of_tiles(x[0], x[1]), right = pair_of_tiles(x[2], x[3]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t other = __builtin_amdgcn_update_dpp(0, low ? right[i] : left[i], 0x128, 0xf, 0xf, false);  // from lane c ^ 8
+    (*first)[i] = low ? left[i] : other;
+    (*second)[i] = low ? other : right[i];
+  }
+}
+
 // 16 or 4 bytes a lane from memory, `off` behind a scalar base, to consecutive LDS.  The
 // compiler would wait for the builtin's copy before every later read of LDS, of the other
 // buffer too; written out, the copy has no register that it returns, and arrive() below is
@@ -161,11 +175,12 @@ __device__ __forceinline__ void tile_of(int id, int tm, int tn, int* im, int* in
 // lanes read at once then fall on all banks.  The scales of a come 8 blocks at a time, since
 // a row's are 32 bytes of one line then (a third of all L2 requests were for them, one by one).
 //
-// 256 x 256, bf16 results, 16384 x 8192 x 2048: 279 us, 1970 TFLOP/s (348 with the barrier
-// between blocks and copies waited for there); 8192 x 8192 x 8192: 467 us, 2350 TFLOP/s.
-// What bounds it: the matrix cores are busy 60% of the time at the 1.9 GHz that the card
-// holds under this load (4 multiply-adds behind each product share the issue slots of two
-// waves), and at K = 2048 the results' 268 MB take 53 us more, as if nothing ran beside them.
+// 256 x 256, bf16 results, 16384 x 8192 x 2048: 268 us, 2050 TFLOP/s; 8192 x 8192 x 8192: 450
+// us, 2440 TFLOP/s.  What bounds it: a SIMD's two waves hardly issue more than their matrix
+// instructions' time holds (4 multiply-adds behind each, the copies: the first 177 us become
+// 214 with the copies, of 4 bytes as of 16 each), and at K = 2048 the results' 268 MB take 54
+// us more, as if nothing ran beside them.  (348 us with the barrier between blocks, 280 with
+// addresses formed for each copy.)
 constexpr int kScales = 8;
 template <Dt OUT, int BM, int BN, int WM, int WN, int KG, int NB>
 __global__ __launch_bounds__(WM * WN * KG * 64, 2) void product8_tile_kernel(Product8 p, int tm, int tn) {
@@ -358,7 +373,7 @@ __global__ __launch_bounds__(WM * WN * KG * 64, 2) void product8_tile_kernel(Pro
     for (int j = 0; j < MT; ++j)
 #pragma unroll
       for (int i = 0; i < NT; ++i) acc[j][i] = floatx4{0.f, 0.f, 0.f, 0.f};
-    int m_at = 0, n_at = 0;
+    const int m_at = now.m0, n_at = now.n0;
     int left = turns;
     do {
     float next_sw = 0.f;
@@ -369,13 +384,15 @@ __global__ __launch_bounds__(WM * WN * KG * 64, 2) void product8_tile_kernel(Pro
       constexpr int t = decltype(step)::value, i = t / MT, j = t % MT;
       if constexpr (t < STEPS) {
         if constexpr (j == 0) {
+          // (in time for the wait behind it: while it is on its way, waits for LDS are waits
+          // for everything)
+          if constexpr (i == (NT > 2 ? 1 : 0)) next_sw = next_scale_of_w();
           if constexpr (i == NT - 1) {  // the next block has landed
             arrive(stores);
             if (ragged && next.turn == turns - 1) {
               if (missing(block(next))) zero_missing(next.rows);
-              arrive(stores);
+              lds_barrier();
             }
-            next_sw = next_scale_of_w();
             advance_to();
             copy_scales();
           }
@@ -412,8 +429,6 @@ __global__ __launch_bounds__(WM * WN * KG * 64, 2) void product8_tile_kernel(Pro
       __builtin_amdgcn_sched_barrier(0);
     });
     sw = next_sw;
-    m_at = now.m0;
-    n_at = now.n0;
     now = next;
     advance_next();
     copied = stores = false;
@@ -432,6 +447,26 @@ __global__ __launch_bounds__(WM * WN * KG * 64, 2) void product8_tile_kernel(Pro
     stores = m_at + BM <= p.M && n_at + BN <= p.N && p.N % 8 == 0;
     asm volatile("" ::: "memory");
     const bool vec = p.N % 4 == 0;
+    if (OUT == Dt::BF16 && NT % 4 == 0 && stores) {
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+#pragma unroll
+        for (int i = 0; i < NT; i += 4) {
+          const int l = anew();
+          const bool low = (l & 8) == 0;
+          uintx4 first, second;
+          lines_of_tiles(low, &acc[j][i], &first, &second);
+          const size_t at = static_cast<size_t>(m_at + wm * (BM / WM) + j * 16) * p.N + n_at + wn * (BN / WN) + i * 16;
+          uint8_t* const out = reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(p.out) + at);
+          const uint32_t off = (static_cast<uint32_t>(l & 7) * p.N + (l >> 4) * 8 + (low ? 0 : 32)) * 2;
+          *reinterpret_cast<uintx4*>(out + off) = first;
+          *reinterpret_cast<uintx4*>(out + static_cast<size_t>(p.N) * 16 + off) = second;
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      asm volatile("" ::: "memory");
+      continue;
+    }
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
       const int l = anew(), m = m_at + wm * (BM / WM) + j * 16 + (l & 15);
@@ -439,12 +474,11 @@ __global__ __launch_bounds__(WM * WN * KG * 64, 2) void product8_tile_kernel(Pro
       if (m >= p.M) continue;
       const size_t at = static_cast<size_t>(m) * p.N;
       if (OUT == Dt::BF16 && p.N % 8 == 0) {
-        // lanes change parts, so that four of them have 64 bytes of a row
 #pragma unroll
         for (int i = 0; i < NT; i += 2) {
           const int n = n0 + i * 16 + (l >> 4) * 8;
           const uintx4 x = pair_of_tiles(acc[j][i], acc[j][i + 1]);
-          if (stores || n < p.N) *reinterpret_cast<uintx4*>(static_cast<uint16_t*>(p.out) + at + n) = x;
+          if (n < p.N) *reinterpret_cast<uintx4*>(static_cast<uint16_t*>(p.out) + at + n) = x;
         }
       } else {
 #pragma unroll
@@ -596,15 +630,16 @@ hipError_t launch_rows(const Product8& p, hipStream_t stream) {
 
 // By how many workgroups a shape gives, one or two a compute unit being what hides latency.
 // Measured (us, replayed graph, weights from memory; rows of 16 x 16 and 16 x 32, tiles of 32,
-// of 64, of 64 x 128, of 128):
-//      16 x 2048 x 2048    4.8   5.7   6.4   8.9  13.6  18.1
-//      64 x 2048 x 2048    7.0   5.9   6.7   9.2  14.1  18.9
-//     128 x 2048 x 2048   11.5   9.6   6.9   9.2  14.1  19.1
-//      64 x 8192 x 4096   38.0  30.8  15.7  14.7  24.0  36.3
-//     512 x 2048 x 2048   37.8  31.4  17.4   9.9  14.0  19.5
-//    1024 x 2048 x 2048   72.6  60.1  29.9  16.2  14.7  19.9
-//     512 x 8192 x 4096    281   226  93.6  47.8  33.7  40.2
-//    1024 x 8192 x 4096    558   448   183  90.9  61.4  52.6   (tiles of 256: 48.7)
+// of 64, of 64 x 128, of 128, of 256):
+//      16 x 2048 x 2048    4.9   5.9   5.9   8.0  11.0  15.7  24.9
+//      64 x 2048 x 2048    7.2   5.9   6.0   8.2  11.4  16.3  25.7
+//     128 x 2048 x 2048   11.8   9.6   6.2   8.1  11.3  16.8  26.6
+//      64 x 8192 x 4096   38.1  31.0  14.2  14.0  19.8  33.9  48.3
+//     512 x 2048 x 2048   38.3  31.4  15.2   9.0  11.7  16.8  28.3
+//    1024 x 2048 x 2048   72.9  60.5  26.4  14.4  12.2  17.2  28.1
+//     512 x 8192 x 4096    282   227  82.5  44.7  30.4  36.5  51.7
+//    1024 x 8192 x 4096    560   451   158  82.5  54.8  43.0  56.1
+//    4096 x 4096 x 4096   1112   893   296   163   105  83.1  65.3
 // Up to 16 rows every workgroup reads a alone, and what counts is w's stream: 16 x 8192 x 4096
 // 12.3 and 10.1 with 16 and 32 columns.
 template <Dt OUT>
