@@ -10,8 +10,8 @@
 //     those of the tiles before it and so has the state that its tile starts from,
 //     while its rows wait in registers; then every thread walks its tokens and stores.
 // The packed batch is one time axis: the first token of a sequence has a map that
-// forgets what was before (A = 0, its own initial state in B), so that ragged batches
-// make no difference.  The gradient is the same scan from the last token to the first,
+// forgets what was before (kForget in A's place, its own initial state in B), so that ragged
+// batches make no difference.  The gradient is the same scan from the last token to the first,
 // of c_t = a_t (dh_t + c_{t+1}), whose r_t = dh_t + c_{t+1} gives dx and dg.
 //
 // Order.  Every join happens in one fixed order, so results do not depend on which
@@ -148,9 +148,16 @@ __device__ __forceinline__ void load_state(const float* base, size_t at, float (
   }
 }
 
-// State behind a map (A, B) from state s.  A decay of zero forgets s, whatever it is:
-// states do not reach another sequence.
-__device__ __forceinline__ float through(float A, float B, float s) { return A == 0.f ? B : fmaf(A, s, B); }
+// A map that starts a sequence has -0 for its A, which no product of decays is: it forgets the
+// state before, whatever that is (infinities and NaN do not reach another sequence), and a
+// product of decays that is 0 does not (0 times them is NaN: they do not get lost in their own).
+constexpr float kForget = -0.f;
+__device__ __forceinline__ bool forgets(float A) { return __float_as_uint(A) == 0x80000000u; }
+// State behind a map (A, B) from state s, and the A of two maps, A's first.
+__device__ __forceinline__ float through(float A, float B, float s) { return forgets(A) ? B : fmaf(A, s, B); }
+__device__ __forceinline__ float joined(float A, float then) {
+  return forgets(A) || forgets(then) ? kForget : A * then;
+}
 
 // Words that workgroups exchange: all ones is "not yet" (a NaN of these bits is
 // replaced by another).
@@ -206,7 +213,7 @@ __device__ __forceinline__ float span_start(const Links& k, int span, size_t ch)
         open = false;
       } else if (!map[i].known()) {
         open = false;
-      } else if (map[i].A() == 0.f) {
+      } else if (forgets(map[i].A())) {
         s = map[i].B();
         from = i;
         open = false;
@@ -254,13 +261,13 @@ __device__ __forceinline__ float tile_start(const Links& k, int i, size_t ch, fl
   for (int j = 0; j < kSpan - 1; ++j)
     if (j < at) {
       pb = through(map[j].A(), map[j].B(), pb);
-      pa *= map[j].A();
+      pa = joined(pa, map[j].A());
     }
   const bool last = at == kSpan - 1;
-  const float sa = pa * A, sb = through(A, B, pb);
+  const float sa = joined(pa, A), sb = through(A, B, pb);
   if (last) tell(k.span_map + span * k.width + ch, sa, sb);
   float s = 0.f;
-  if (span > 0 && pa != 0.f) s = before != kNone ? __uint_as_float(before) : span_start(k, span, ch);
+  if (span > 0 && !forgets(pa)) s = before != kNone ? __uint_as_float(before) : span_start(k, span, ch);
   if (last) tell(k.span_end + span * k.width + ch, through(sa, sb, s));
   return through(pa, pb, s);
 }
@@ -400,7 +407,7 @@ __global__ __launch_bounds__(THREADS, BACK ? 1 : IO == Dt::BF16 && G == Dt::F32 
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       if constexpr (!LOGIT) A[v] = __builtin_amdgcn_exp2f(A[v]);
-      if (forget) A[v] = 0.f;
+      if (forget) A[v] = kForget;
     }
     store_vec<Dt::F32, V>(&map_a[group][0], lane * V, A);
     store_vec<Dt::F32, V>(&map_b[group][0], lane * V, B);
@@ -416,7 +423,7 @@ __global__ __launch_bounds__(THREADS, BACK ? 1 : IO == Dt::BF16 && G == Dt::F32 
         const int at = BACK ? GROUPS - 1 - j : j;
         const float ga = map_a[at][tid];
         tb = through(ga, map_b[at][tid], tb);
-        ta *= ga;
+        ta = joined(ta, ga);
       }
       s = tile_start(k, order, static_cast<size_t>(col) * CC + tid, ta, tb);
     }

@@ -170,6 +170,78 @@ def test_infinities_stay_in_their_sequence_and_channel(value):
         assert torch.equal(back["dstate_in"][keep], got["dstate_in"][keep])
 
 
+SEQS = [300, 5, 700, 1, 40, 2100, 64]
+
+
+def spoilt(d, n, name, value, c, t):
+    """d with one element of sequence n changed, and where sequence n's rows are."""
+    x = cuda(d)
+    at = d["cu"].tolist()
+    x[name] = x[name].clone()
+    x[name][at[n] + t if t >= 0 else at[n + 1] + t, c] = value
+    return x, at[n], at[n + 1]
+
+
+@pytest.mark.parametrize("n", [0, 2, 3, 5])
+@pytest.mark.parametrize("name, value", [("x", float("nan")), ("x", float("inf")), ("g", float("nan")),
+                                         ("g", float("inf")), ("state_in", float("nan"))])
+@pytest.mark.parametrize("D, gate", [(24, "log"), (23, "logit")])
+def test_steep_decays_keep_infinities_in_their_sequence(D, gate, name, value, n):
+    """To the end of its sequence, over tiles whose product of decays is 0, and no further, over
+    tiles whose product of decays is not a number."""
+    if gate == "logit" and name == "g" and value == float("inf"):
+        value = float("nan")  # (a logit of infinity is a decay of 1)
+    d = ref.make(SEQS, D, gate, False, "f32", "f32", kind="steep", seed=n)
+    clean, clean_out = forward(d)
+    t = min(3, SEQS[n] - 1)
+    if name == "state_in":
+        x = cuda(d)
+        x["state_in"] = x["state_in"].clone()
+        x["state_in"][n, 9] = value
+        lo, hi = d["cu"].tolist()[n:n + 2]
+        t = 0
+    else:
+        x, lo, hi = spoilt(d, n, name, value, 9, t)
+    h, out = forward(d, x)
+    bad = torch.zeros_like(h, dtype=torch.bool)
+    bad[lo + t:hi, 9] = True
+    assert torch.equal(h[~bad], clean[~bad]) and not torch.isfinite(h[bad]).any()
+    bad = torch.zeros_like(out, dtype=torch.bool)
+    bad[n, 9] = True
+    assert torch.equal(out[~bad], clean_out[~bad]) and not torch.isfinite(out[bad]).any()
+
+
+@pytest.mark.parametrize("n", [0, 2, 3, 5])
+@pytest.mark.parametrize("name", ["dh", "g"])
+@pytest.mark.parametrize("D, gate", [(24, "log"), (23, "logit")])
+def test_steep_decays_keep_infinities_in_their_sequence_gradient(D, gate, name, n):
+    d = ref.make(SEQS, D, gate, False, "f32", "f32", kind="steep", seed=n)
+    h, _ = forward(d)
+    clean = backward(d, h)
+    t = -min(3, SEQS[n])
+    x, lo, hi = spoilt(d, n, name, float("nan"), 9, t)
+    got = backward(d, h, x)
+    row = hi + t
+    # dx_t is r_t, that does not hold a_t; dg_t and dstate_in are a_t r_t
+    for out, first in (("dx", row if name == "dh" else row - 1), ("dg", row)):
+        bad = torch.zeros_like(got[out], dtype=torch.bool)
+        bad[lo:first + 1, 9] = True
+        assert torch.equal(got[out][~bad], clean[out][~bad]), out
+        assert not torch.isfinite(got[out][bad]).any(), out
+    bad = torch.zeros_like(got["dstate_in"], dtype=torch.bool)
+    bad[n, 9] = True
+    assert torch.equal(got["dstate_in"][~bad], clean["dstate_in"][~bad])
+    assert not torch.isfinite(got["dstate_in"][bad]).any()
+
+
+@pytest.mark.parametrize("D", [12, 100, 508])
+@pytest.mark.parametrize("gdtype", ["bf16", "f32"])
+def test_widths_of_four(D, gdtype):
+    """fp32 rows of 16-byte loads that bf16's would not have."""
+    check_all(ref.make(RAGGED, D, "log", True, "f32", gdtype, seed=D, pad=3))
+    check_all(ref.make(RAGGED, D, "log", True, "bf16", gdtype, seed=D, pad=3))
+
+
 def test_bad_offsets_stay_inside():
     """Offsets that decrease, are negative or pass the end: wrong results, nothing out of range."""
     import gated_delta_rule_100_amd as gdr
