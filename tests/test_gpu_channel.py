@@ -234,6 +234,32 @@ def test_steep_decays_keep_infinities_in_their_sequence_gradient(D, gate, name, 
     assert not torch.isfinite(got["dstate_in"][bad]).any()
 
 
+@pytest.mark.parametrize("gate, complement", FORMS)
+@pytest.mark.parametrize("dtype, gdtype", TYPES)
+def test_slow_decays_keep_their_precision(gate, complement, dtype, gdtype):
+    """States that remember hundreds of tokens, in the 2-norm.  Each step multiplies what it
+    keeps by a decay and adds with fp32 roundings, independent from one token to the next:
+    sqrt(tokens remembered) of them, 3 of 2^-24 at most, where errors of one sign would give
+    as many as tokens."""
+    gen = torch.Generator().manual_seed(5)
+    lens, D = [1500, 700], 96
+    d = ref.make(lens, D, gate, complement, dtype, gdtype, seed=5)
+    z = 5 + torch.randn(sum(lens), D, generator=gen, dtype=torch.float64) / 2
+    g = z if gate == "logit" else -torch.nn.functional.softplus(-z)
+    d["g"] = g.to(ref.DT[gdtype])
+    want_h, want_s = ref.forward(d)
+    h, out = forward(d)
+    keep = float((1 / (1 - ref.terms(d)[0])).mean())
+    within = 3 * keep ** 0.5 * 2.0 ** -24
+    assert float((out.cpu().double() - want_s).norm() / want_s.norm()) <= within
+    got = backward(d, h)
+    want, _ = ref.backward(d, h.cpu())
+    assert float((got["dstate_in"].cpu().double() - want["dstate_in"]).norm() /
+                 want["dstate_in"].norm()) <= within
+    if dtype == "f32":
+        assert float((h.cpu().double() - want_h).norm() / want_h.norm()) <= within
+
+
 @pytest.mark.parametrize("D", [12, 100, 508])
 @pytest.mark.parametrize("gdtype", ["bf16", "f32"])
 def test_widths_of_four(D, gdtype):
