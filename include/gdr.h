@@ -529,8 +529,8 @@ gdr_status gdr_product8(const void* a, const float* a_scale, const void* w, cons
  *     x, h, dh and dx share io_dtype, g and dg have g_dtype.  States are fp32.
  *   - x and g may be slices of wider token rows: x_stride and g_stride are the
  *     elements from one row to the next, 0 for dense, at least D and at most 2^24.
- *     Where D and both strides are multiples of 8 (of 4 with io_dtype GDR_FP32),
- *     rows are read with 16-byte loads, otherwise element by element.
+ *     Rows are fastest where D and both strides are multiples of 8 (of 4 with
+ *     io_dtype GDR_FP32).
  *   - g <= 0 is expected of GDR_CHANNEL_LOG (a decay); -110 or less, -infinity among
  *     it, is a decay of exactly zero.  1 - a is formed without cancellation.
  *   - cu_seqlens[N] may be below T_total: rows behind the last sequence are not
