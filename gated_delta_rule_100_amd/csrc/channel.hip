@@ -365,13 +365,17 @@ void channel_scan_kernel(Channel p, Links k) {
   constexpr bool REST = COMP || (BACK && LOGIT);
   __shared__ int ticket;
   __shared__ int first_of[TT], last_of[TT];  // sequence that starts, or ends, at a token
+  __shared__ int offsets[64];
   __shared__ float map_a[GROUPS][CC], map_b[GROUPS][CC];
   const int tid = threadIdx.x, lane = tid % S::LANES, group = tid / S::LANES;
   const int col = blockIdx.x % k.cols;
+  // Offsets of up to 63 sequences: asked for before the rows, which they would wait for.
+  const bool few = p.N < 64;
+  const int offset = few ? p.cu[min(tid & 63, p.N)] : 0;
   int order = 0;
   if (k.tiles > 1) {
     if (tid == 0) ticket = static_cast<int>(atomicAdd(k.ticket + col * kTicketStep, 1u));
-    __syncthreads();
+    lds_barrier();
     order = ticket;
   }
   const int tile = BACK ? k.tiles - 1 - order : order;
@@ -400,9 +404,18 @@ void channel_scan_kernel(Channel p, Links k) {
   }
   // where sequences start and end among the tile's tokens
   for (int i = tid; i < TT; i += THREADS) first_of[i] = last_of[i] = -1;
-  __syncthreads();
-  const auto cu = [&](int m) { return min(max(p.cu[m], 0), p.T); };
-  const int valid = cu(p.N), m0 = first_at(p.cu, p.N, t0);
+  const auto inside = [&](int at) { return min(max(at, 0), p.T); };
+  int valid, m0;
+  if (few) {
+    if (tid < 64) offsets[tid] = inside(offset);
+    valid = inside(__builtin_amdgcn_readlane(offset, p.N));
+    m0 = __popcll(__ballot((tid & 63) <= p.N && offset < t0));
+  } else {
+    valid = inside(p.cu[p.N]);
+    m0 = first_at(p.cu, p.N, t0);
+  }
+  lds_barrier();
+  const auto cu = [&](int m) { return few ? offsets[m] : inside(p.cu[m]); };
   const int until = tile == k.tiles - 1 ? p.T : t0 + TT - 1;  // empty sequences are this tile's up to here
   for (int m = m0 + tid; m <= p.N; m += THREADS) {
     const int at = cu(m);
@@ -423,7 +436,7 @@ void channel_scan_kernel(Channel p, Links k) {
       at_c.load_state(from, static_cast<size_t>(m) * p.D + c, s);
       at_c.template store<Dt::F32>(to, static_cast<size_t>(m) * p.D + c, s);
     }
-  __syncthreads();
+  lds_barrier();
   // the maps of this thread's tokens, joined.  `enter`: sequences whose first token of
   // the pass is here; the state of the latest is kept, for its buffer may be written
   // by the thread that holds the sequence's end (in place) before the walk below.
@@ -469,7 +482,7 @@ void channel_scan_kernel(Channel p, Links k) {
     store_vec<Dt::F32, V>(&map_a[group][0], lane * V, A);
     store_vec<Dt::F32, V>(&map_b[group][0], lane * V, B);
   }
-  __syncthreads();
+  lds_barrier();
   // one thread a channel: the tile's map, the state it starts from, and each group's
   if (tid < CC && col * CC + tid < p.D) {
     float s = 0.f;
@@ -492,7 +505,7 @@ void channel_scan_kernel(Channel p, Links k) {
       s = through(ga, gb, s);
     }
   }
-  __syncthreads();
+  lds_barrier();
   if (!mine) return;
   float s[V];
   {
