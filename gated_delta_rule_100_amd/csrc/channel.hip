@@ -25,6 +25,13 @@
 // floats in 8 bytes, state: 4 bytes), so no fence orders anything; all ones stand for
 // "not yet", which a fill kernel writes before each pass.  A wait is bounded all the
 // same (kPatience), for a workspace that two calls share against the rules.
+//
+// What bounds it: memory.  2048 channels, 4 sequences of 4096 tokens, bf16 logits and
+// complement: 55.5 us, 3.6 TB/s of the bytes that have to move (1 GiB copied: 5.1 TB/s); 8
+// ragged sequences, 32768 tokens of 4096 channels, fp32 decays: 225 us, 4.8 TB/s; one of
+// 131072 tokens, 512 channels: 102 us, 4.0 TB/s; gradient of the first: 95 us, 4.2 TB/s.
+// What is left is a fill kernel (5 us with its launch), the first's vector instructions for
+// two exponentials and two reciprocals an element, and tiles that wait for those before.
 #include <type_traits>
 
 #include "channel.h"
@@ -34,8 +41,8 @@ namespace gdr {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-// Tiles of a span, and spans looked back at together.  Measured (prompts, the document of
-// above, us): 59 and 104; spans of 16 tiles 64 and 110, of 4 tiles 59 and 114; 8 spans 64 and
+// Tiles of a span, and spans looked back at together.  Measured (prompts and the document of
+// above, when they took 59 and 104 us): spans of 16 tiles 64 and 110, of 4 tiles 59 and 114; 8 spans 64 and
 // 112, 2 spans 59 and 109, 1 span 59 and 134.
 constexpr int kSpan = 8;
 constexpr int kBack = 4;
@@ -77,7 +84,7 @@ __device__ __forceinline__ float rest_of_log(float g, float a) {
 // rounding, no difference that cancels; NaN passes.  Errors of decays close to 1 add up over
 // the 1 / (1 - a) tokens that a state remembers: with 1 / (1 + e^-z) for a, bf16 logits of
 // sequences of 3000 and 500 tokens left states off by 3e-6, and by 3.6e-7 so, for 2 us of the
-// prompts' 59.
+// prompts.
 template <bool LOGIT, bool REST>
 __device__ __forceinline__ Decay decay_of(float g) {
   if constexpr (LOGIT) {
@@ -369,8 +376,10 @@ void channel_scan_kernel(Channel p, Links k) {
   __shared__ float map_a[GROUPS][CC], map_b[GROUPS][CC];
   const int tid = threadIdx.x, lane = tid % S::LANES, group = tid / S::LANES;
   const int col = blockIdx.x % k.cols;
-  // Offsets of up to 63 sequences: asked for before the rows, which they would wait for.
-  const bool few = p.N < 64;
+  // Offsets of up to 63 sequences: asked for before the rows, which they would wait for
+  // (prompts 55.6 us, 59.3 with offsets behind the rows; gradient 94 and 96; but 4096 + 4096
+  // tokens of 2048 channels in fp32 50 and 47.7: there they come behind).
+  const bool few = (BACK || IO == Dt::BF16) && p.N < 64;
   const int offset = few ? p.cu[min(tid & 63, p.N)] : 0;
   int order = 0;
   if (k.tiles > 1) {
@@ -624,7 +633,7 @@ size_t links_bytes(size_t tiles, size_t cols, size_t width) {
   return tiles > 1 ? ticket_bytes(cols) + width * (8 * tiles + 12 * spans) : 0;
 }
 
-// 8 tokens a thread: with 4, prompts take 65 us (59), the packed batch 256 (232), the document
+// 8 tokens a thread: with 4, prompts took 65 us (59), the packed batch 256 (232), the document
 // 132 (104) and the gradient 94 (96); 16 spill.  Rows that are not on 16
 // bytes, 8192 tokens of 2047 channels in bf16: 51 us (76 element by element).
 template <bool BACK>

@@ -260,6 +260,16 @@ def test_slow_decays_keep_their_precision(gate, complement, dtype, gdtype):
         assert float((h.cpu().double() - want_h).norm() / want_h.norm()) <= within
 
 
+@pytest.mark.parametrize("N", [62, 63, 64, 65, 200])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_numbers_of_sequences(N, dtype):
+    """Short ones, empty ones and a long one, as many as a wave's lanes and about."""
+    gen = torch.Generator().manual_seed(N)
+    lens = torch.randint(0, 20, (N,), generator=gen).tolist()
+    lens[N // 2], lens[-1] = 400, 0
+    check_all(ref.make(lens, 40, "logit", True, dtype, "f32", seed=N, pad=5))
+
+
 @pytest.mark.parametrize("D", [12, 100, 508])
 @pytest.mark.parametrize("gdtype", ["bf16", "f32"])
 def test_widths_of_four(D, gdtype):
