@@ -166,3 +166,21 @@ def test_more_than_2_31_elements(which):
     d = dict(a=take(a, rows), sa=sa[rows], w=take(w, at),
              sw=sw[at[::128] // 128] if N > 1000 else sw)
     ref.check(which, out[rows][:, at], d)
+
+
+@pytest.mark.parametrize("N, K, times, dtype", [(65544, 144, 71, torch.bfloat16),
+                                                (65544, 144, 71, torch.float32),
+                                                (136, 8192, 600, torch.bfloat16)])
+def test_more_than_2_32(N, K, times, dtype):
+    """More than 2^32 results, and more than 2^32 bytes of rows: the same 1000 rows again and again."""
+    import gated_delta_rule_100_amd as gdr
+    say(f"product {times * 1000} {N} {K} {dtype}")
+    d = ref.make(1000, N, K, seed=K)
+    x = cuda(d)
+    a = x["a"].view(torch.uint8).repeat(times, 1).view(ref.E4M3)
+    out = torch.full((times * 1000, N), float("nan"), dtype=dtype, device="cuda")
+    gdr.gdr_product8(a, x["sa"].repeat(times, 1), x["w"], x["sw"], out)
+    torch.cuda.synchronize()
+    ref.check("first", out[:1000], d, ref.product(x, "cuda"))
+    for i in range(1, times):
+        assert torch.equal(out[i * 1000:(i + 1) * 1000], out[:1000]), i
