@@ -13,6 +13,7 @@
 
 #include "gdr_device.h"
 #include "product.h"
+#include "product_lanes.h"
 
 namespace gdr {
 namespace {
@@ -22,8 +23,6 @@ typedef _Float16 halfx8 __attribute__((ext_vector_type(8)));
 typedef uint32_t uintx4 __attribute__((ext_vector_type(4)));
 typedef int intx4 __attribute__((ext_vector_type(4)));
 typedef int intx8 __attribute__((ext_vector_type(8)));
-
-constexpr int kBlock = 128;
 
 // f(0), f(1), ... with their arguments as constants (the loop is too long for the compiler
 // to unroll).
@@ -510,20 +509,20 @@ __global__ __launch_bounds__(kWaves * 64) void product8_rows_kernel(Product8 p) 
 #pragma unroll
   for (int j = 0; j < MT; ++j) {
     const int m = min(m0 + j * 16 + c16, p.M - 1);
-    ar[j] = p.a + static_cast<size_t>(m) * p.K + q * 16;
+    ar[j] = p.a + static_cast<size_t>(m) * p.K;
     sa[j] = p.a_scale + static_cast<size_t>(m) * kb;
   }
 #pragma unroll
-  for (int i = 0; i < NT; ++i) wr[i] = p.w + static_cast<size_t>(min(n0 + i * 16 + c16, p.N - 1)) * p.K + q * 16;
+  for (int i = 0; i < NT; ++i) wr[i] = p.w + static_cast<size_t>(min(n0 + i * 16 + c16, p.N - 1)) * p.K;
   const float* sw = p.w_scale + static_cast<size_t>(n0 / kBlock) * kb;
-  // A block as loaded.  Lanes behind the rows' end load the row's first bytes, without a
-  // branch, and have them taken for zeros when they are used.
+  // A block as loaded.  Lanes behind the rows' end load the rows' first bytes, without a
+  // branch (lane_offset), and have them taken for zeros when they are used.
   struct Block {
     intx4 w[NT][2], a[MT][2];
     float sa[MT], sw;
   };
   const auto read = [&](int b, Block& x) {
-    const int k = b * kBlock, lo = k + q * 16 < p.K ? k : 0, hi = k + 64 + q * 16 < p.K ? k + 64 : 0;
+    const int lo = lane_offset(p.K, b, q, 0), hi = lane_offset(p.K, b, q, 1);
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       x.w[i][0] = *reinterpret_cast<const intx4*>(wr[i] + lo);
@@ -545,7 +544,7 @@ __global__ __launch_bounds__(kWaves * 64) void product8_rows_kernel(Product8 p) 
   const auto multiply = [&](int b, Block& x) {
     if ((b + 1) * kBlock > p.K) {
       const intx4 zero = {0, 0, 0, 0};
-      const bool lo = b * kBlock + q * 16 < p.K, hi = b * kBlock + 64 + q * 16 < p.K;
+      const bool lo = lane_has(p.K, b, q, 0), hi = lane_has(p.K, b, q, 1);
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         x.w[i][0] = lo ? x.w[i][0] : zero;
