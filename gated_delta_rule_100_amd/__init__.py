@@ -40,6 +40,7 @@ __all__ = [
     "gdr_block_norm_backward_workspace_bytes",
     "gdr_block_norm8",
     "gdr_product8",
+    "gdr_product8_max_rows",
     "gdr_channel_decode",
     "gdr_channel_prefill",
     "gdr_channel_prefill_workspace_bytes",
@@ -119,6 +120,8 @@ def _load():
     lib.gdr_block_norm8.restype = I
     lib.gdr_product8.argtypes = [P] * 5 + [I, I, I, I, P]
     lib.gdr_product8.restype = I
+    lib.gdr_product8_max_rows.argtypes = [I]
+    lib.gdr_product8_max_rows.restype = I
     lib.gdr_channel_decode.argtypes = [P, P, P, P, I, I, L, L, I, I, I, I, P]
     lib.gdr_channel_decode.restype = I
     lib.gdr_channel_prefill.argtypes = [P, P, P, I, P, P, P, I, I, L, L, I, I, I, I, P, S, P]
@@ -699,11 +702,16 @@ def gdr_product8(a, a_scale, w, w_scale, out, *, stream=None) -> None:
     _launch("gdr_product8", _load().gdr_product8, dev, stream, *args)
 
 
+def gdr_product8_max_rows(N) -> int:
+    return int(_load().gdr_product8_max_rows(N))
+
+
 def _norm8_after(o, dev, stream, *, project=None, **norm):
     """_norm_after with a result in 8 bits (gdr_block_norm8), and behind it the product
     that `project` asks for, a dict of gdr_product8's w, w_scale and out: rows of w are as
     long as a row of o, or as all heads of a token where o has heads of whole blocks of
-    128.  Everything is checked now."""
+    128.  Everything is checked now, as _norm_after does it: the numbers of rows by what
+    the library says that it takes."""
     who, lib = "gdr_block_norm8", _load()
     at, ptrs, rows, tail = _norm8_call(o, **norm)
     if at != dev:
@@ -727,6 +735,8 @@ def _norm8_after(o, dev, stream, *, project=None, **norm):
     if on != dev:
         raise GdrError("y8 is on another device than the first tensor")
     _launch("gdr_product8", lib.gdr_product8, dev, stream, *args[:5], 0, *args[6:])
+    if M > lib.gdr_product8_max_rows(F):
+        raise GdrError(f"gdr_product8: M={M} N={F}")
 
     def both():
         first()

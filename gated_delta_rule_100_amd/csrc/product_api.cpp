@@ -14,16 +14,24 @@ using gdr::fail;
 
 // (a tile's rows are addressed by 32 bits)
 constexpr int kMaxSize = 1 << 24, kMaxDepth = 1 << 22;
+constexpr int64_t kResults = int64_t{1} << 36;  // fewer than these
+
+int max_rows(int N) {
+  if (N <= 0 || N > kMaxSize) return 0;
+  const int64_t most = (kResults - 1) / N;
+  return most < kMaxSize ? static_cast<int>(most) : kMaxSize;
+}
 
 }  // namespace
 
 extern "C" {
 
+int gdr_product8_max_rows(int N) { return max_rows(N); }
+
 gdr_status gdr_product8(const void* a, const float* a_scale, const void* w, const float* w_scale,
                         void* out, int M, int N, int K, gdr_dtype out_dtype, gdr_stream_t stream) {
   const char* who = "gdr_product8";
-  if (M < 0 || N <= 0 || K <= 0 || M > kMaxSize || N > kMaxSize || K > kMaxDepth ||
-      static_cast<int64_t>(M) * N >= int64_t{1} << 36)
+  if (M < 0 || N <= 0 || K <= 0 || N > kMaxSize || K > kMaxDepth || M > max_rows(N))
     return fail(GDR_ERR_INVALID_ARG, "%s: M=%d N=%d K=%d", who, M, N, K);
   if (K % 16 != 0) return fail(GDR_ERR_UNSUPPORTED, "%s: K=%d is not a multiple of 16", who, K);
   if (out_dtype != GDR_BF16 && out_dtype != GDR_FP32)

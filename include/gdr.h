@@ -515,6 +515,9 @@ gdr_status gdr_block_norm8(const void* x, const void* w_after, const void* gate,
 gdr_status gdr_product8(const void* a, const float* a_scale, const void* w, const float* w_scale,
                         void* out, int M, int N, int K, gdr_dtype out_dtype, gdr_stream_t stream);
 
+/* Most rows M that gdr_product8 takes with N columns; 0 on a bad N. */
+int gdr_product8_max_rows(int N);
+
 /*
  * The gated linear recurrence with a decay for each channel -- a recurrence whose
  * state is a vector (gated recurrent units without a nonlinearity in time, the
