@@ -400,7 +400,9 @@ __global__ __launch_bounds__(WM * WN * KG * 64, 2) void product8_tile_kernel(Pro
         }
         if constexpr (i == 0) {
           af[j].set(ar[j]);
-          scale[j] = sa[j] * sw;
+          // (a group without a block has zeros for it, which the scale of another block, where
+          // that is infinite, would make NaN)
+          scale[j] = KG == 1 || block(now) < kb ? sa[j] * sw : 0.f;
         }
         part[t & 3] = block_sum(wf, af[j]);
         if constexpr (i == NT - 1) {
