@@ -24,7 +24,8 @@
 // of dispatch.  What is published is one word, written and read at once (map: two
 // floats in 8 bytes, state: 4 bytes), so no fence orders anything; all ones stand for
 // "not yet", which a fill kernel writes before each pass.  A wait is bounded all the
-// same (kPatience), for a workspace that two calls share against the rules.
+// same (kPatience) and a ticket checked, for a workspace that two calls share against the
+// rules: their results are wrong, but they end and stay inside their operands.
 //
 // What bounds it: memory.  2048 channels, 4 sequences of 4096 tokens, bf16 logits and
 // complement: 55.5 us, 3.6 TB/s of the bytes that have to move (1 GiB copied: 5.1 TB/s); 8
@@ -35,6 +36,7 @@
 #include <type_traits>
 
 #include "channel.h"
+#include "channel_order.h"
 #include "gdr_device.h"
 
 namespace gdr {
@@ -370,7 +372,7 @@ void channel_scan_kernel(Channel p, Links k) {
   using S = Shape<V, L, THREADS>;
   constexpr int CC = S::CC, TT = S::TT, GROUPS = S::GROUPS;
   constexpr bool REST = COMP || (BACK && LOGIT);
-  __shared__ int ticket;
+  __shared__ uint32_t ticket;
   __shared__ int first_of[TT], last_of[TT];  // sequence that starts, or ends, at a token
   __shared__ int offsets[64];
   __shared__ float map_a[GROUPS][CC], map_b[GROUPS][CC];
@@ -383,11 +385,12 @@ void channel_scan_kernel(Channel p, Links k) {
   const int offset = few ? p.cu[min(tid & 63, p.N)] : 0;
   int order = 0;
   if (k.tiles > 1) {
-    if (tid == 0) ticket = static_cast<int>(atomicAdd(k.ticket + col * kTicketStep, 1u));
+    if (tid == 0) ticket = atomicAdd(k.ticket + col * kTicketStep, 1u);
     lds_barrier();
-    order = ticket;
+    if (!has_tile(ticket, k.tiles)) return;
+    order = static_cast<int>(ticket);
   }
-  const int tile = BACK ? k.tiles - 1 - order : order;
+  const int tile = tile_of_ticket(order, k.tiles, BACK);
   const int t0 = tile * TT, tg = t0 + group * L;
   const int c = col * CC + lane * V;
   const bool mine = c < p.D;
