@@ -736,8 +736,11 @@ def _norm8_after(o, dev, stream, *, project=None, **norm):
         raise GdrError(f"{who}: rows of w have {K} values, those of o {D}, in heads of whole "
                        "blocks of 128")
     M, F = o.numel() // K if K else 0, w.shape[0]
-    if out.shape != (*o.shape[:-1 if K == D else -2], F):
-        raise GdrError(f"{who}: out must have shape {(*o.shape[:-1 if K == D else -2], F)}")
+    shapes = [(*o.shape[:-1], F)] if K == D else []
+    if o.dim() >= 3 and K == o.shape[-2] * D:  # (of one head, both)
+        shapes.append((*o.shape[:-2], F))
+    if out.shape not in shapes:
+        raise GdrError(f"{who}: out must have shape {' or '.join(map(str, shapes))}")
     on, args = _product8_call(norm["y8"].view(M, K), norm["y_scale"].view(M, -(-K // 128)), w,
                               project["w_scale"], out.view(M, F))
     if on != dev:
