@@ -190,6 +190,7 @@ __global__ __launch_bounds__(WM * WN * KG * 64, 2) void product8_tile_kernel(Pro
   static_assert(COPIES * WAVES * 8 == BM + BN && BN / 8 % WAVES == 0, "copies");
   static_assert(SCALES * WAVES * 64 == BM * kScales, "scales");
   static_assert(WAVES % 2 == 0, "a lane's piece");
+  static_assert(KG == 1 || WAVES * 64 >= BM, "a lane's row of scales");
   static_assert(NT % 2 == 0, "rows of w in two places");
   __shared__ uint8_t all_rows[KG][NB][BN + BM][kBlock];  // of w, then of a
   __shared__ float all_scales[KG][NB][BM][kScales];
@@ -321,6 +322,14 @@ __global__ __launch_bounds__(WM * WN * KG * 64, 2) void product8_tile_kernel(Pro
     for (int i = 0; i < COPIES; ++i)
       *reinterpret_cast<intx4*>(&rows[0][(i * WAVES + wave) * 8][0] + buffer + l * 16) = intx4{0, 0, 0, 0};
   };
+  // A group without a block in a tile's last turn has zeros for it, and the scales of the last
+  // block that is there: they become zeros too, since an infinite one would make NaN of them.
+  const auto without = [&](const Place& c) { return KG > 1 && block(c) >= kb; };
+  const auto zero_scales = [&](const Place& c, float* scale_of_w) {
+    const int r = wave * 64 + anew();
+    if (r < BM) *reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(scales[0][r]) + c.scales) = 0.f;
+    *scale_of_w = 0.f;
+  };
   // A block's scales of this lane's rows of a, and the wave's scale of w.
   const uint8_t* const scales_of_a = reinterpret_cast<const uint8_t*>(scales[0][wm * (BM / WM) + c16]);
   const auto scale_of_a = [&](const Place& c, int j) {
@@ -353,6 +362,7 @@ __global__ __launch_bounds__(WM * WN * KG * 64, 2) void product8_tile_kernel(Pro
   arrive(false);
   if (ragged && turns == 1) {
     if (missing(kg)) zero_missing(0);
+    if (without(now)) zero_scales(now, &sw);
     arrive(false);
   }
   copy_scales();
@@ -390,6 +400,7 @@ __global__ __launch_bounds__(WM * WN * KG * 64, 2) void product8_tile_kernel(Pro
             arrive(stores);
             if (ragged && next.turn == turns - 1) {
               if (missing(block(next))) zero_missing(next.rows);
+              if (without(next)) zero_scales(next, &next_sw);
               lds_barrier();
             }
             advance_to();
@@ -400,9 +411,7 @@ __global__ __launch_bounds__(WM * WN * KG * 64, 2) void product8_tile_kernel(Pro
         }
         if constexpr (i == 0) {
           af[j].set(ar[j]);
-          // (a group without a block has zeros for it, which the scale of another block, where
-          // that is infinite, would make NaN)
-          scale[j] = KG == 1 || block(now) < kb ? sa[j] * sw : 0.f;
+          scale[j] = sa[j] * sw;
         }
         part[t & 3] = block_sum(wf, af[j]);
         if constexpr (i == NT - 1) {
