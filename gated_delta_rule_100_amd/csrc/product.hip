@@ -188,6 +188,7 @@ __global__ __launch_bounds__(WM * WN * KG * 64, 2) void product8_tile_kernel(Pro
   constexpr int COPIES = (BM + BN) / 8 / WAVES;  // of 8 rows, a wave
   constexpr int SCALES = BM * kScales / 64 / WAVES;
   static_assert(COPIES * WAVES * 8 == BM + BN && BN / 8 % WAVES == 0, "copies");
+  static_assert(COPIES % 2 == 0, "copies in halves");
   static_assert(SCALES * WAVES * 64 == BM * kScales, "scales");
   static_assert(WAVES % 2 == 0, "a lane's piece");
   static_assert(KG == 1 || WAVES * 64 >= BM, "a lane's row of scales");
@@ -639,8 +640,8 @@ hipError_t launch_rows(const Product8& p, hipStream_t stream) {
 }
 
 // By how many workgroups a shape gives, one or two a compute unit being what hides latency.
-// Measured (us, replayed graph, weights from memory; rows of 16 x 16 and 16 x 32, tiles of 32,
-// of 64, of 64 x 128, of 128, of 256):
+// Measured with bf16 results (us, replayed graph, weights from memory; rows of 16 x 16 and
+// 16 x 32, tiles of 32, of 64, of 64 x 128, of 128, of 256):
 //      16 x 2048 x 2048    4.9   5.9   5.9   8.0  11.0  15.7  24.9
 //      64 x 2048 x 2048    7.2   5.9   6.0   8.2  11.4  16.3  25.7
 //     128 x 2048 x 2048   11.8   9.6   6.2   8.1  11.3  16.8  26.6
@@ -650,6 +651,16 @@ hipError_t launch_rows(const Product8& p, hipStream_t stream) {
 //     512 x 8192 x 4096    282   227  82.5  44.7  30.4  36.5  51.7
 //    1024 x 8192 x 4096    560   451   158  82.5  54.8  43.0  56.1
 //    4096 x 4096 x 4096   1112   893   296   163   105  83.1  65.3
+// and with fp32 results, for which the rule takes the fastest too but for 64 x 8192 x 4096, by 2%:
+//      16 x 2048 x 2048    4.9   5.8   6.7  10.2  15.8  21.0
+//      64 x 2048 x 2048    7.2   5.8   6.8  10.4  16.5  21.6
+//     128 x 2048 x 2048   12.0   9.7   6.9  10.4  16.4  22.5
+//      64 x 8192 x 4096   38.7  31.9  16.5  16.8  28.8  40.1
+//     512 x 2048 x 2048   38.8  32.4  18.1  11.1  16.7  23.2
+//    1024 x 2048 x 2048   73.7  62.0  32.5  18.7  17.4  23.6
+//     512 x 8192 x 4096    282   236   101  59.6  45.5  48.8
+//    1024 x 8192 x 4096    559   465   197   113  85.4  69.9
+//    4096 x 4096 x 4096   1114   923   391   218   161   136
 // Up to 16 rows every workgroup reads a alone, and what counts is w's stream: 16 x 8192 x 4096
 // 12.3 and 10.1 with 16 and 32 columns.
 template <Dt OUT>
